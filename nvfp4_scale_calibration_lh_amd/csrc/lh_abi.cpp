@@ -1,124 +1,24 @@
 // C ABI of the calibration library (declarations and contracts in include/lh.h).
 //
-// This file validates arguments before anything is launched, selects the device that owns the
-// pointers (restoring the caller's current device), keeps per-device accumulation scratch memory
-// (from a library-owned stream-ordered pool) that calls hand on in stream order, and launches the
-// kernels on the caller's stream.  Its only other state is a thread-local error message.
+// This file holds the calibration entry points.  It validates arguments before anything is launched,
+// selects the device that owns the pointers (restoring the caller's current device), keeps
+// per-device accumulation scratch memory (from a library-owned stream-ordered pool) that calls hand
+// on in stream order, and launches the kernels on the caller's stream.
 #include <hip/hip_runtime.h>
 
-#include <cstdarg>
-#include <cstdio>
 #include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <mutex>
-#include <string>
 #include <vector>
 
 #include "../../include/lh.h"
+#include "lh_host.hpp"
 #include "lh_internal.hpp"
 
+using namespace lh::host;
+
 namespace {
-
-thread_local std::string g_last_error;
-
-lh_status fail(lh_status code, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  g_last_error = buf;
-  return code;
-}
-
-lh_status ok() {
-  g_last_error.clear();
-  return LH_OK;
-}
-
-lh_status hip_fail(hipError_t e, const char* what) {
-  (void)hipGetLastError();  // clear the sticky launch error so the caller's next call is clean
-  return fail(LH_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-}
-
-bool dtype_ok(int d) { return d == LH_DTYPE_F32 || d == LH_DTYPE_BF16; }
-
-// Device that owns `p`, or -1 (with the error message set) if p is not device memory.
-int device_of(const void* p, const char* name) {
-  hipPointerAttribute_t attr;
-  std::memset(&attr, 0, sizeof(attr));
-  hipError_t e = hipPointerGetAttributes(&attr, p);
-  if (e != hipSuccess) {
-    (void)hipGetLastError();
-    fail(LH_ERR_INVALID_ARGUMENT, "%s is not a device pointer (%s)", name, hipGetErrorString(e));
-    return -1;
-  }
-  if (attr.type != hipMemoryTypeDevice && attr.type != hipMemoryTypeManaged) {
-    fail(LH_ERR_INVALID_ARGUMENT, "%s is not device memory", name);
-    return -1;
-  }
-  return attr.device;
-}
-
-struct PtrCheck {
-  const void* p;
-  const char* name;
-};
-
-// All non-null pointers must be device memory of one device, 16-byte aligned where required.
-lh_status check_pointers(std::initializer_list<PtrCheck> ptrs, int* dev_out) {
-  int dev = -1;
-  for (const PtrCheck& c : ptrs) {
-    if (!c.p) continue;
-    int d = device_of(c.p, c.name);
-    if (d < 0) return LH_ERR_INVALID_ARGUMENT;
-    if (dev >= 0 && d != dev) return fail(LH_ERR_INVALID_ARGUMENT, "%s is on device %d, other pointers on device %d", c.name, d, dev);
-    dev = d;
-  }
-  if (dev < 0) return fail(LH_ERR_INVALID_ARGUMENT, "no device pointer given");
-  *dev_out = dev;
-  return LH_OK;
-}
-
-lh_status check_aligned(const void* p, const char* name) {
-  if (p && (reinterpret_cast<uintptr_t>(p) % 16) != 0)
-    return fail(LH_ERR_INVALID_ARGUMENT, "%s must be 16-byte aligned", name);
-  return LH_OK;
-}
-
-// Switches to `dev` for the lifetime of the guard and checks that it is a gfx950 device.
-class DeviceGuard {
- public:
-  lh_status enter(int dev) {
-    hipError_t e = hipGetDevice(&prev_);
-    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
-    if (prev_ != dev) {
-      e = hipSetDevice(dev);
-      if (e != hipSuccess) return hip_fail(e, "hipSetDevice");
-      switched_ = true;
-    }
-    static std::mutex mu;
-    static std::vector<int> arch_ok(64, -1);
-    std::lock_guard<std::mutex> lk(mu);
-    if (dev < 0 || dev >= (int)arch_ok.size()) return fail(LH_ERR_UNSUPPORTED, "device %d out of range", dev);
-    if (arch_ok[dev] < 0) {
-      hipDeviceProp_t prop;
-      e = hipGetDeviceProperties(&prop, dev);
-      if (e != hipSuccess) return hip_fail(e, "hipGetDeviceProperties");
-      arch_ok[dev] = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : 0;
-    }
-    if (!arch_ok[dev]) return fail(LH_ERR_UNSUPPORTED, "device %d is not gfx950 (MI355X)", dev);
-    return LH_OK;
-  }
-  ~DeviceGuard() {
-    if (switched_) (void)hipSetDevice(prev_);
-  }
-
- private:
-  int prev_ = 0;
-  bool switched_ = false;
-};
 
 // One stream-ordered pool per device; its release threshold keeps freed scratch for reuse.
 hipError_t scratch_pool(int dev, hipMemPool_t* pool) {
@@ -572,7 +472,7 @@ lh_status lh_absmax(const void* W, lh_dtype w_dtype, int64_t n_groups, int64_t e
   return ok();
 }
 
-const char* lh_last_error(void) { return g_last_error.c_str(); }
+const char* lh_last_error(void) { return g_last_error; }
 
 int lh_version(void) { return LH_VERSION; }
 
