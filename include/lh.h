@@ -40,6 +40,11 @@
  *     not rule out, with a rigorous error bound, and any block whose winner is not certain is
  *     re-scored in float64 with exact quantization.
  *
+ * The entry points of a decode step (lh_rms_norm_quant, lh_matvec, lh_cache_write, lh_cache_read,
+ * lh_paged_attention) run what the calibration leaves behind: 8-bit rows for quantized products,
+ * products with the calibrated NVFP4 weights, and a key-value cache in the same formats.  They keep
+ * no state, allocate nothing and may be captured into a HIP graph.
+ *
  * Citations are to the pages this library follows: "Add activation-aware local Hessian scale
  * calibration" (PR #1976), "add local hessian calibration" (PR #788), "Add WMSE weight scale
  * search calibration" (PR #2283) and "Add composable scale calibration to GPTQ" (PR #2004).
@@ -53,7 +58,7 @@
 extern "C" {
 #endif
 
-#define LH_VERSION 6
+#define LH_VERSION 7
 
 typedef enum {
   LH_OK = 0,
@@ -62,12 +67,14 @@ typedef enum {
   LH_ERR_HIP = 3               /* a HIP runtime call or launch failed */
 } lh_status;
 
-/* The two sentinels widen the enum's value range to every 32-bit int: a value other than F32 or
- * BF16 coming from a caller is then a well-defined lh_dtype in C and C++, and every entry point
- * rejects it with LH_ERR_UNSUPPORTED.  They are not dtypes. */
+/* E4M3 is the type of lh_matvec's 8-bit rows alone; the other entry points take F32 and BF16.
+ * The two sentinels widen the enum's value range to every 32-bit int: another value coming from a
+ * caller is then a well-defined lh_dtype in C and C++, and every entry point rejects what it does
+ * not take with LH_ERR_UNSUPPORTED.  They are not dtypes. */
 typedef enum {
   LH_DTYPE_F32 = 0,
   LH_DTYPE_BF16 = 1,
+  LH_DTYPE_E4M3 = 2,
   LH_DTYPE_RANGE_MIN_ = -2147483647 - 1,
   LH_DTYPE_RANGE_MAX_ = 2147483647
 } lh_dtype;
@@ -306,6 +313,132 @@ lh_status lh_dequantize_ex(const uint8_t* scale_code, const uint8_t* fp4, lh_dty
  */
 lh_status lh_absmax(const void* W, lh_dtype w_dtype, int64_t n_groups, int64_t elems_per_group,
                     float* amax_out, void* stream);
+
+/*
+ * Root-mean-square norm of a residual stream, with the residual's addition and 8-bit output: the
+ * input of a quantized product.
+ *   h[t,i] = X[t,i] + R[t,i] rounded to dtype          (h = X when R is NULL)
+ *   y[t,i] = h[t,i] / sqrt(mean_i h[t,i]^2 + eps) * gamma[i]                        (in fp32)
+ *   per row (group = 0) or per 128 channels of a row (group = 128, the last run may be shorter):
+ *     scale = max|y| * fp32(1/448),  q = the E4M3 value nearest to y / scale (0 where scale = 0)
+ * X, R [rows, cin] of dtype; gamma [cin] of dtype; eps >= 0 and finite.  summed [rows, cin] of dtype
+ * receives h; it is required with R, must be NULL without, and may be X or R itself.
+ * q [rows, cin] E4M3 bytes; q_scale [rows] or [rows, ceil(cin/128)] fp32.  All 16-byte aligned
+ * but q_scale.  Sums are fp32; a row of zeros (with eps = 0, too) gives q = 0.
+ * Errors: INVALID_ARGUMENT for rows < 0 or over 2^31-1, cin <= 0 or cin % 16 or cin > 2^24, a group
+ * other than 0 and 128, a bad eps, R without summed or the reverse, NULL required pointers,
+ * misaligned, non-device or mixed-device pointers.
+ */
+lh_status lh_rms_norm_quant(const void* X, const void* R, lh_dtype dtype, int64_t rows, int64_t cin,
+                            const void* gamma, float eps, int64_t group, void* summed, uint8_t* q,
+                            float* q_scale, void* stream);
+
+/*
+ * Products of a few rows with NVFP4 weights as lh_scale_sweep writes them, dense or per expert (a
+ * decode step's tokens, drafted tokens, small batches):
+ *   Y[t,c] = sum_k Wq[g][c][k] x[t,k] for the rows t of group g,
+ *   Wq[g][c][k] = E2M1(nibble) * v_code * g_g,  g_g = fp32(global_amax[g] / (6 * scale_norm)),
+ * that is lh_dequantize_ex's weights before their rounding.  Products are exact and sums fp32, in a
+ * fixed order; g_g multiplies the sum, which is rounded once to Y's type.
+ * scale_code [n_groups, cout, cin/16], fp4 [n_groups, cout, cin/2] (8-byte aligned), global_amax
+ * [n_groups], scale_norm as in lh_sweep_options.
+ * X [rows, cin], 16-byte aligned: F32, BF16, or E4M3 bytes with x_scale fp32, one per row (x_group = 0,
+ * [rows]) or one per 128 channels (x_group = 128, [rows, ceil(cin/128)]), as lh_rms_norm_quant
+ * writes them; x_scale is NULL and x_group 0 for the other types.
+ * Y [rows, cout]: F32 for F32 rows, BF16 otherwise.
+ * Groups as everywhere; a group without rows is skipped.  Any number of rows works; the weights are
+ * read again for every 64 rows (16 per group with several groups).
+ * Errors: INVALID_ARGUMENT for the shapes of lh_accumulate and lh_scale_sweep, cin > 2^24, a launch of
+ * over 2^31-1 workgroups, scale_norm that is not a positive finite E4M3 value, x_scale or x_group
+ * that do not fit the type, NULL required pointers, misaligned, non-device or mixed-device pointers.
+ */
+lh_status lh_matvec(const void* X, lh_dtype x_dtype, const float* x_scale, int64_t x_group, int64_t rows,
+                    int64_t cin, const int64_t* group_offsets, int64_t n_groups, int64_t cout,
+                    const uint8_t* scale_code, const uint8_t* fp4, const float* global_amax,
+                    float scale_norm, void* Y, void* stream);
+
+/*
+ * A paged key-value cache in one of two formats, owned by the caller.  Pages hold page_size tokens
+ * of every key-value head, head by head; a token's slot is page * page_size + its place in the page.
+ *   LH_CACHE_E4M3   k, v [n_pages, n_heads, page_size, head_dim] bytes; k_scale, v_scale NULL.
+ *                   value = fp32(E4M3 * s), s = fp32(amax[head] * fp32(1/448))
+ *   LH_CACHE_FP4    k, v [n_pages, n_heads, page_size, head_dim/2], element 2j in the low nibble of
+ *                   byte j; k_scale, v_scale [n_pages, n_heads, page_size, head_dim/16] E4M3 bytes.
+ *                   value = fp32(E2M1 * s), s = fp32(v * g), g = fp32(amax[head] * fp32(1/2688)):
+ *                   the NVFP4 rule of lh_activation_fake_quant along head_dim, the head as the
+ *                   group, with g a product by the rounded reciprocal (GPU tensor libraries
+ *                   evaluate amax / 2688 that way; codes made there by this rule are the same)
+ * k_amax, v_amax [n_heads] fp32 device: the calibrated largest magnitude per head (>= 0, finite;
+ * see lh_absmax); larger elements saturate.  Codes are 16-byte, scales 4-byte aligned.
+ */
+typedef enum {
+  LH_CACHE_E4M3 = 0,
+  LH_CACHE_FP4 = 1,
+  LH_CACHE_RANGE_MIN_ = -2147483647 - 1, /* not formats; see lh_dtype */
+  LH_CACHE_RANGE_MAX_ = 2147483647
+} lh_cache_format;
+
+typedef struct {
+  lh_cache_format format;
+  int64_t n_pages, page_size, n_heads, head_dim;
+  uint8_t *k, *v, *k_scale, *v_scale;
+  const float *k_amax, *v_amax;
+} lh_cache;
+
+/*
+ * Quantizes new tokens' keys and values and writes them to their slots.  Every rounding is that of
+ * the exact quotient, ties to the even code.
+ * cache: HOST struct, read during the call.  K, V: element (t, head, i) at t * stride + head *
+ * head_dim + i, strides in elements (at least n_heads * head_dim), so they may be parts of a wider
+ * projection's rows; 16-byte aligned, strides multiples of 16 bytes.
+ * slots [tokens] int64 device; a slot outside [0, n_pages * page_size) is skipped.  Slots named
+ * twice in one call end with one of their tokens (either), head by head.
+ * Errors: UNSUPPORTED for an unknown dtype or format; INVALID_ARGUMENT for n_pages, page_size,
+ * n_heads or head_dim < 1, head_dim % 16, head_dim > 65536, over 2^31-1 heads or tokens of a page, a
+ * launch of over 2^31-1 workgroups, tokens < 0, bad strides, NULL required pointers or block scales that do not fit the
+ * format, misaligned, non-device or mixed-device pointers.
+ */
+lh_status lh_cache_write(const lh_cache* cache, const void* K, int64_t k_stride, const void* V,
+                         int64_t v_stride, lh_dtype dtype, int64_t tokens, const int64_t* slots,
+                         void* stream);
+
+/*
+ * Reads slots back: K, V [tokens, n_heads, head_dim] of dtype (fp32 value, rounded to nearest-even
+ * bf16 for BF16), dense, 16-byte aligned.  A slot outside the cache reads as zeros.  Errors as
+ * lh_cache_write.
+ */
+lh_status lh_cache_read(const lh_cache* cache, const int64_t* slots, int64_t tokens, lh_dtype dtype,
+                        void* K, void* V, void* stream);
+
+/*
+ * Attention of one new token per sequence over the cache (its own key and value already written):
+ *   O[b,h] = sum_t p_t V[t, h/share],  p = softmax_t(scale * Q[b,h] . K[t, h/share]),
+ *   t < lengths[b], share = n_q_heads / n_heads; token t of sequence b is in page
+ *   block_table[b][t / page_size] at place t % page_size.
+ * Q: element (b, h, i) at b * q_stride + h * head_dim + i; O [batch, n_q_heads, head_dim] dense, both
+ * of dtype, 16-byte aligned, q_stride a multiple of 16 bytes.  block_table [batch, max_pages] and
+ * lengths [batch] int32 device.  A length is taken as between 0 and max_pages * page_size; a
+ * sequence of length 0 gives zeros.  Entries of the table past a sequence's last page are not
+ * read; a page outside the cache is read as page 0.  head_dim is 64, 128 or 256.
+ * K and V enter exactly; q is held to 2^-40 of its head's largest element (fp32: to 2^-22 of each
+ * element too), p to fp16 (fp32: two fp16 pieces), and maxima, sums and outputs are fp32.
+ * workspace: device memory of at least lh_paged_attention_workspace bytes (16-byte aligned; NULL if
+ * that is 0) that no other call uses until this one has run.
+ * Errors: UNSUPPORTED for an unknown dtype or format, or another head_dim; INVALID_ARGUMENT as
+ * lh_cache_write, n_q_heads not a positive multiple of n_heads, batch < 0, max_pages < 0,
+ * max_pages * page_size over 2^31-1, a scale that is not finite, a short workspace.
+ */
+lh_status lh_paged_attention(const lh_cache* cache, const void* Q, int64_t q_stride, lh_dtype dtype,
+                             int64_t batch, int64_t n_q_heads, const int32_t* block_table,
+                             int64_t max_pages, const int32_t* lengths, float scale, void* O,
+                             void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Bytes of workspace that lh_paged_attention needs for these sizes (a host computation; 0 for
+ * arguments that it refuses).
+ */
+int64_t lh_paged_attention_workspace(const lh_cache* cache, int64_t batch, int64_t n_q_heads,
+                                     int64_t max_pages);
 
 /* Message of the last error on the calling thread ("" if none); valid until its next call. */
 const char* lh_last_error(void);

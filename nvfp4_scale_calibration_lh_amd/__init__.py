@@ -1,4 +1,5 @@
-"""Python binding of ``liblh.so``, the MI355X local-Hessian NVFP4 weight-scale calibration library.
+"""Python binding of ``liblh.so``, the MI355X local-Hessian NVFP4 weight-scale calibration library and
+the decode-step operators on the formats it calibrates.
 
 The functions carry the names of the C entry points in ``include/lh.h`` and only marshal
 arguments: they check dtypes, shapes and devices of torch tensors, allocate missing outputs with
@@ -19,11 +20,13 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("LH_LIBRARY") or os.path.join(_PKG, "liblh.so")
 
 LH_OK, LH_ERR_INVALID_ARGUMENT, LH_ERR_UNSUPPORTED, LH_ERR_HIP = 0, 1, 2, 3
-LH_DTYPE_F32, LH_DTYPE_BF16 = 0, 1
+LH_DTYPE_F32, LH_DTYPE_BF16, LH_DTYPE_E4M3 = 0, 1, 2
+LH_CACHE_E4M3, LH_CACHE_FP4 = 0, 1
 
 EXPORTED = ("lh_accumulate", "lh_accumulate_noalloc", "lh_accumulate_act_aware", "lh_accumulate_act_aware_fq", "lh_activation_fake_quant",
             "lh_accumulate_sweep", "lh_dequantize", "lh_dequantize_ex", "lh_scale_sweep", "lh_scale_sweep_ex", "lh_scale_sweep_diag",
-            "lh_scale_sweep_diag_ex", "lh_scale_sweep_mse", "lh_absmax", "lh_last_error", "lh_version")
+            "lh_scale_sweep_diag_ex", "lh_scale_sweep_mse", "lh_absmax", "lh_rms_norm_quant", "lh_matvec", "lh_cache_write",
+            "lh_cache_read", "lh_paged_attention", "lh_paged_attention_workspace", "lh_last_error", "lh_version")
 MAX_MULTIPLIERS = 128
 
 
@@ -31,6 +34,12 @@ class SweepOptions(ctypes.Structure):
     """lh_sweep_options: scale_norm (448 or 256 for "4/6"), the amax multipliers (host array)."""
     _fields_ = [("scale_norm", ctypes.c_float), ("n_multipliers", ctypes.c_int32),
                 ("multipliers", ctypes.POINTER(ctypes.c_float))]
+
+
+class CacheStruct(ctypes.Structure):
+    """lh_cache: the format, sizes and device pointers of a paged key-value cache."""
+    _fields_ = ([("format", ctypes.c_int)] + [(n, ctypes.c_int64) for n in ("n_pages", "page_size", "n_heads", "head_dim")]
+                + [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "k_amax", "v_amax")])
 
 
 class LHError(RuntimeError):
@@ -66,11 +75,19 @@ def lib() -> ctypes.CDLL:
         h.lh_scale_sweep_mse.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp]
         h.lh_absmax.argtypes = [vp, i32, i64, i64, vp, vp]
         h.lh_dequantize.argtypes = [vp, vp, i32, i64, i64, i64, vp, vp, vp, vp]
+        h.lh_rms_norm_quant.argtypes = [vp, vp, i32, i64, i64, vp, f32, i64, vp, vp, vp, vp]
+        h.lh_matvec.argtypes = [vp, i32, vp, i64, i64, i64, vp, i64, i64, vp, vp, vp, f32, vp, vp]
+        h.lh_cache_write.argtypes = [vp, vp, i64, vp, i64, i32, i64, vp, vp]
+        h.lh_cache_read.argtypes = [vp, vp, i64, i32, vp, vp, vp]
+        h.lh_paged_attention.argtypes = [vp, vp, i64, i32, i64, i64, vp, i64, vp, f32, vp, vp, i64, vp]
+        h.lh_paged_attention_workspace.argtypes = [vp, i64, i64, i64]
         for f in ("lh_accumulate", "lh_accumulate_noalloc", "lh_accumulate_act_aware", "lh_accumulate_act_aware_fq",
                   "lh_activation_fake_quant", "lh_scale_sweep", "lh_scale_sweep_ex", "lh_scale_sweep_diag_ex",
                   "lh_dequantize_ex", "lh_accumulate_sweep",
-                  "lh_scale_sweep_diag", "lh_scale_sweep_mse", "lh_absmax", "lh_dequantize"):
+                  "lh_scale_sweep_diag", "lh_scale_sweep_mse", "lh_absmax", "lh_dequantize", "lh_rms_norm_quant",
+                  "lh_matvec", "lh_cache_write", "lh_cache_read", "lh_paged_attention"):
             getattr(h, f).restype = ctypes.c_int
+        h.lh_paged_attention_workspace.restype = ctypes.c_int64
         h.lh_last_error.argtypes = []
         h.lh_last_error.restype = ctypes.c_char_p
         h.lh_version.argtypes = []
@@ -404,3 +421,188 @@ def lh_absmax(W: torch.Tensor, amax: Optional[torch.Tensor] = None) -> torch.Ten
     _need(amax, "amax", (G,), torch.float32)
     _check(lib().lh_absmax(_ptr(W), _dtype_code(W), G, per, _ptr(amax), _stream(W.device)))
     return amax
+
+
+def _rows_scales(t: torch.Tensor, group: int) -> Tuple[int, ...]:
+    rows, cin = t.shape
+    return (rows, 1 if group == 0 else -(-cin // group))
+
+
+def lh_rms_norm_quant(X: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.Tensor] = None, *,
+                      eps: float = 1e-6, group: int = 0, q: Optional[torch.Tensor] = None,
+                      scale: Optional[torch.Tensor] = None, summed: Optional[torch.Tensor] = None):
+    """(q, scale, summed): the RMS norm of X + residual times gamma, X [rows, cin], as E4M3 q [rows, cin]
+    (torch.float8_e4m3fn) with scale [rows, 1], or [rows, ceil(cin/128)] for group = 128, and the
+    sum itself in X's dtype (None without a residual; it may be X or residual for an update in place)."""
+    _need(X, "X")
+    if X.dim() != 2:
+        raise ValueError("X must be [rows, cin]")
+    rows, cin = X.shape
+    if group not in (0, 128):
+        raise ValueError("group must be 0 or 128")
+    _need(gamma, "gamma", (cin,), X.dtype)
+    if residual is not None:
+        _need(residual, "residual", X.shape, X.dtype)
+        if summed is None:
+            summed = torch.empty_like(X)
+    if summed is not None:
+        _need(summed, "summed", X.shape, X.dtype)
+    if q is None:
+        q = torch.empty((rows, cin), dtype=torch.float8_e4m3fn, device=X.device)
+    if scale is None:
+        scale = torch.empty(_rows_scales(X, group), dtype=torch.float32, device=X.device)
+    _need(q, "q", X.shape, torch.float8_e4m3fn)
+    _need(scale, "scale", _rows_scales(X, group), torch.float32)
+    _check(lib().lh_rms_norm_quant(_ptr(X), _ptr(residual), _dtype_code(X), rows, cin, _ptr(gamma), float(eps), group,
+                                   _ptr(summed), _ptr(q), _ptr(scale), _stream(X.device)))
+    return q, scale, summed
+
+
+def lh_matvec(X: torch.Tensor, code: torch.Tensor, fp4: torch.Tensor, amax: torch.Tensor, Y: Optional[torch.Tensor] = None, *,
+              x_scale: Optional[torch.Tensor] = None, x_group: int = 0, offsets: Optional[torch.Tensor] = None,
+              norm: float = 448.0) -> torch.Tensor:
+    """Y [rows, cout]: X [rows, cin] times the NVFP4 weights (code [G, cout, cin/16], fp4 [G, cout, cin/2], amax
+    [G]) of a scale sweep with normalization `norm`, the rows of each group (offsets [G+1]) against its
+    matrix.  X is fp32, bf16, or torch.float8_e4m3fn with x_scale as lh_rms_norm_quant gives it (x_group 0:
+    [rows, 1], 128: [rows, ceil(cin/128)]); Y is fp32 for fp32 X, otherwise bf16."""
+    _need(X, "X")
+    if X.dim() != 2 or code.dim() != 3:
+        raise ValueError("X must be [rows, cin] and code [G, cout, cin/16]")
+    rows, cin = X.shape
+    offsets, G = _offsets(offsets, X)
+    cout = code.shape[1]
+    _need(code, "code", (G, cout, cin // 16), torch.uint8)
+    _need(fp4, "fp4", (G, cout, cin // 2), torch.uint8)
+    _need(amax, "amax", (G,), torch.float32)
+    if x_group not in (0, 128):
+        raise ValueError("x_group must be 0 or 128")
+    if X.dtype == torch.float8_e4m3fn:
+        dtype = LH_DTYPE_E4M3
+        if x_scale is None:
+            raise ValueError("x_scale is required for E4M3 rows")
+        _need(x_scale, "x_scale", _rows_scales(X, x_group), torch.float32)
+    else:
+        dtype = _dtype_code(X)
+        if x_scale is not None or x_group != 0:
+            raise ValueError("x_scale and x_group are for E4M3 rows")
+    y_dtype = torch.float32 if dtype == LH_DTYPE_F32 else torch.bfloat16
+    if Y is None:
+        Y = torch.empty((rows, cout), dtype=y_dtype, device=X.device)
+    _need(Y, "Y", (rows, cout), y_dtype)
+    _check(lib().lh_matvec(_ptr(X), dtype, _ptr(x_scale), x_group, rows, cin, _ptr(offsets), G, cout, _ptr(code),
+                           _ptr(fp4), _ptr(amax), float(norm), _ptr(Y), _stream(X.device)))
+    return Y
+
+
+class Cache:
+    """A paged key-value cache: its code tensors k, v [n_pages, n_heads, page_size, head_dim] uint8 (E4M3) or
+    [..., head_dim/2] with block scales k_scale, v_scale [..., head_dim/16] uint8 (NVFP4), and the calibrated
+    amax per head k_amax, v_amax [n_heads] fp32.  `Cache.empty` makes the tensors."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_amax: torch.Tensor, v_amax: torch.Tensor,
+                 k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None):
+        if k.dim() != 4:
+            raise ValueError("k must be [n_pages, n_heads, page_size, head_dim (or half of it)]")
+        if (k_scale is None) != (v_scale is None):
+            raise ValueError("k_scale and v_scale must be given together")
+        four = k_scale is not None
+        pages, heads, page_size, width = k.shape
+        self.head_dim = 2 * width if four else width
+        if self.head_dim % 16:
+            raise ValueError("head_dim must be a multiple of 16")
+        _need(k, "k", dtype=torch.uint8)
+        _need(v, "v", k.shape, torch.uint8)
+        _need(k_amax, "k_amax", (heads,), torch.float32)
+        _need(v_amax, "v_amax", (heads,), torch.float32)
+        if four:
+            _need(k_scale, "k_scale", (pages, heads, page_size, self.head_dim // 16), torch.uint8)
+            _need(v_scale, "v_scale", (pages, heads, page_size, self.head_dim // 16), torch.uint8)
+        self.k, self.v, self.k_amax, self.v_amax, self.k_scale, self.v_scale = k, v, k_amax, v_amax, k_scale, v_scale
+        self.n_pages, self.n_heads, self.page_size = pages, heads, page_size
+        self.struct = CacheStruct(LH_CACHE_FP4 if four else LH_CACHE_E4M3, pages, page_size, heads, self.head_dim,
+                                  k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if four else None,
+                                  v_scale.data_ptr() if four else None, k_amax.data_ptr(), v_amax.data_ptr())
+
+    @classmethod
+    def empty(cls, n_pages: int, page_size: int, n_heads: int, head_dim: int, k_amax: torch.Tensor, v_amax: torch.Tensor, *,
+              four_bit: bool) -> "Cache":
+        """A cache of zeros on the device of k_amax."""
+        def new(n):
+            return torch.zeros((n_pages, n_heads, page_size, n), dtype=torch.uint8, device=k_amax.device)
+        if four_bit:
+            return cls(new(head_dim // 2), new(head_dim // 2), k_amax, v_amax, new(head_dim // 16), new(head_dim // 16))
+        return cls(new(head_dim), new(head_dim), k_amax, v_amax)
+
+
+def _heads(t: torch.Tensor, name: str, heads: int, dim: int, dtype=None, tokens=None) -> int:
+    """Checks a [tokens, heads, dim] tensor whose tokens may lie apart; its stride between tokens."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or (tokens is not None and t.shape[0] != tokens):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({'tokens' if tokens is None else tokens}, {heads}, {dim})")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    stride = t.stride()
+    if (dim > 1 and stride[2] != 1) or (heads > 1 and stride[1] != dim):
+        raise ValueError(f"{name} must hold each token's heads in one run of memory")
+    return stride[0] if t.shape[0] > 1 else max(stride[0], heads * dim)
+
+
+def lh_cache_write(cache: Cache, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor) -> None:
+    """Quantizes K, V [tokens, n_heads, head_dim] (fp32 or bf16; tokens may lie apart, as parts of a projection's
+    rows do) into the cache at slots [tokens] int64 (page * page_size + place; outside the cache: skipped)."""
+    ks = _heads(K, "K", cache.n_heads, cache.head_dim)
+    vs = _heads(V, "V", cache.n_heads, cache.head_dim, K.dtype, K.shape[0])
+    _need(slots, "slots", (K.shape[0],), torch.int64)
+    _check(lib().lh_cache_write(ctypes.byref(cache.struct), _ptr(K), ks, _ptr(V), vs, _dtype_code(K), K.shape[0], _ptr(slots),
+                                _stream(K.device)))
+
+
+def lh_cache_read(cache: Cache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16, K: Optional[torch.Tensor] = None,
+                  V: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(K, V) [tokens, n_heads, head_dim] of dtype (bf16 or fp32): the values held at slots [tokens] int64."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("dtype must be torch.bfloat16 or torch.float32")
+    _need(slots, "slots", dtype=torch.int64)
+    shape = (slots.numel(), cache.n_heads, cache.head_dim)
+    if K is None:
+        K = torch.empty(shape, dtype=dtype, device=slots.device)
+    if V is None:
+        V = torch.empty(shape, dtype=dtype, device=slots.device)
+    _need(K, "K", shape, dtype)
+    _need(V, "V", shape, dtype)
+    _check(lib().lh_cache_read(ctypes.byref(cache.struct), _ptr(slots), shape[0], LH_DTYPE_BF16 if dtype == torch.bfloat16 else LH_DTYPE_F32,
+                               _ptr(K), _ptr(V), _stream(slots.device)))
+    return K, V
+
+
+def lh_paged_attention_workspace(cache: Cache, batch: int, n_q_heads: int, max_pages: int) -> int:
+    """Bytes of workspace that lh_paged_attention needs for these sizes."""
+    return int(lib().lh_paged_attention_workspace(ctypes.byref(cache.struct), batch, n_q_heads, max_pages))
+
+
+def lh_paged_attention(Q: torch.Tensor, cache: Cache, block_table: torch.Tensor, lengths: torch.Tensor, O: Optional[torch.Tensor] = None, *,
+                       scale: float, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """O [batch, n_q_heads, head_dim]: one new token's attention per sequence, Q [batch, n_q_heads, head_dim] (fp32 or
+    bf16; sequences may lie apart) over tokens t < lengths[b] in pages block_table[b] (int32 [batch, max_pages]).
+    workspace (uint8) is allocated on the current stream when needed and not given."""
+    if block_table.dim() != 2 or Q.dim() != 3:
+        raise ValueError("block_table must be [batch, max_pages] and Q [batch, n_q_heads, head_dim]")
+    batch, heads, dim = Q.shape
+    stride = _heads(Q, "Q", heads, cache.head_dim)
+    pages = block_table.shape[1]
+    _need(block_table, "block_table", (batch, pages), torch.int32)
+    _need(lengths, "lengths", (batch,), torch.int32)
+    if O is None:
+        O = torch.empty((batch, heads, dim), dtype=Q.dtype, device=Q.device)
+    _need(O, "O", (batch, heads, dim), Q.dtype)
+    if workspace is None:
+        need = lh_paged_attention_workspace(cache, batch, heads, pages)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=Q.device)
+    else:
+        _need(workspace, "workspace", dtype=torch.uint8)
+    _check(lib().lh_paged_attention(ctypes.byref(cache.struct), _ptr(Q), stride, _dtype_code(Q), batch, heads, _ptr(block_table), pages,
+                                    _ptr(lengths), float(scale), _ptr(O), _ptr(workspace),
+                                    0 if workspace is None else workspace.numel(), _stream(Q.device)))
+    return O

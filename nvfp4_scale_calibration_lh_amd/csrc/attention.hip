@@ -1,0 +1,498 @@
+// Attention of one new token per sequence over the paged, quantised key-value cache:
+//   o[h] = sum_t p_t v_t,  p = softmax over the sequence's tokens of scale * (q[h] . k_t),
+// head h reading the keys and values of key-value head h / share.  An empty sequence gives 0.
+//
+// Bound by reading the cache once, so one workgroup serves up to 16 of the query heads that share a
+// key-value head (the column side of a 16-wide matrix instruction), and a long sequence is split
+// over workgroups whose partial (maximum, sum, output) a second kernel joins.  Within a workgroup
+// the four waves take 32-token tiles in turn, each with a running maximum and sum of its own, and
+// meet in LDS at the end.
+//
+// A tile is two matrix products without any exchange between lanes:
+//   S^T = K Q^T   A = 16 tokens of K, B = the heads' q; the result's lane (head, quarter) holds
+//                 tokens 4*quarter + r of each 16
+//   O^T = V^T P^T B = P^T in exactly that lane layout, A = V^T with its tokens taken in the same order
+// Every code is exact in fp16: E2M1 times its E4M3 block scale has at most 6 significant bits in
+// [2^-10, 2688], E4M3 has 4 in [2^-9, 448]; the heads' global scales multiply scores and outputs.
+// q is multiplied by the power of two that brings its head's largest element to [2^14, 2^15):
+// bf16 then fits fp16 exactly down to 2^-40 of that element, fp32 is held as two fp16 pieces.
+// p is made as 2^(s - m + 10) with m within 4 of the running maximum, so it stays under 2^14 and
+// tokens 2^-24 below the largest keep all fp16 bits; for fp32 it is two pieces as well.  Sums,
+// maxima and outputs are fp32.
+#include "lh_internal.hpp"
+
+#include <algorithm>
+
+namespace lh {
+namespace {
+
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kTile = 32;                    // tokens a wave takes at a time
+constexpr int kStep = kTile * kWaves;        // tokens a workgroup takes at a time
+constexpr int kHeads = 16;                   // query heads of one workgroup
+constexpr int kMinChunk = 256;               // tokens below which a sequence is not split further
+constexpr float kPBits = 10.0f;              // p = 2^(s - m + kPBits)
+
+struct Args {
+  const void* q;
+  int64_t q_stride;
+  const uint8_t *k, *v, *k_scale, *v_scale;
+  const float *k_amax, *v_amax;
+  const int* table;
+  const int* lengths;
+  void* o;
+  float* part;                               // [pair][split][2 + D][16]: m, l, then the outputs
+  float scale_log2;                          // softmax scale * log2(e)
+  int heads, share, tiles, splits, width;
+  int64_t n_pages;
+  unsigned page_size, page_mul, page_shift;  // n / page_size = n * page_mul >> page_shift, n < 2^31
+};
+
+template <int N, class F>
+__device__ inline void each(F&& f) {
+  if constexpr (N > 0) {
+    each<N - 1>(f);
+    f(std::integral_constant<int, N - 1>{});
+  }
+}
+
+// B bytes as 32-bit words.
+template <int B>
+struct Bytes {
+  unsigned w[B < 4 ? 1 : B / 4];
+};
+template <int B>
+__device__ inline Bytes<B> load(const uint8_t* p) {
+  Bytes<B> r;
+  if constexpr (B == 1) {
+    r.w[0] = *p;
+  } else if constexpr (B == 2) {
+    r.w[0] = *(const unsigned short*)p;
+  } else if constexpr (B == 4) {
+    r.w[0] = *(const unsigned*)p;
+  } else if constexpr (B == 8) {
+    const uint2 v = *(const uint2*)p;
+    r.w[0] = v.x, r.w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < B / 16; ++i) {
+      const uint4 v = ((const uint4*)p)[i];
+      r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
+    }
+  }
+  return r;
+}
+
+// Elements 2P and 2P + 1 of a run of codes.
+template <bool FOUR, int P, int B>
+__device__ inline h2 pair_of(const Bytes<B>& b) {
+  if constexpr (FOUR)
+    return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(b.w[P / 4], 1.0f, P % 4);
+  else
+    return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)b.w[P / 2], 1.0f, P % 2 == 1);
+}
+
+// The E4M3 block scale in byte I, in both halves.
+template <int I, int B>
+__device__ inline h2 scale_of(const Bytes<B>& b) {
+  const h2 s = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)b.w[I / 4], 1.0f, (I & 2) != 0);
+  return h2{s[I & 1], s[I & 1]};
+}
+
+// The tokens [from, to) of one sequence that one split takes, and how many splits it has.
+struct Range {
+  int from, to, splits;
+};
+__device__ inline Range range_of(int len, int split, int splits) {
+  int chunk = (len + splits - 1) / splits;
+  chunk = max((chunk + kStep - 1) / kStep * kStep, kMinChunk);
+  return {min(split * chunk, len), min(split * chunk + chunk, len), (len + chunk - 1) / chunk};
+}
+__device__ inline int length_of(const Args& a, int64_t b) {
+  const int64_t most = (int64_t)a.width * a.page_size;
+  const int len = a.lengths[b];
+  return len < 0 ? 0 : (len > most ? (int)most : len);
+}
+
+// FOUR: NVFP4 codes, otherwise E4M3.  F32: fp32 q and o.  ALIGNED: 16 | page_size, so 16 tokens
+// share a page and its number is one scalar load.
+template <bool FOUR, int D, bool F32, bool ALIGNED>
+__global__ __launch_bounds__(kThreads) void k_attention(const Args a) {
+  constexpr int kSteps = D / 32;                        // 32-deep matrix instructions of q . k
+  constexpr int kOut = D / 16;                          // 16-row tiles of the output
+  constexpr int kPieces = F32 ? 2 : 1;
+  constexpr int kRow = FOUR ? D / 2 : D;                // code bytes of one token
+  constexpr int kKB = kRow / 4, kVB = kRow / 16;        // code bytes a lane takes of a K / V token
+  constexpr int kKS = D / 64;                           // K block scales of a lane
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int i = lane & 15, quarter = lane >> 4;
+
+  unsigned id = blockIdx.x;
+  const int split = id % a.splits;
+  id /= a.splits;
+  const int tile = id % a.tiles;
+  id /= a.tiles;
+  const int kvh = id % a.heads;
+  const int64_t b = id / a.heads;
+  const int len = length_of(a, b);
+  const Range rg = range_of(len, split, a.splits);
+  if (split > 0 && rg.from >= rg.to) return;            // split 0 of an empty sequence writes zeros
+
+  const int head = tile * kHeads + i;                   // of this lane's column, within the share
+  const bool live_head = head < a.share;
+  const int64_t qh = (int64_t)kvh * a.share + head;
+
+  // q, its power of two, and the factor of the scores
+  h8 qf[kSteps][kPieces];
+  float factor;
+  {
+    float x[D / 4];
+    if constexpr (F32) {
+      const uint4* p = (const uint4*)((const float*)a.q + b * a.q_stride + qh * D + quarter * (D / 4));
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        const uint4 v = live_head ? p[j] : uint4{0, 0, 0, 0};
+        x[4 * j] = __uint_as_float(v.x), x[4 * j + 1] = __uint_as_float(v.y);
+        x[4 * j + 2] = __uint_as_float(v.z), x[4 * j + 3] = __uint_as_float(v.w);
+      }
+    } else {
+      const uint4* p = (const uint4*)((const unsigned short*)a.q + b * a.q_stride + qh * D + quarter * (D / 4));
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        const uint4 v = live_head ? p[j] : uint4{0, 0, 0, 0};
+        const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          x[8 * j + 2 * k] = __uint_as_float(w[k] << 16);
+          x[8 * j + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+        }
+      }
+    }
+    float top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < D / 4; ++j) top = fmaxf(top, fabsf(x[j]));
+    top = fmaxf(top, __shfl_xor(top, 16, 64));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    const int e = min(14 - (int)((__float_as_uint(top) >> 23) & 255u) + 127, 126);
+    const float up = ldexpf(1.0f, e);
+    factor = a.scale_log2 * cache_unit(a.k_amax[kvh], FOUR) * ldexpf(1.0f, -e);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float f = x[8 * s + k] * up;
+        qf[s][0][k] = (_Float16)f;
+        if constexpr (F32) qf[s][1][k] = (_Float16)(f - (float)qf[s][0][k]);
+      }
+  }
+
+  const int* table = a.table + b * a.width;
+  const int last = len - 1;
+  // Element offset (in tokens of one head) of a token's codes.
+  auto page_base = [&](int page) {
+    const int64_t p = (unsigned)page < (uint64_t)a.n_pages ? page : 0;   // a bad page reads page 0
+    return (p * a.heads + kvh) * a.page_size;
+  };
+  auto divide = [&](unsigned n) { return (unsigned)(((uint64_t)n * a.page_mul) >> a.page_shift); };
+  // Row of token t (t <= last) in the codes: base16 is the tile's 16-token group (uniform).
+  struct Group {
+    int64_t row;                                        // of its first token
+    int first;
+  };
+  auto group_at = [&](int t16) {
+    Group g;
+    g.first = __builtin_amdgcn_readfirstlane(min(t16, last & ~15));
+    const unsigned p = divide((unsigned)g.first);
+    g.row = page_base(table[p]) + (unsigned)(g.first - (int)(p * a.page_size));
+    return g;
+  };
+  auto row_at = [&](const Group& g, int t) -> int64_t {
+    const int tc = min(t, last);
+    if constexpr (ALIGNED) return g.row + (tc - g.first);
+    const unsigned p = divide((unsigned)tc);
+    return page_base(table[p]) + (unsigned)(tc - (int)(p * a.page_size));
+  };
+
+  Bytes<kKB> kc[2];
+  Bytes<kKS> ks[2];
+  Bytes<kVB> vc[8];
+  unsigned vs[8];
+  auto load_k = [&](const Group* g, int t0) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int64_t row = row_at(g[x], t0 + 16 * x + i);
+      kc[x] = load<kKB>(a.k + row * kRow + quarter * kKB);
+      if constexpr (FOUR) ks[x] = load<kKS>(a.k_scale + row * (D / 16) + quarter * kKS);
+    }
+  };
+  auto load_v = [&](const Group* g, int t0) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int64_t row = row_at(g[e / 4], t0 + 16 * (e / 4) + 4 * quarter + e % 4);
+      vc[e] = load<kVB>(a.v + row * kRow + i * kVB);
+      if constexpr (FOUR) vs[e] = a.v_scale[row * (D / 16) + (i * kOut) / 16];
+    }
+  };
+
+  v4f acc[kOut];
+#pragma unroll
+  for (int n = 0; n < kOut; ++n) acc[n] = v4f{0, 0, 0, 0};
+  float m = -INFINITY, l = 0.0f;
+
+  int t0 = rg.from + wave * kTile;
+  Group g[2];
+  if (t0 < rg.to) {
+    if constexpr (ALIGNED) g[0] = group_at(t0), g[1] = group_at(t0 + 16);
+    load_k(g, t0);
+    load_v(g, t0);
+  }
+  for (; t0 < rg.to; t0 += kStep) {
+    const int next = t0 + kStep;
+    const bool more = next < rg.to;
+    Group gn[2];
+    if constexpr (ALIGNED) {
+      if (more) gn[0] = group_at(next), gn[1] = group_at(next + 16);
+    }
+    // scores
+    v4f s[2] = {v4f{0, 0, 0, 0}, v4f{0, 0, 0, 0}};
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      each<kSteps>([&](auto st) {
+        constexpr int S = decltype(st)::value;
+        h8 kf;
+        each<4>([&](auto pp) {
+          constexpr int P = decltype(pp)::value;
+          h2 v = pair_of<FOUR, 4 * S + P>(kc[x]);
+          if constexpr (FOUR) v *= scale_of<S / 2>(ks[x]);
+          kf[2 * P] = v[0];
+          kf[2 * P + 1] = v[1];
+        });
+#pragma unroll
+        for (int pc = 0; pc < kPieces; ++pc)
+          s[x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[S][pc], s[x], 0, 0, 0);
+      });
+    }
+    if (more) load_k(gn, next);
+    // p, with the running maximum moved only when a score passes it by more than 4
+    float p[8], tmax = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int t = t0 + 16 * (e / 4) + 4 * quarter + e % 4;
+      p[e] = t < rg.to ? s[e / 4][e % 4] * factor : -INFINITY;
+      tmax = fmaxf(tmax, p[e]);
+    }
+    if (__any(tmax > m + 4.0f)) {
+      tmax = fmaxf(tmax, __shfl_xor(tmax, 16, 64));
+      tmax = fmaxf(tmax, __shfl_xor(tmax, 32, 64));
+      const float mn = fmaxf(m, tmax);
+      const float alpha = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      l *= alpha;
+#pragma unroll
+      for (int n = 0; n < kOut; ++n) acc[n] *= alpha;
+    }
+    const float shift = m == -INFINITY ? 0.0f : kPBits - m;
+    h8 pf[kPieces];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float f = __builtin_amdgcn_exp2f(p[e] + shift);
+      l += f;
+      pf[0][e] = (_Float16)f;
+      if constexpr (F32) pf[1][e] = (_Float16)(f - (float)pf[0][e]);
+    }
+    // output
+    each<kOut / 2>([&](auto nn) {
+      constexpr int P = decltype(nn)::value;
+      h8 lo, hi;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        h2 v = pair_of<FOUR, P>(vc[e]);
+        if constexpr (FOUR) {
+          const h2 sc = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)vs[e], 1.0f, false);
+          v *= h2{sc[0], sc[0]};
+        }
+        lo[e] = v[0];
+        hi[e] = v[1];
+      }
+#pragma unroll
+      for (int pc = 0; pc < kPieces; ++pc) {
+        acc[2 * P] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, pf[pc], acc[2 * P], 0, 0, 0);
+        acc[2 * P + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, pf[pc], acc[2 * P + 1], 0, 0, 0);
+      }
+    });
+    if (more) load_v(gn, next);
+    g[0] = gn[0], g[1] = gn[1];
+  }
+  l += __shfl_xor(l, 16, 64);
+  l += __shfl_xor(l, 32, 64);
+
+  // the four waves: a common maximum, then sums of the outputs in two halving steps
+  __shared__ float sh_m[kWaves][kHeads], sh_l[kWaves][kHeads];
+  __shared__ float sh_o[kWaves / 2][kHeads][D + 4];
+  if (quarter == 0) sh_m[wave][i] = m;
+  __syncthreads();
+  float top = sh_m[0][i];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) top = fmaxf(top, sh_m[w][i]);
+  const float alpha = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+  if (quarter == 0) sh_l[wave][i] = l * alpha;
+#pragma unroll
+  for (int n = 0; n < kOut; ++n) acc[n] *= alpha;
+  auto at = [&](int w, int n, int r) -> float& { return sh_o[w][i][(4 * quarter + r) * kOut + n]; };
+#pragma unroll
+  for (int half = kWaves / 2; half >= 1; half /= 2) {
+    if (wave >= half && wave < 2 * half) {
+#pragma unroll
+      for (int n = 0; n < kOut; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) at(wave - half, n, r) = acc[n][r];
+    }
+    __syncthreads();
+    if (wave < half) {
+#pragma unroll
+      for (int n = 0; n < kOut; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[n][r] += at(wave, n, r);
+    }
+    __syncthreads();
+  }
+  if (wave != 0 || !live_head) return;
+  l = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) l += sh_l[w][i];
+  const int d0 = 4 * quarter * kOut;                    // this lane's D / 4 outputs are contiguous
+  if (rg.splits <= 1) {
+    const float f = l > 0.0f ? cache_unit(a.v_amax[kvh], FOUR) / l : 0.0f;
+    const int64_t to = (b * a.heads * a.share + qh) * D + d0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int n = 0; n < kOut; n += 4) {
+        const v4f v = {acc[n][r] * f, acc[n + 1][r] * f, acc[n + 2][r] * f, acc[n + 3][r] * f};
+        if constexpr (F32) {
+          *(v4f*)((float*)a.o + to + r * kOut + n) = v;
+        } else {
+          const v2bf x = __builtin_convertvector((v2f){v[0], v[1]}, v2bf), y = __builtin_convertvector((v2f){v[2], v[3]}, v2bf);
+          *(uint2*)((unsigned short*)a.o + to + r * kOut + n) = uint2{__builtin_bit_cast(unsigned, x), __builtin_bit_cast(unsigned, y)};
+        }
+      }
+    return;
+  }
+  float* part = a.part + (((b * a.heads + kvh) * a.tiles + tile) * (int64_t)a.splits + split) * (kHeads * (D + 2));
+  if (quarter == 0) part[i] = top, part[kHeads + i] = l;
+  float* out = part + 2 * kHeads + i * D + d0;
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int n = 0; n < kOut; n += 4) *(v4f*)(out + r * kOut + n) = v4f{acc[n][r], acc[n + 1][r], acc[n + 2][r], acc[n + 3][r]};
+}
+
+// Joins the partial results of a sequence's splits, in their order; one workgroup a query head, one
+// thread an element.  Sequences with one split were finished by it.
+template <bool FOUR, int D, bool F32>
+__global__ __launch_bounds__(D) void k_attention_join(const Args a) {
+  const int share = a.share;
+  const int64_t b = blockIdx.x / (unsigned)(a.heads * share);
+  const int h = blockIdx.x % (unsigned)(a.heads * share), kvh = h / share, head = h % share;
+  const int splits = range_of(length_of(a, b), 0, a.splits).splits;
+  if (splits <= 1) return;
+  const int tile = head / kHeads, i = head % kHeads;
+  const float* part = a.part + (((b * a.heads + kvh) * a.tiles + tile) * (int64_t)a.splits) * (kHeads * (D + 2));
+  constexpr int kPart = kHeads * (D + 2);
+  float top = -INFINITY;
+  for (int s = 0; s < splits; ++s) top = fmaxf(top, part[(int64_t)s * kPart + i]);
+  float l = 0.0f, o = 0.0f;
+  for (int s = 0; s < splits; ++s) {
+    const float* p = part + (int64_t)s * kPart;
+    const float f = p[i] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(p[i] - top);
+    l = fmaf(p[kHeads + i], f, l);
+    o = fmaf(p[2 * kHeads + i * D + threadIdx.x], f, o);
+  }
+  o = l > 0.0f ? o * (cache_unit(a.v_amax[kvh], FOUR) / l) : 0.0f;
+  const int64_t to = (int64_t)blockIdx.x * D + threadIdx.x;
+  if constexpr (F32)
+    ((float*)a.o)[to] = o;
+  else
+    ((__bf16*)a.o)[to] = (__bf16)o;
+}
+
+// About this many workgroups in all where the sequences are long enough.
+constexpr int64_t kWorkgroups = 2048;
+
+int splits_for(const CacheView& c, int64_t batch, int64_t share, int64_t width) {
+  const int64_t pairs = std::max<int64_t>(batch * c.heads * ((share + kHeads - 1) / kHeads), 1);
+  const int64_t most = std::max<int64_t>((width * c.page_size + kMinChunk - 1) / kMinChunk, 1);
+  return (int)std::min((kWorkgroups + pairs - 1) / pairs, most);
+}
+
+template <bool FOUR, int D, bool F32>
+void launch_typed(const Args& a, unsigned grid, unsigned join, hipStream_t stream) {
+  if (a.page_size % 16 == 0)
+    hipLaunchKernelGGL((k_attention<FOUR, D, F32, true>), dim3(grid), dim3(kThreads), 0, stream, a);
+  else
+    hipLaunchKernelGGL((k_attention<FOUR, D, F32, false>), dim3(grid), dim3(kThreads), 0, stream, a);
+  if (a.splits > 1) hipLaunchKernelGGL((k_attention_join<FOUR, D, F32>), dim3(join), dim3(D), 0, stream, a);
+}
+
+template <int D>
+void launch_dim(const Args& a, bool four, bool f32, unsigned grid, unsigned join, hipStream_t stream) {
+  if (four) {
+    if (f32) launch_typed<true, D, true>(a, grid, join, stream);
+    else launch_typed<true, D, false>(a, grid, join, stream);
+  } else {
+    if (f32) launch_typed<false, D, true>(a, grid, join, stream);
+    else launch_typed<false, D, false>(a, grid, join, stream);
+  }
+}
+
+}  // namespace
+
+int64_t attention_grid(const CacheView& c, int64_t batch, int64_t share, int64_t width) {
+  return batch * c.heads * ((share + kHeads - 1) / kHeads) * splits_for(c, batch, share, width);
+}
+
+int64_t attention_workspace(const CacheView& c, int64_t batch, int64_t share, int64_t width) {
+  if (splits_for(c, batch, share, width) <= 1) return 0;
+  return attention_grid(c, batch, share, width) * kHeads * (c.dim + 2) * (int64_t)sizeof(float);
+}
+
+hipError_t launch_attention(const CacheView& c, const void* q, bool bf16, int64_t batch, int64_t share, int64_t q_stride,
+                            const int* table, int64_t width, const int* lengths, float scale, void* o, void* work,
+                            hipStream_t stream) {
+  Args a{};
+  a.q = q;
+  a.q_stride = q_stride;
+  a.k = c.k, a.v = c.v, a.k_scale = c.k_scale, a.v_scale = c.v_scale;
+  a.k_amax = c.k_amax, a.v_amax = c.v_amax;
+  a.table = table;
+  a.lengths = lengths;
+  a.o = o;
+  a.part = (float*)work;
+  a.scale_log2 = scale * 1.44269504088896340736f;
+  a.heads = (int)c.heads;
+  a.share = (int)share;
+  a.tiles = (int)((share + kHeads - 1) / kHeads);
+  a.splits = splits_for(c, batch, share, width);
+  a.width = (int)width;
+  a.n_pages = c.n_pages;
+  a.page_size = (unsigned)c.page_size;
+  unsigned lg = 0;
+  while ((uint64_t(1) << lg) < a.page_size) ++lg;
+  a.page_shift = 31 + lg;
+  a.page_mul = (unsigned)(((uint64_t(1) << a.page_shift) + a.page_size - 1) / a.page_size);
+  const unsigned grid = (unsigned)attention_grid(c, batch, share, width);
+  const unsigned join = (unsigned)(batch * c.heads * share);
+  if (c.dim == 64) launch_dim<64>(a, c.four, !bf16, grid, join, stream);
+  else if (c.dim == 128) launch_dim<128>(a, c.four, !bf16, grid, join, stream);
+  else launch_dim<256>(a, c.four, !bf16, grid, join, stream);
+  return hipGetLastError();
+}
+
+}  // namespace lh

@@ -72,4 +72,42 @@ hipError_t launch_dequantize(const uint8_t* code, const uint8_t* fp4, const floa
                              int64_t cout, int64_t cin, bool bf16, void* Wq, float* block_amax, float gdiv,
                              hipStream_t stream);
 
+// h = round(x + r) (x without r), its RMS norm times gamma as E4M3 q and scales s: one per row, or
+// one per 128 channels (grouped).  r and h are both given or both NULL; h may be x or r.
+hipError_t launch_rms_norm(const void* x, const void* r, bool bf16, int64_t rows, int64_t cin, const void* gamma,
+                           float eps, bool grouped, void* h, uint8_t* q, float* s, hipStream_t stream);
+
+// y[t] = W_g x[t] for the rows t of each group; x_type 0 bf16, 1 fp32, 2 E4M3 with x_scales scales a
+// row; y is fp32 for fp32 x, otherwise bf16.  offsets NULL with one group.
+hipError_t launch_matvec(const void* x, int x_type, const float* x_scale, int64_t x_scales, int64_t rows, int64_t cin,
+                         int64_t cout, const int64_t* offsets, int64_t n_groups, const uint8_t* code, const uint8_t* fp4,
+                         const float* amax, float gdiv, void* y, hipStream_t stream);
+
+// Global scale of one key-value head from its amax.  A product with the rounded reciprocal, as GPU
+// tensor libraries evaluate amax / 448 and amax / 2688, so codes made there by that rule are the
+// same bits.
+__host__ __device__ inline float cache_unit(float amax, bool four) {
+  return amax * (four ? 1.0f / 2688.0f : 1.0f / 448.0f);
+}
+
+// A paged key-value cache (four: NVFP4 codes with block scales, otherwise E4M3).
+struct CacheView {
+  uint8_t *k, *v, *k_scale, *v_scale;
+  const float *k_amax, *v_amax;
+  int64_t n_pages, page_size, heads, dim;
+  bool four;
+};
+hipError_t launch_cache_write(const CacheView& c, const void* k, const void* v, bool bf16, int64_t tokens,
+                              int64_t k_stride, int64_t v_stride, const int64_t* slots, hipStream_t stream);
+hipError_t launch_cache_read(const CacheView& c, const int64_t* slots, int64_t tokens, void* k, void* v, bool bf16,
+                             hipStream_t stream);
+
+// Attention of one token per sequence; `share` query heads per key-value head.  attention_grid is
+// the launch's workgroups, attention_workspace its scratch in bytes (0: none).
+int64_t attention_grid(const CacheView& c, int64_t batch, int64_t share, int64_t width);
+int64_t attention_workspace(const CacheView& c, int64_t batch, int64_t share, int64_t width);
+hipError_t launch_attention(const CacheView& c, const void* q, bool bf16, int64_t batch, int64_t share, int64_t q_stride,
+                            const int* table, int64_t width, const int* lengths, float scale, void* o, void* work,
+                            hipStream_t stream);
+
 }  // namespace lh
