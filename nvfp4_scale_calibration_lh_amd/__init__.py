@@ -118,11 +118,12 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(device: torch.device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+def _stream(device: torch.device) -> int:
+    """Handle of torch's current stream on the device (0.1 us; the torch.cuda.Stream object costs 1.8 us a call)."""
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device.index is None else device.index)
 
 
 def _need(t: torch.Tensor, name: str, shape=None, dtype=None):
@@ -130,7 +131,7 @@ def _need(t: torch.Tensor, name: str, shape=None, dtype=None):
         raise ValueError(f"{name} must be a GPU tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
@@ -423,9 +424,18 @@ def lh_absmax(W: torch.Tensor, amax: Optional[torch.Tensor] = None) -> torch.Ten
     return amax
 
 
-def _rows_scales(t: torch.Tensor, group: int) -> Tuple[int, ...]:
-    rows, cin = t.shape
-    return (rows, 1 if group == 0 else -(-cin // group))
+def _scales(cin: int, group: int) -> int:
+    """Scales of one row of cin channels."""
+    if group == 0:
+        return 1
+    if group != 128:
+        raise ValueError("the group of a scale must be 0 (the row) or 128")
+    return (cin + 127) // 128
+
+
+# New outputs are made with empty(*sizes) or empty_like, the cheapest of torch's forms, and only outputs that the
+# caller gave are checked: at one token these calls are bound by the host.
+_empty = torch.empty
 
 
 def lh_rms_norm_quant(X: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.Tensor] = None, *,
@@ -437,24 +447,28 @@ def lh_rms_norm_quant(X: torch.Tensor, gamma: torch.Tensor, residual: Optional[t
     _need(X, "X")
     if X.dim() != 2:
         raise ValueError("X must be [rows, cin]")
-    rows, cin = X.shape
-    if group not in (0, 128):
-        raise ValueError("group must be 0 or 128")
-    _need(gamma, "gamma", (cin,), X.dtype)
+    shape, dtype, device = X.shape, X.dtype, X.device
+    rows, cin = shape
+    n = _scales(cin, group)
+    _need(gamma, "gamma", (cin,), dtype)
     if residual is not None:
-        _need(residual, "residual", X.shape, X.dtype)
+        _need(residual, "residual", shape, dtype)
         if summed is None:
             summed = torch.empty_like(X)
-    if summed is not None:
-        _need(summed, "summed", X.shape, X.dtype)
+        else:
+            _need(summed, "summed", shape, dtype)
+    elif summed is not None:
+        raise ValueError("summed is for a residual")
     if q is None:
-        q = torch.empty((rows, cin), dtype=torch.float8_e4m3fn, device=X.device)
+        q = _empty(rows, cin, dtype=torch.float8_e4m3fn, device=device)
+    else:
+        _need(q, "q", shape, torch.float8_e4m3fn)
     if scale is None:
-        scale = torch.empty(_rows_scales(X, group), dtype=torch.float32, device=X.device)
-    _need(q, "q", X.shape, torch.float8_e4m3fn)
-    _need(scale, "scale", _rows_scales(X, group), torch.float32)
-    _check(lib().lh_rms_norm_quant(_ptr(X), _ptr(residual), _dtype_code(X), rows, cin, _ptr(gamma), float(eps), group,
-                                   _ptr(summed), _ptr(q), _ptr(scale), _stream(X.device)))
+        scale = _empty(rows, n, dtype=torch.float32, device=device)
+    else:
+        _need(scale, "scale", (rows, n), torch.float32)
+    _check(lib().lh_rms_norm_quant(X.data_ptr(), _ptr(residual), _dtype_code(X), rows, cin, gamma.data_ptr(), eps, group,
+                                   _ptr(summed), q.data_ptr(), scale.data_ptr(), _stream(device)))
     return q, scale, summed
 
 
@@ -469,28 +483,30 @@ def lh_matvec(X: torch.Tensor, code: torch.Tensor, fp4: torch.Tensor, amax: torc
     if X.dim() != 2 or code.dim() != 3:
         raise ValueError("X must be [rows, cin] and code [G, cout, cin/16]")
     rows, cin = X.shape
-    offsets, G = _offsets(offsets, X)
+    device = X.device
+    G = 1
+    if offsets is not None:
+        offsets, G = _offsets(offsets, X)
     cout = code.shape[1]
     _need(code, "code", (G, cout, cin // 16), torch.uint8)
     _need(fp4, "fp4", (G, cout, cin // 2), torch.uint8)
     _need(amax, "amax", (G,), torch.float32)
-    if x_group not in (0, 128):
-        raise ValueError("x_group must be 0 or 128")
     if X.dtype == torch.float8_e4m3fn:
         dtype = LH_DTYPE_E4M3
         if x_scale is None:
             raise ValueError("x_scale is required for E4M3 rows")
-        _need(x_scale, "x_scale", _rows_scales(X, x_group), torch.float32)
+        _need(x_scale, "x_scale", (rows, _scales(cin, x_group)), torch.float32)
     else:
         dtype = _dtype_code(X)
         if x_scale is not None or x_group != 0:
             raise ValueError("x_scale and x_group are for E4M3 rows")
     y_dtype = torch.float32 if dtype == LH_DTYPE_F32 else torch.bfloat16
     if Y is None:
-        Y = torch.empty((rows, cout), dtype=y_dtype, device=X.device)
-    _need(Y, "Y", (rows, cout), y_dtype)
-    _check(lib().lh_matvec(_ptr(X), dtype, _ptr(x_scale), x_group, rows, cin, _ptr(offsets), G, cout, _ptr(code),
-                           _ptr(fp4), _ptr(amax), float(norm), _ptr(Y), _stream(X.device)))
+        Y = _empty(rows, cout, dtype=y_dtype, device=device)
+    else:
+        _need(Y, "Y", (rows, cout), y_dtype)
+    _check(lib().lh_matvec(X.data_ptr(), dtype, _ptr(x_scale), x_group, rows, cin, _ptr(offsets), G, cout, code.data_ptr(),
+                           fp4.data_ptr(), amax.data_ptr(), norm, Y.data_ptr(), _stream(device)))
     return Y
 
 
@@ -506,22 +522,24 @@ class Cache:
         if (k_scale is None) != (v_scale is None):
             raise ValueError("k_scale and v_scale must be given together")
         four = k_scale is not None
-        pages, heads, page_size, width = k.shape
-        self.head_dim = 2 * width if four else width
-        if self.head_dim % 16:
+        shape = k.shape
+        pages, heads, page_size, width = shape
+        dim = 2 * width if four else width
+        if dim % 16:
             raise ValueError("head_dim must be a multiple of 16")
         _need(k, "k", dtype=torch.uint8)
-        _need(v, "v", k.shape, torch.uint8)
+        _need(v, "v", shape, torch.uint8)
         _need(k_amax, "k_amax", (heads,), torch.float32)
         _need(v_amax, "v_amax", (heads,), torch.float32)
         if four:
-            _need(k_scale, "k_scale", (pages, heads, page_size, self.head_dim // 16), torch.uint8)
-            _need(v_scale, "v_scale", (pages, heads, page_size, self.head_dim // 16), torch.uint8)
+            scales = (pages, heads, page_size, dim // 16)
+            _need(k_scale, "k_scale", scales, torch.uint8)
+            _need(v_scale, "v_scale", scales, torch.uint8)
         self.k, self.v, self.k_amax, self.v_amax, self.k_scale, self.v_scale = k, v, k_amax, v_amax, k_scale, v_scale
-        self.n_pages, self.n_heads, self.page_size = pages, heads, page_size
-        self.struct = CacheStruct(LH_CACHE_FP4 if four else LH_CACHE_E4M3, pages, page_size, heads, self.head_dim,
-                                  k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if four else None,
-                                  v_scale.data_ptr() if four else None, k_amax.data_ptr(), v_amax.data_ptr())
+        self.n_pages, self.n_heads, self.page_size, self.head_dim = pages, heads, page_size, dim
+        self.struct = CacheStruct(LH_CACHE_FP4 if four else LH_CACHE_E4M3, pages, page_size, heads, dim, k.data_ptr(),
+                                  v.data_ptr(), _ptr(k_scale), _ptr(v_scale), k_amax.data_ptr(), v_amax.data_ptr())
+        self.ref = ctypes.byref(self.struct)
 
     @classmethod
     def empty(cls, n_pages: int, page_size: int, n_heads: int, head_dim: int, k_amax: torch.Tensor, v_amax: torch.Tensor, *,
@@ -538,23 +556,26 @@ def _heads(t: torch.Tensor, name: str, heads: int, dim: int, dtype=None, tokens=
     """Checks a [tokens, heads, dim] tensor whose tokens may lie apart; its stride between tokens."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or (tokens is not None and t.shape[0] != tokens):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({'tokens' if tokens is None else tokens}, {heads}, {dim})")
+    shape = t.shape
+    n = shape[0] if tokens is None else tokens
+    if shape != (n, heads, dim):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected ({'tokens' if tokens is None else n}, {heads}, {dim})")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    stride = t.stride()
-    if (dim > 1 and stride[2] != 1) or (heads > 1 and stride[1] != dim):
+    a, b, c = t.stride()
+    if (dim > 1 and c != 1) or (heads > 1 and b != dim):
         raise ValueError(f"{name} must hold each token's heads in one run of memory")
-    return stride[0] if t.shape[0] > 1 else max(stride[0], heads * dim)
+    return a if n > 1 else heads * dim
 
 
 def lh_cache_write(cache: Cache, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor) -> None:
     """Quantizes K, V [tokens, n_heads, head_dim] (fp32 or bf16; tokens may lie apart, as parts of a projection's
     rows do) into the cache at slots [tokens] int64 (page * page_size + place; outside the cache: skipped)."""
     ks = _heads(K, "K", cache.n_heads, cache.head_dim)
-    vs = _heads(V, "V", cache.n_heads, cache.head_dim, K.dtype, K.shape[0])
-    _need(slots, "slots", (K.shape[0],), torch.int64)
-    _check(lib().lh_cache_write(ctypes.byref(cache.struct), _ptr(K), ks, _ptr(V), vs, _dtype_code(K), K.shape[0], _ptr(slots),
+    tokens = K.shape[0]
+    vs = _heads(V, "V", cache.n_heads, cache.head_dim, K.dtype, tokens)
+    _need(slots, "slots", (tokens,), torch.int64)
+    _check(lib().lh_cache_write(cache.ref, K.data_ptr(), ks, V.data_ptr(), vs, _dtype_code(K), tokens, slots.data_ptr(),
                                 _stream(K.device)))
 
 
@@ -563,22 +584,26 @@ def lh_cache_read(cache: Cache, slots: torch.Tensor, dtype: torch.dtype = torch.
     """(K, V) [tokens, n_heads, head_dim] of dtype (bf16 or fp32): the values held at slots [tokens] int64."""
     if dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("dtype must be torch.bfloat16 or torch.float32")
+    if slots.dim() != 1:
+        raise ValueError("slots must be [tokens]")
     _need(slots, "slots", dtype=torch.int64)
-    shape = (slots.numel(), cache.n_heads, cache.head_dim)
+    tokens, heads, dim, device = slots.shape[0], cache.n_heads, cache.head_dim, slots.device
     if K is None:
-        K = torch.empty(shape, dtype=dtype, device=slots.device)
+        K = _empty(tokens, heads, dim, dtype=dtype, device=device)
+    else:
+        _need(K, "K", (tokens, heads, dim), dtype)
     if V is None:
-        V = torch.empty(shape, dtype=dtype, device=slots.device)
-    _need(K, "K", shape, dtype)
-    _need(V, "V", shape, dtype)
-    _check(lib().lh_cache_read(ctypes.byref(cache.struct), _ptr(slots), shape[0], LH_DTYPE_BF16 if dtype == torch.bfloat16 else LH_DTYPE_F32,
-                               _ptr(K), _ptr(V), _stream(slots.device)))
+        V = torch.empty_like(K)
+    else:
+        _need(V, "V", (tokens, heads, dim), dtype)
+    _check(lib().lh_cache_read(cache.ref, slots.data_ptr(), tokens, LH_DTYPE_BF16 if dtype == torch.bfloat16 else LH_DTYPE_F32,
+                               K.data_ptr(), V.data_ptr(), _stream(device)))
     return K, V
 
 
 def lh_paged_attention_workspace(cache: Cache, batch: int, n_q_heads: int, max_pages: int) -> int:
     """Bytes of workspace that lh_paged_attention needs for these sizes."""
-    return int(lib().lh_paged_attention_workspace(ctypes.byref(cache.struct), batch, n_q_heads, max_pages))
+    return int(lib().lh_paged_attention_workspace(cache.ref, batch, n_q_heads, max_pages))
 
 
 def lh_paged_attention(Q: torch.Tensor, cache: Cache, block_table: torch.Tensor, lengths: torch.Tensor, O: Optional[torch.Tensor] = None, *,
@@ -589,20 +614,23 @@ def lh_paged_attention(Q: torch.Tensor, cache: Cache, block_table: torch.Tensor,
     if block_table.dim() != 2 or Q.dim() != 3:
         raise ValueError("block_table must be [batch, max_pages] and Q [batch, n_q_heads, head_dim]")
     batch, heads, dim = Q.shape
+    device = Q.device
     stride = _heads(Q, "Q", heads, cache.head_dim)
     pages = block_table.shape[1]
     _need(block_table, "block_table", (batch, pages), torch.int32)
     _need(lengths, "lengths", (batch,), torch.int32)
     if O is None:
-        O = torch.empty((batch, heads, dim), dtype=Q.dtype, device=Q.device)
-    _need(O, "O", (batch, heads, dim), Q.dtype)
-    if workspace is None:
-        need = lh_paged_attention_workspace(cache, batch, heads, pages)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=Q.device)
+        O = _empty(batch, heads, dim, dtype=Q.dtype, device=device)
     else:
+        _need(O, "O", (batch, heads, dim), Q.dtype)
+    nbytes = 0
+    if workspace is not None:
         _need(workspace, "workspace", dtype=torch.uint8)
-    _check(lib().lh_paged_attention(ctypes.byref(cache.struct), _ptr(Q), stride, _dtype_code(Q), batch, heads, _ptr(block_table), pages,
-                                    _ptr(lengths), float(scale), _ptr(O), _ptr(workspace),
-                                    0 if workspace is None else workspace.numel(), _stream(Q.device)))
+        nbytes = workspace.numel()
+    else:
+        nbytes = lib().lh_paged_attention_workspace(cache.ref, batch, heads, pages)
+        if nbytes:
+            workspace = _empty(nbytes, dtype=torch.uint8, device=device)
+    _check(lib().lh_paged_attention(cache.ref, Q.data_ptr(), stride, _dtype_code(Q), batch, heads, block_table.data_ptr(), pages,
+                                    lengths.data_ptr(), scale, O.data_ptr(), _ptr(workspace), nbytes, _stream(device)))
     return O

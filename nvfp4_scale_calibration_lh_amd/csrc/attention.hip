@@ -38,6 +38,7 @@ constexpr int kTile = 32;                    // tokens a wave takes at a time
 constexpr int kStep = kTile * kWaves;        // tokens a workgroup takes at a time
 constexpr int kHeads = 16;                   // query heads of one workgroup
 constexpr int kMinChunk = 256;               // tokens below which a sequence is not split further
+constexpr int kWorkgroups = 2048;            // about this many in all where the sequences are long enough
 constexpr float kPBits = 10.0f;              // p = 2^(s - m + kPBits)
 
 struct Args {
@@ -394,42 +395,67 @@ __global__ __launch_bounds__(kThreads) void k_attention(const Args a) {
     for (int n = 0; n < kOut; n += 4) *(v4f*)(out + r * kOut + n) = v4f{acc[n][r], acc[n + 1][r], acc[n + 2][r], acc[n + 3][r]};
 }
 
-// Joins the partial results of a sequence's splits, in their order; one workgroup a query head, one
-// thread an element.  Sequences with one split were finished by it.
+// Joins the partial results of a sequence's splits; one workgroup a query head.  The splits' maxima
+// and sums are turned into weights in LDS, then D / 4 threads take four elements each and the
+// workgroup's kRuns such sets take the splits in turn, so that many loads are in flight; sums go in
+// a fixed order.  Sequences with one split were finished by it.
 template <bool FOUR, int D, bool F32>
-__global__ __launch_bounds__(D) void k_attention_join(const Args a) {
-  const int share = a.share;
-  const int64_t b = blockIdx.x / (unsigned)(a.heads * share);
-  const int h = blockIdx.x % (unsigned)(a.heads * share), kvh = h / share, head = h % share;
+__global__ __launch_bounds__(kThreads) void k_attention_join(const Args a) {
+  constexpr int kPart = kHeads * (D + 2), kRuns = kThreads / (D / 4);
+  __shared__ float weight[kWorkgroups];
+  __shared__ float red[2][kWaves];
+  __shared__ v4f sum[kRuns][D / 4];
+  const int64_t b = blockIdx.x / (unsigned)(a.heads * a.share);
+  const int h = blockIdx.x % (unsigned)(a.heads * a.share), kvh = h / a.share, head = h % a.share;
   const int splits = range_of(length_of(a, b), 0, a.splits).splits;
   if (splits <= 1) return;
   const int tile = head / kHeads, i = head % kHeads;
-  const float* part = a.part + (((b * a.heads + kvh) * a.tiles + tile) * (int64_t)a.splits) * (kHeads * (D + 2));
-  constexpr int kPart = kHeads * (D + 2);
+  const float* part = a.part + (((b * a.heads + kvh) * a.tiles + tile) * (int64_t)a.splits) * kPart + i;
   float top = -INFINITY;
-  for (int s = 0; s < splits; ++s) top = fmaxf(top, part[(int64_t)s * kPart + i]);
-  float l = 0.0f, o = 0.0f;
-  for (int s = 0; s < splits; ++s) {
-    const float* p = part + (int64_t)s * kPart;
-    const float f = p[i] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(p[i] - top);
-    l = fmaf(p[kHeads + i], f, l);
-    o = fmaf(p[2 * kHeads + i * D + threadIdx.x], f, o);
+  for (int s = threadIdx.x; s < splits; s += kThreads) top = fmaxf(top, weight[s] = part[(int64_t)s * kPart]);
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+  if ((threadIdx.x & 63) == 0) red[0][threadIdx.x >> 6] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) top = fmaxf(top, red[0][w]);
+  float l = 0.0f;
+  for (int s = threadIdx.x; s < splits; s += kThreads) {        // this thread's own entries
+    const float f = weight[s] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(weight[s] - top);
+    weight[s] = f;
+    l = fmaf(part[(int64_t)s * kPart + kHeads], f, l);
   }
-  o = l > 0.0f ? o * (cache_unit(a.v_amax[kvh], FOUR) / l) : 0.0f;
-  const int64_t to = (int64_t)blockIdx.x * D + threadIdx.x;
-  if constexpr (F32)
-    ((float*)a.o)[to] = o;
-  else
-    ((__bf16*)a.o)[to] = (__bf16)o;
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) l += __shfl_xor(l, o, 64);
+  if ((threadIdx.x & 63) == 0) red[1][threadIdx.x >> 6] = l;
+  __syncthreads();
+  l = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) l += red[1][w];
+  const int run = threadIdx.x / (D / 4), d4 = threadIdx.x % (D / 4);
+  const v4f* out = (const v4f*)(part - i + 2 * kHeads + i * D) + d4;
+  v4f o = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int s = run; s < splits; s += kRuns) o += weight[s] * out[(int64_t)s * (kPart / 4)];
+  sum[run][d4] = o;
+  __syncthreads();
+  if (run != 0) return;
+#pragma unroll
+  for (int r = 1; r < kRuns; ++r) o += sum[r][d4];
+  o *= l > 0.0f ? cache_unit(a.v_amax[kvh], FOUR) / l : 0.0f;
+  const int64_t to = (int64_t)blockIdx.x * D + 4 * d4;
+  if constexpr (F32) {
+    *(v4f*)((float*)a.o + to) = o;
+  } else {
+    const v2bf x = __builtin_convertvector((v2f){o[0], o[1]}, v2bf), y = __builtin_convertvector((v2f){o[2], o[3]}, v2bf);
+    *(uint2*)((unsigned short*)a.o + to) = uint2{__builtin_bit_cast(unsigned, x), __builtin_bit_cast(unsigned, y)};
+  }
 }
-
-// About this many workgroups in all where the sequences are long enough.
-constexpr int64_t kWorkgroups = 2048;
 
 int splits_for(const CacheView& c, int64_t batch, int64_t share, int64_t width) {
   const int64_t pairs = std::max<int64_t>(batch * c.heads * ((share + kHeads - 1) / kHeads), 1);
   const int64_t most = std::max<int64_t>((width * c.page_size + kMinChunk - 1) / kMinChunk, 1);
-  return (int)std::min((kWorkgroups + pairs - 1) / pairs, most);
+  return (int)std::min<int64_t>((kWorkgroups + pairs - 1) / pairs, most);
 }
 
 template <bool FOUR, int D, bool F32>
@@ -438,7 +464,7 @@ void launch_typed(const Args& a, unsigned grid, unsigned join, hipStream_t strea
     hipLaunchKernelGGL((k_attention<FOUR, D, F32, true>), dim3(grid), dim3(kThreads), 0, stream, a);
   else
     hipLaunchKernelGGL((k_attention<FOUR, D, F32, false>), dim3(grid), dim3(kThreads), 0, stream, a);
-  if (a.splits > 1) hipLaunchKernelGGL((k_attention_join<FOUR, D, F32>), dim3(join), dim3(D), 0, stream, a);
+  if (a.splits > 1) hipLaunchKernelGGL((k_attention_join<FOUR, D, F32>), dim3(join), dim3(kThreads), 0, stream, a);
 }
 
 template <int D>

@@ -117,8 +117,8 @@ lh_status lh_matvec(const void* X, lh_dtype x_dtype, const float* x_scale, int64
     return fail(LH_ERR_INVALID_ARGUMENT, eight ? "x_scale is required for E4M3 rows" : "x_scale must be NULL for rows that are not E4M3");
   if (rows == 0 || cout == 0) return ok();
   if (!X || !Y || !scale_code || !fp4 || !global_amax) return fail(LH_ERR_INVALID_ARGUMENT, "X, scale_code, fp4, global_amax and Y are required");
-  // at most one workgroup per 16 channels for every 16 rows and, with several groups, for every group with rows
-  const int64_t pieces = (rows + 15) / 16 + (n_groups > 1 ? std::min(n_groups, rows) : 0);
+  // at most one workgroup per 16 channels for every 4 rows and, with several groups, for every group with rows
+  const int64_t pieces = (rows + 3) / 4 + (n_groups > 1 ? std::min(n_groups, rows) : 0);
   if (pieces > kMaxInt / ((cout + 15) / 16)) return fail(LH_ERR_INVALID_ARGUMENT, "too many rows for one call");
   if ((st = check_aligned(X, "X")) != LH_OK) return st;
   if (reinterpret_cast<uintptr_t>(fp4) % 8 != 0) return fail(LH_ERR_INVALID_ARGUMENT, "fp4 must be 8-byte aligned");
