@@ -394,8 +394,8 @@ typedef struct {
  * slots [tokens] int64 device; a slot outside [0, n_pages * page_size) is skipped.  Slots named
  * twice in one call end with one of their tokens (either), head by head.
  * Errors: UNSUPPORTED for an unknown dtype or format; INVALID_ARGUMENT for n_pages, page_size,
- * n_heads or head_dim < 1, head_dim % 16, head_dim > 65536, over 2^31-1 heads or tokens of a page, a
- * launch of over 2^31-1 workgroups, tokens < 0, bad strides, NULL required pointers or block scales that do not fit the
+ * n_heads or head_dim < 1, head_dim % 16, head_dim > 65536, n_heads * head_dim over 2^27,
+ * page_size over 2^31-1, over 2^40 slots, a launch of over 2^31-1 workgroups, tokens < 0, bad strides, NULL required pointers or block scales that do not fit the
  * format, misaligned, non-device or mixed-device pointers.
  */
 lh_status lh_cache_write(const lh_cache* cache, const void* K, int64_t k_stride, const void* V,

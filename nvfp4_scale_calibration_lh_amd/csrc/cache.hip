@@ -10,9 +10,10 @@
 //          nibbles E2M1 nearest to |x| / s, s = fp32(v g): the input quantizer's rule on this g
 // Every rounding decision is the one of the exact quotient.
 //
-// HBM-bound: a lane owns 8 elements (16 bytes of bf16, half of a 16-element block, whose other half
-// is in the neighbouring lane), consecutive lanes own consecutive elements, and keys and values go
-// in one launch (blockIdx.y).
+// Bound by memory where the instructions allow it: a lane owns a 16-element block (32 bytes of bf16),
+// consecutive lanes own consecutive blocks, and keys and values go in one launch (blockIdx.y).  Indices
+// are split by multiplications with reciprocals from the host: with 32-bit divisions and 8 elements a
+// lane, 8191 tokens of 8 x 128 took 16 us to write, bound by instructions.
 #include "acc_stream.hpp"
 #include "lh_internal.hpp"
 
@@ -28,6 +29,20 @@ typedef unsigned v2u __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
 
+// Division by d of n < 2^31: (2 n * mul) >> 32 >> lg with mul = ceil(2^(31 + lg) / d), lg = ceil(log2 d).
+struct Divisor {
+  unsigned d, mul, lg;
+};
+__device__ inline unsigned divide(unsigned n, const Divisor& by) { return __umulhi(2 * n, by.mul) >> by.lg; }
+Divisor divisor(int64_t d) {
+  Divisor r{(unsigned)d, 0, 0};
+  while ((int64_t(1) << r.lg) < d) ++r.lg;
+  r.mul = (unsigned)(((uint64_t(1) << (31 + r.lg)) + (uint64_t)d - 1) / (uint64_t)d);
+  return r;
+}
+
+constexpr unsigned kTokens = 16;
+
 struct Args {
   const void* in[2];          // K, V (write)
   int64_t in_stride[2];       // elements between tokens
@@ -36,60 +51,79 @@ struct Args {
   uint8_t* scales[2];
   const float* amax[2];
   const int64_t* slots;
-  int64_t n_units;            // tokens * heads * dim / 8
+  int64_t tokens, n_blocks;   // n_blocks: tokens rounded up to kTokens, * heads * dim / 16
   int64_t n_slots;
-  unsigned heads, dim8, page_size;
+  unsigned heads;
+  Divisor dim16, group, page; // blocks of one head's row, of kTokens tokens, tokens of a page
 };
 
-// First element of unit (token, head, u) in the paged codes, or -1 for a slot outside the cache.
-__device__ inline int64_t place(const Args& a, int64_t token, unsigned head, unsigned u) {
+// The first block of (token, head) in the paged codes, in 16-element blocks, or -1 for a slot outside
+// the cache.
+__device__ inline int64_t place(const Args& a, int64_t token, unsigned head) {
   const int64_t slot = a.slots[token];
   if (slot < 0 || slot >= a.n_slots) return -1;
   int64_t page;
   unsigned at;
-  if (a.n_slots <= 0xFFFFFFFFll) {
-    page = (unsigned)slot / a.page_size;
-    at = (unsigned)slot % a.page_size;
+  if (a.n_slots <= 0x7FFFFFFFll) {
+    const unsigned p = divide((unsigned)slot, a.page);
+    page = p;
+    at = (unsigned)slot - p * a.page.d;
   } else {
-    page = slot / a.page_size;
-    at = (unsigned)(slot % a.page_size);
+    page = slot / a.page.d;
+    at = (unsigned)(slot - page * a.page.d);
   }
-  return (((page * a.heads + head) * a.page_size + at) * a.dim8 + u) * 8;
+  return ((page * a.heads + head) * a.page.d + at) * a.dim16.d;
 }
 
-// (token, head, unit) of linear unit i; 32-bit divisions where the total allows them.
+// (token, head, block) of linear block i: 16 tokens of a head, then the next head's, then the next 16
+// tokens, so that neighbouring slots' codes and scales, which lie side by side per head, are written
+// as whole lines by one workgroup.  A token past the last is none.
 __device__ inline void split(const Args& a, int64_t i, int64_t* token, unsigned* head, unsigned* u) {
-  const unsigned per = a.heads * a.dim8;
+  int64_t group;
   unsigned rest;
-  if (a.n_units <= 0xFFFFFFFFll) {
-    *token = (unsigned)i / per;
-    rest = (unsigned)i % per;
+  if (a.n_blocks <= 0x7FFFFFFFll) {
+    const unsigned g = divide((unsigned)i, a.group);
+    group = g;
+    rest = (unsigned)i - g * a.group.d;
   } else {
-    *token = i / per;
-    rest = (unsigned)(i % per);
+    group = i / a.group.d;
+    rest = (unsigned)(i - group * a.group.d);
   }
-  *head = rest / a.dim8;
-  *u = rest % a.dim8;
+  const unsigned row = divide(rest, a.dim16);
+  *u = rest - row * a.dim16.d;
+  *head = row / kTokens;
+  *token = group * kTokens + row % kTokens;
 }
 
-// E4M3 code of |x| / s between codes lo and lo + 1: the sign of m s - |x| (m their midpoint, 5
-// significant bits) is exact in one fma; a tie goes to the even code.
-__device__ inline unsigned e4m3_resolve(float ax, float s, unsigned lo) {
-  const float a = __builtin_amdgcn_cvt_f32_fp8((int)lo, 0), b = __builtin_amdgcn_cvt_f32_fp8((int)lo + 1, 0);
-  const float d = fmaf(0.5f * (a + b), s, -ax);
+// E4M3 code of a / (f s) between codes lo and lo + 1: the sign of f m s - a (m their midpoint, so f m
+// has at most 7 significant bits for f = 1 or 6) is exact in one fma; a tie goes to the even code.
+template <int F>
+__device__ inline unsigned e4m3_resolve(float a, float s, unsigned lo) {
+  const float x = __builtin_amdgcn_cvt_f32_fp8((int)lo, 0), y = __builtin_amdgcn_cvt_f32_fp8((int)lo + 1, 0);
+  const float d = fmaf(0.5f * F * (x + y), s, -a);
   return d < 0.0f ? lo + 1 : (d > 0.0f ? lo : lo + (lo & 1));
 }
 
-// Eight signed E4M3 bytes of x / s.  As in the fake-quant: the quotient through the 1-ulp hardware
-// reciprocal, pushed up and down by 2^-19, brackets the exact one; where the two round apart, the
-// exact decision is taken.  s outside [2^-100, 2^100] (not fast) decides on float64 quotients.
-__device__ inline v2u e4m3_codes(const float* x, float s, bool fast) {
-  v2u out = {0, 0};
+// The reciprocal and its neighbours that bracket an exact quotient: through the 1-ulp hardware
+// reciprocal (and the rounding of 6 g) a quotient is within 2^-21 of the exact one, so what it rounds
+// to when pushed up and down by 2^-19 differs only where the exact decision has to be taken.
+constexpr float kUp = 1.0000019073486328125f, kDown = 0.9999980926513671875f;
+
+// E4M3 code of a block's scale, top / (6 g); g in [2^-100, 2^100].
+__device__ inline unsigned block_code(float top, float g) {
+  const float t = top * __builtin_amdgcn_rcpf(6.0f * g);
+  const unsigned c = (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(fminf(t * kUp, 448.0f), fminf(t * kDown, 448.0f), 0, false);
+  const unsigned up = c & 255u, dn = (c >> 8) & 255u;
+  return up == dn ? up : e4m3_resolve<6>(top, g, dn);
+}
+
+// Sixteen signed E4M3 bytes of x / s.  s outside [2^-100, 2^100] (not fast) decides on float64 quotients.
+__device__ inline v4u e4m3_codes(const float* x, float s, bool fast) {
+  v4u out = {0, 0, 0, 0};
   if (fast) {
-    const float is = __builtin_amdgcn_rcpf(s);
-    const float iu = is * 1.0000019073486328125f, id = is * 0.9999980926513671875f;
+    const float is = __builtin_amdgcn_rcpf(s), iu = is * kUp, id = is * kDown;
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
+    for (int w = 0; w < 4; ++w) {
       auto pack = [&](float f) {
         float t[4];
 #pragma unroll
@@ -104,14 +138,14 @@ __device__ inline v2u e4m3_codes(const float* x, float s, bool fast) {
         for (int k = 0; k < 4; ++k) {
           const unsigned cu = (up >> (8 * k)) & 127u, cd = (dn >> (8 * k)) & 127u;
           if (cu != cd)
-            up = (up & ~(127u << (8 * k))) | (e4m3_resolve(fabsf(x[4 * w + k]), s, cd) << (8 * k));
+            up = (up & ~(127u << (8 * k))) | (e4m3_resolve<1>(fabsf(x[4 * w + k]), s, cd) << (8 * k));
         }
       }
       out[w] = up;
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < 16; ++k) {
       const float v = s > 0.0f ? stream::e4m3_nearest((double)fabsf(x[k]) / (double)s) : 0.0f;
       const unsigned c = (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(copysignf(v, x[k]), 0.0f, 0, false) & 255u;
       out[k / 4] |= c << (8 * (k % 4));
@@ -124,7 +158,7 @@ __device__ inline v2u e4m3_codes(const float* x, float s, bool fast) {
 __device__ inline unsigned e2m1_nibbles(const float* x, float s, bool fast) {
   if (fast) {
     const float is = s == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(s);
-    const float iu = is * 1.0000019073486328125f, id = is * 0.9999980926513671875f;
+    const float iu = is * kUp, id = is * kDown;
     unsigned up = 0u, dn = 0u;
     auto pack = [&](auto sel) {
       constexpr int p = decltype(sel)::value;
@@ -158,50 +192,48 @@ template <bool BF16, bool FOUR>
 __global__ __launch_bounds__(kThreads) void k_cache_write(const Args a) {
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   const int kv = blockIdx.y;
-  // units past the end repeat the last one, so that both lanes of a block exist; they store nothing
+  if (i >= a.n_blocks) return;
   int64_t token;
   unsigned head, u;
-  split(a, std::min(i, a.n_units - 1), &token, &head, &u);
-  const int64_t from = token * a.in_stride[kv] + (int64_t)(head * a.dim8 + u) * 8;
-  float x[8];
-  if constexpr (BF16) {
-    const v4u v = __builtin_nontemporal_load((const v4u*)((const unsigned short*)a.in[kv] + from));
+  split(a, i, &token, &head, &u);
+  if (token >= a.tokens) return;
+  const int64_t from = token * a.in_stride[kv] + (int64_t)(head * a.dim16.d + u) * 16;
+  float x[16];
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      x[2 * p] = stream::bf16_lo(v[p]);
-      x[2 * p + 1] = stream::bf16_hi(v[p]);
-    }
-  } else {
-    const v4u* p = (const v4u*)((const float*)a.in[kv] + from);
+  for (int h = 0; h < (BF16 ? 2 : 4); ++h) {
+    if constexpr (BF16) {
+      const v4u v = ((const v4u*)((const unsigned short*)a.in[kv] + from))[h];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const v4u v = __builtin_nontemporal_load(p + h);
+      for (int p = 0; p < 4; ++p) {
+        x[8 * h + 2 * p] = stream::bf16_lo(v[p]);
+        x[8 * h + 2 * p + 1] = stream::bf16_hi(v[p]);
+      }
+    } else {
+      const v4u v = ((const v4u*)((const float*)a.in[kv] + from))[h];
 #pragma unroll
       for (int k = 0; k < 4; ++k) x[4 * h + k] = __uint_as_float(v[k]);
     }
   }
   const float amax = a.amax[kv][head];
-  const int64_t to = place(a, token, head, u);
-  const bool live = i < a.n_units && to >= 0;
+  const int64_t row = place(a, token, head);
+  if (row < 0) return;
+  const int64_t to = row + u;
   if constexpr (FOUR) {
     const float g = cache_unit(amax, true);
     const bool fast = g >= 0x1p-100f && g <= 0x1p100f;
-    const double inv6g = 1.0 / (6.0 * (double)g);
-    unsigned m = 0;
+    float top = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(x[k]) & 0x7FFFFFFFu);
-    m = max(m, stream::dpp_u<0xB1>(m));               // the lane pair: the whole block
-    const float top = __uint_as_float(m);
-    const float v = fast ? stream::e4m3_nearest_f32(top, inv6g)
-                         : (g > 0.0f ? stream::e4m3_nearest((double)top * inv6g) : 0.0f);
-    const unsigned nib = e2m1_nibbles(x, v * g, fast);
-    if (!live) return;
-    *(unsigned*)(a.codes[kv] + to / 2) = nib;
-    if (u % 2 == 0) a.scales[kv][to / 16] = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(v, 0.0f, 0, false);
+    for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(x[k]));
+    unsigned code = 0;
+    if (fast) code = block_code(top, g);
+    else if (g > 0.0f) code = (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(stream::e4m3_nearest((double)top / (6.0 * (double)g)), 0.0f, 0, false) & 255u;
+    const float s = __builtin_amdgcn_cvt_f32_fp8((int)code, 0) * g;
+    const v2u nib = {e2m1_nibbles(x, s, fast), e2m1_nibbles(x + 8, s, fast)};
+    ((v2u*)a.codes[kv])[to] = nib;
+    a.scales[kv][to] = (uint8_t)code;
   } else {
     const float s = cache_unit(amax, false);
-    const v2u c = e4m3_codes(x, s, s >= 0x1p-100f && s <= 0x1p100f);
-    if (live) *(v2u*)(a.codes[kv] + to) = c;
+    ((v4u*)a.codes[kv])[to] = e4m3_codes(x, s, s >= 0x1p-100f && s <= 0x1p100f);
   }
 }
 
@@ -209,33 +241,38 @@ template <bool BF16, bool FOUR>
 __global__ __launch_bounds__(kThreads) void k_cache_read(const Args a) {
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   const int kv = blockIdx.y;
-  if (i >= a.n_units) return;
+  if (i >= a.n_blocks) return;
   int64_t token;
   unsigned head, u;
   split(a, i, &token, &head, &u);
-  const int64_t from = place(a, token, head, u);
-  float x[8];
-  if (from < 0) {
+  if (token >= a.tokens) return;
+  const int64_t to = (token * a.heads + head) * a.dim16.d + u;
+  const int64_t row = place(a, token, head);
+  float x[16];
+  if (row < 0) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = 0.0f;
+    for (int k = 0; k < 16; ++k) x[k] = 0.0f;
   } else if constexpr (FOUR) {
-    const unsigned nib = *(const unsigned*)(a.codes[kv] + from / 2);
-    const float s = __builtin_amdgcn_cvt_f32_fp8((int)a.scales[kv][from / 16], 0) * cache_unit(a.amax[kv][head], true);
+    const v2u nib = ((const v2u*)a.codes[kv])[row + u];
+    const float s = __builtin_amdgcn_cvt_f32_fp8((int)a.scales[kv][row + u], 0) * cache_unit(a.amax[kv][head], true);
     auto dec = [&](auto sel) {
       constexpr int p = decltype(sel)::value;
-      const v2f v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(nib, 1.0f, p);
-      x[2 * p] = v[0] * s;
-      x[2 * p + 1] = v[1] * s;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const v2f v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(nib[w], 1.0f, p);
+        x[8 * w + 2 * p] = v[0] * s;
+        x[8 * w + 2 * p + 1] = v[1] * s;
+      }
     };
     dec(std::integral_constant<int, 0>{});
     dec(std::integral_constant<int, 1>{});
     dec(std::integral_constant<int, 2>{});
     dec(std::integral_constant<int, 3>{});
   } else {
-    const v2u c = *(const v2u*)(a.codes[kv] + from);
+    const v4u c = ((const v4u*)a.codes[kv])[row + u];
     const float s = cache_unit(a.amax[kv][head], false);
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
+    for (int w = 0; w < 4; ++w) {
       const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[w], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[w], true);
       x[4 * w] = lo[0] * s;
       x[4 * w + 1] = lo[1] * s;
@@ -243,20 +280,15 @@ __global__ __launch_bounds__(kThreads) void k_cache_read(const Args a) {
       x[4 * w + 3] = hi[1] * s;
     }
   }
-  if constexpr (BF16) {
+#pragma unroll
+  for (int h = 0; h < (BF16 ? 2 : 4); ++h) {
     v4u o;
 #pragma unroll
-    for (int p = 0; p < 4; ++p)
-      o[p] = __builtin_bit_cast(unsigned, __builtin_convertvector((v2f){x[2 * p], x[2 * p + 1]}, v2bf));
-    __builtin_nontemporal_store(o, (v4u*)a.out[kv] + i);
-  } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      v4u o;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[k] = __float_as_uint(x[4 * h + k]);
-      __builtin_nontemporal_store(o, (v4u*)a.out[kv] + 2 * i + h);
+    for (int p = 0; p < 4; ++p) {
+      if constexpr (BF16) o[p] = __builtin_bit_cast(unsigned, __builtin_convertvector((v2f){x[8 * h + 2 * p], x[8 * h + 2 * p + 1]}, v2bf));
+      else o[p] = __float_as_uint(x[4 * h + p]);
     }
+    ((v4u*)a.out[kv])[to * (BF16 ? 2 : 4) + h] = o;
   }
 }
 
@@ -269,10 +301,12 @@ Args args_of(const CacheView& c, int64_t tokens, const int64_t* slots) {
   }
   a.slots = slots;
   a.heads = (unsigned)c.heads;
-  a.dim8 = (unsigned)(c.dim / 8);
-  a.page_size = (unsigned)c.page_size;
+  a.dim16 = divisor(c.dim / 16);
+  a.group = divisor(kTokens * c.heads * (c.dim / 16));
+  a.page = divisor(c.page_size);
   a.n_slots = c.n_pages * c.page_size;
-  a.n_units = tokens * c.heads * (c.dim / 8);
+  a.tokens = tokens;
+  a.n_blocks = (tokens + kTokens - 1) / kTokens * a.group.d;
   return a;
 }
 
@@ -285,7 +319,7 @@ hipError_t launch_cache_write(const CacheView& c, const void* k, const void* v, 
   a.in[1] = v;
   a.in_stride[0] = k_stride;
   a.in_stride[1] = v_stride;
-  const dim3 grid((unsigned)((a.n_units + kThreads - 1) / kThreads), 2);
+  const dim3 grid((unsigned)((a.n_blocks + kThreads - 1) / kThreads), 2);
   if (c.four) {
     if (bf16) hipLaunchKernelGGL((k_cache_write<true, true>), grid, dim3(kThreads), 0, stream, a);
     else hipLaunchKernelGGL((k_cache_write<false, true>), grid, dim3(kThreads), 0, stream, a);
@@ -301,7 +335,7 @@ hipError_t launch_cache_read(const CacheView& c, const int64_t* slots, int64_t t
   Args a = args_of(c, tokens, slots);
   a.out[0] = k;
   a.out[1] = v;
-  const dim3 grid((unsigned)((a.n_units + kThreads - 1) / kThreads), 2);
+  const dim3 grid((unsigned)((a.n_blocks + kThreads - 1) / kThreads), 2);
   if (c.four) {
     if (bf16) hipLaunchKernelGGL((k_cache_read<true, true>), grid, dim3(kThreads), 0, stream, a);
     else hipLaunchKernelGGL((k_cache_read<false, true>), grid, dim3(kThreads), 0, stream, a);

@@ -41,7 +41,7 @@ lh_status check_cache(const lh_cache* c, lh::CacheView* out) {
   if (c->n_pages < 1 || c->page_size < 1 || c->n_heads < 1 || c->head_dim < 1)
     return fail(LH_ERR_INVALID_ARGUMENT, "n_pages, page_size, n_heads and head_dim must be positive");
   if (c->head_dim % 16 || c->head_dim > 65536) return fail(LH_ERR_INVALID_ARGUMENT, "head_dim must be a multiple of 16 up to 65536 (got %lld)", (long long)c->head_dim);
-  if (c->page_size > kMaxInt || c->n_heads > kMaxInt / c->head_dim || c->n_pages > (int64_t(1) << 40) / c->page_size)
+  if (c->page_size > kMaxInt || c->n_heads > (int64_t(1) << 27) / c->head_dim || c->n_pages > (int64_t(1) << 40) / c->page_size)
     return fail(LH_ERR_INVALID_ARGUMENT, "the cache is too large");
   if (!c->k || !c->v || !c->k_amax || !c->v_amax) return fail(LH_ERR_INVALID_ARGUMENT, "k, v, k_amax and v_amax are required");
   if (four != (c->k_scale != nullptr) || four != (c->v_scale != nullptr))
@@ -57,10 +57,10 @@ lh_status check_cache(const lh_cache* c, lh::CacheView* out) {
   return LH_OK;
 }
 
-// Workgroups of the cache kernels (256 lanes of 8 elements), which must fit a launch.
+// Workgroups of the cache kernels (256 lanes of 16 elements, tokens in sixteens), which must fit a launch.
 lh_status check_tokens(const lh::CacheView& c, int64_t tokens) {
   if (tokens < 0) return fail(LH_ERR_INVALID_ARGUMENT, "tokens must be >= 0 (got %lld)", (long long)tokens);
-  if (tokens > kMaxInt * 256 / (c.heads * (c.dim / 8))) return fail(LH_ERR_INVALID_ARGUMENT, "too many tokens for one call");
+  if (tokens > kMaxInt * 256 / (c.heads * (c.dim / 16)) - 16) return fail(LH_ERR_INVALID_ARGUMENT, "too many tokens for one call");
   return LH_OK;
 }
 

@@ -33,7 +33,7 @@ typedef unsigned v4u_a1 __attribute__((ext_vector_type(4), aligned(1)));
 
 constexpr int kChunk = 128;                  // elements of k a wave takes at a time
 constexpr int kMaxWaves = 8;
-constexpr int kComputeUnits = 256, kMaxRun = 8;
+constexpr int kComputeUnits = 256;
 
 enum { kXBf16 = 0, kXF32 = 1, kXE4m3 = 2 };
 
@@ -554,8 +554,9 @@ void launch_tile(Args a, hipStream_t stream) {
   const int steps = (chunks + kMaxWaves * U - 1) / (kMaxWaves * U);
   const int waves = (chunks + U * steps - 1) / (U * steps);
   const int64_t pieces = a.n_groups == 1 ? (a.rows + rows - 1) / rows : a.rows / rows + std::min(a.n_groups, a.rows);
-  const int64_t resident = kComputeUnits * std::max((U <= 2 ? 16 : 8) / waves, 1) * (a.n_groups == 1 ? 1 : 2);
-  a.run = (int)std::min<int64_t>((pieces * tiles + resident - 1) / resident, kMaxRun);
+  const int64_t resident = kComputeUnits * std::max((U <= 2 ? 16 : 8) / waves, 1) * (a.n_groups == 1 ? 1 : 4);
+  // 8 tiles were better than 4 or 16 for one large matrix, 16 than 8 for several (the rows of x are fetched less often)
+  a.run = (int)std::min<int64_t>((pieces * tiles + resident - 1) / resident, a.n_groups == 1 ? 8 : 16);
   const dim3 grid((unsigned)(pieces * ((tiles + a.run - 1) / a.run)));
   auto go = [&](auto kernel, int together) {
     hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), (size_t)waves * MT * NT * together * 1024, stream, a);
@@ -568,28 +569,35 @@ void launch_tile(Args a, hipStream_t stream) {
   go(k_matvec<X, MT, NT, U, P, 2, false, true, 1>, 1);
 }
 
+// One group: the smallest piece that holds its rows.  Several: pieces of 4 rows where most groups have
+// one or two (rows of popular groups then share a read of the weights only through the caches: 80 rows
+// over 512 groups 35 us against 43, 320 rows 93 against 76), otherwise of 16.
 template <int X>
 void launch_x(const Args& a, hipStream_t stream) {
   const int chunks = a.cin / kChunk;
-  // rows of a piece: all of them where there is one group; with several, the smallest that holds twice the mean
-  const int64_t rows = a.n_groups == 1 ? a.rows : 2 * a.rows / std::min(a.n_groups, a.rows);
-  if (chunks <= 8 && (a.n_groups > 1 || a.rows <= 16 || chunks == 0)) {
-    launch_tile<X, 1, 1, 1, 1>(a, stream);
-  } else if (a.n_groups > 1 || a.rows <= 16) {
-    if (chunks <= 16) {
-      if (rows <= 8) launch_tile<X, 1, 1, 2, 2>(a, stream);
-      else launch_tile<X, 1, 1, 2, 1>(a, stream);
-    } else if (rows <= 4) {
-      launch_tile<X, 1, 1, 4, 4>(a, stream);
-    } else if (rows <= 8) {
-      launch_tile<X, 1, 1, 4, 2>(a, stream);
+  const bool one = a.n_groups == 1;
+  const int64_t rows = one ? a.rows : (4 * a.rows <= a.n_groups ? 4 : 16);
+  constexpr int kU = X == kXF32 ? 1 : 4;             // fp32 rows that fill the columns: 48 registers a chunk
+  if (rows > 16 && chunks > 0) {
+    if constexpr (X == kXF32) {
+      launch_tile<X, 2, 2, 1, 1>(a, stream);
     } else {
-      launch_tile<X, 1, 1, X == kXF32 ? 1 : 4, 1>(a, stream);
+      if (rows <= 32) launch_tile<X, 2, 2, 1, 1>(a, stream);
+      else launch_tile<X, 4, 2, 1, 1>(a, stream);
     }
-  } else if (a.rows <= 32 || X == kXF32) {
-    launch_tile<X, 2, 2, 1, 1>(a, stream);
-  } else if constexpr (X != kXF32) {
-    launch_tile<X, 4, 2, 1, 1>(a, stream);
+  } else if (chunks <= 8) {
+    launch_tile<X, 1, 1, 1, 1>(a, stream);
+  } else if (chunks <= 16) {
+    if (rows <= 8) launch_tile<X, 1, 1, 2, 2>(a, stream);
+    else launch_tile<X, 1, 1, 2, 1>(a, stream);
+  } else if (rows <= 4) {
+    launch_tile<X, 1, 1, 4, 4>(a, stream);
+  } else if (rows <= 8) {
+    launch_tile<X, 1, 1, 4, 2>(a, stream);
+  } else if (chunks <= 24) {                         // 6 to 8 waves where 4 chunks a wave would leave fewer
+    launch_tile<X, 1, 1, X == kXF32 ? 1 : 3, 1>(a, stream);
+  } else {
+    launch_tile<X, 1, 1, kU, 1>(a, stream);
   }
 }
 
