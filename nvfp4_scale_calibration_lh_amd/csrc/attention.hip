@@ -37,8 +37,8 @@ constexpr int kWaves = kThreads / 64;
 constexpr int kTile = 32;                    // tokens a wave takes at a time
 constexpr int kStep = kTile * kWaves;        // tokens a workgroup takes at a time
 constexpr int kHeads = 16;                   // query heads of one workgroup
-constexpr int kMinChunk = 256;               // tokens below which a sequence is not split further
-constexpr int kWorkgroups = 2048;            // about this many in all where the sequences are long enough
+constexpr int kMinChunk = 512;               // tokens below which a sequence is not split further
+constexpr int kWorkgroups = 1024;            // about this many in all where the sequences are long enough
 constexpr float kPBits = 10.0f;              // p = 2^(s - m + kPBits)
 
 struct Args {
@@ -122,17 +122,20 @@ __device__ inline int length_of(const Args& a, int64_t b) {
   return len < 0 ? 0 : (len > most ? (int)most : len);
 }
 
-// FOUR: NVFP4 codes, otherwise E4M3.  F32: fp32 q and o.  ALIGNED: 16 | page_size, so 16 tokens
-// share a page and its number is one scalar load.
-template <bool FOUR, int D, bool F32, bool ALIGNED>
-__global__ __launch_bounds__(kThreads) void k_attention(const Args a) {
+// Where the 16 tokens of a group lie: in one page (16 | page_size), in at most two (page_size > 16), the
+// page numbers being scalar loads, or anywhere, with a lookup for each token.
+enum { kOnePage = 0, kTwoPages = 1, kAnyPages = 2 };
+
+// FOUR: NVFP4 codes, otherwise E4M3.  F32: fp32 q and o.  128 registers leave room for four waves of a SIMD.
+template <bool FOUR, int D, bool F32, int PAGES>
+__global__ __launch_bounds__(kThreads, D <= 128 && !F32 ? 4 : 1) void k_attention(const Args a) {
   constexpr int kSteps = D / 32;                        // 32-deep matrix instructions of q . k
   constexpr int kOut = D / 16;                          // 16-row tiles of the output
   constexpr int kPieces = F32 ? 2 : 1;
   constexpr int kRow = FOUR ? D / 2 : D;                // code bytes of one token
   constexpr int kKB = kRow / 4, kVB = kRow / 16;        // code bytes a lane takes of a K / V token
   constexpr int kKS = D / 64;                           // K block scales of a lane
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, quarter = lane >> 4;
 
   unsigned id = blockIdx.x;
@@ -182,8 +185,8 @@ __global__ __launch_bounds__(kThreads) void k_attention(const Args a) {
     top = fmaxf(top, __shfl_xor(top, 16, 64));
     top = fmaxf(top, __shfl_xor(top, 32, 64));
     const int e = min(14 - (int)((__float_as_uint(top) >> 23) & 255u) + 127, 126);
-    const float up = ldexpf(1.0f, e);
-    factor = a.scale_log2 * cache_unit(a.k_amax[kvh], FOUR) * ldexpf(1.0f, -e);
+    const float up = copysignf(ldexpf(1.0f, e), a.scale_log2);        // so that the factor is not negative
+    factor = fabsf(a.scale_log2) * cache_unit(a.k_amax[kvh], FOUR) * ldexpf(1.0f, -e);
 #pragma unroll
     for (int s = 0; s < kSteps; ++s)
 #pragma unroll
@@ -196,29 +199,46 @@ __global__ __launch_bounds__(kThreads) void k_attention(const Args a) {
 
   const int* table = a.table + b * a.width;
   const int last = len - 1;
-  // Element offset (in tokens of one head) of a token's codes.
+  // The first row of a page in the codes, in tokens of one head; a page outside the cache is page 0.
   auto page_base = [&](int page) {
-    const int64_t p = (unsigned)page < (uint64_t)a.n_pages ? page : 0;   // a bad page reads page 0
+    const int64_t p = (unsigned)page < (uint64_t)a.n_pages ? page : 0;
     return (p * a.heads + kvh) * a.page_size;
   };
   auto divide = [&](unsigned n) { return (unsigned)(((uint64_t)n * a.page_mul) >> a.page_shift); };
-  // Row of token t (t <= last) in the codes: base16 is the tile's 16-token group (uniform).
+  // 16 tokens from t16 on: the row of the first, how many follow it up to the sequence's last token, and
+  // with two pages the first token of the second and how much further its row lies.  Tokens past the
+  // last repeat it, so every load is of the sequence.
   struct Group {
-    int64_t row;                                        // of its first token
-    int first;
+    int64_t row, jump;
+    int rest, cut;
   };
   auto group_at = [&](int t16) {
-    Group g;
-    g.first = __builtin_amdgcn_readfirstlane(min(t16, last & ~15));
-    const unsigned p = divide((unsigned)g.first);
-    g.row = page_base(table[p]) + (unsigned)(g.first - (int)(p * a.page_size));
+    const int first = __builtin_amdgcn_readfirstlane(min(t16, last & ~15));
+    const unsigned p = divide((unsigned)first);
+    const unsigned in = first - p * a.page_size;
+    Group g{page_base(table[p]) + in, 0, last - first, 16};
+    if constexpr (PAGES == kTwoPages) {
+      g.cut = min((int)(a.page_size - in), 16);
+      const bool second = g.cut <= min(g.rest, 15);      // the sequence has tokens there
+      g.jump = page_base(table[second ? p + 1 : p]) - g.row - g.cut;
+    }
     return g;
   };
-  auto row_at = [&](const Group& g, int t) -> int64_t {
+  auto row_at = [&](int t) {
     const int tc = min(t, last);
-    if constexpr (ALIGNED) return g.row + (tc - g.first);
     const unsigned p = divide((unsigned)tc);
     return page_base(table[p]) + (unsigned)(tc - (int)(p * a.page_size));
+  };
+  // Pointer to element `each` * row + `in` of a token, the j-th of group g at t16.
+  auto find = [&](const uint8_t* base, const Group& g, int t16, int j, int each, int in) {
+    if constexpr (PAGES == kAnyPages) {
+      return base + row_at(t16 + j) * each + in;
+    } else {
+      const unsigned at = min(j, g.rest);
+      const uint8_t* p = base + g.row * each;
+      if constexpr (PAGES == kTwoPages) p += (int)at >= g.cut ? g.jump * each : 0;
+      return p + (at * each + in);
+    }
   };
 
   Bytes<kKB> kc[2];
@@ -228,39 +248,43 @@ __global__ __launch_bounds__(kThreads) void k_attention(const Args a) {
   auto load_k = [&](const Group* g, int t0) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const int64_t row = row_at(g[x], t0 + 16 * x + i);
-      kc[x] = load<kKB>(a.k + row * kRow + quarter * kKB);
-      if constexpr (FOUR) ks[x] = load<kKS>(a.k_scale + row * (D / 16) + quarter * kKS);
+      kc[x] = load<kKB>(find(a.k, g[x], t0 + 16 * x, i, kRow, quarter * kKB));
+      if constexpr (FOUR) ks[x] = load<kKS>(find(a.k_scale, g[x], t0 + 16 * x, i, D / 16, quarter * kKS));
     }
   };
   auto load_v = [&](const Group* g, int t0) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int64_t row = row_at(g[e / 4], t0 + 16 * (e / 4) + 4 * quarter + e % 4);
-      vc[e] = load<kVB>(a.v + row * kRow + i * kVB);
-      if constexpr (FOUR) vs[e] = a.v_scale[row * (D / 16) + (i * kOut) / 16];
+      const int x = e / 4, j = 4 * quarter + e % 4;
+      vc[e] = load<kVB>(find(a.v, g[x], t0 + 16 * x, j, kRow, i * kVB));
+      if constexpr (FOUR) vs[e] = *find(a.v_scale, g[x], t0 + 16 * x, j, D / 16, i * kOut / 16);
     }
   };
 
   v4f acc[kOut];
 #pragma unroll
   for (int n = 0; n < kOut; ++n) acc[n] = v4f{0, 0, 0, 0};
-  float m = -INFINITY, l = 0.0f;
+  // m is within 4 of the running maximum (0 before the first tile); the sum of p is a product with ones,
+  // which also adds up the quarters' tokens
+  float m = -INFINITY;
+  v4f total = {0, 0, 0, 0};
+  h8 ones;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) ones[e] = (_Float16)1.0f;
 
   int t0 = rg.from + wave * kTile;
   Group g[2];
   if (t0 < rg.to) {
-    if constexpr (ALIGNED) g[0] = group_at(t0), g[1] = group_at(t0 + 16);
+    if constexpr (PAGES != kAnyPages) g[0] = group_at(t0), g[1] = group_at(t0 + 16);
     load_k(g, t0);
     load_v(g, t0);
   }
   for (; t0 < rg.to; t0 += kStep) {
+    // The next tile's loads are not conditional, so that the waits for this one's count exactly; past
+    // the end they repeat the sequence's last token.
     const int next = t0 + kStep;
-    const bool more = next < rg.to;
     Group gn[2];
-    if constexpr (ALIGNED) {
-      if (more) gn[0] = group_at(next), gn[1] = group_at(next + 16);
-    }
+    if constexpr (PAGES != kAnyPages) gn[0] = group_at(next), gn[1] = group_at(next + 16);
     // scores
     v4f s[2] = {v4f{0, 0, 0, 0}, v4f{0, 0, 0, 0}};
 #pragma unroll
@@ -280,34 +304,39 @@ __global__ __launch_bounds__(kThreads) void k_attention(const Args a) {
           s[x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[S][pc], s[x], 0, 0, 0);
       });
     }
-    if (more) load_k(gn, next);
-    // p, with the running maximum moved only when a score passes it by more than 4
-    float p[8], tmax = -INFINITY;
+    load_k(gn, next);
+    // p, with the running maximum moved only when a score passes it by more than 4; a repeated token
+    // has the last one's score, so it does not disturb the maximum
+    float tmax = s[0][0];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int t = t0 + 16 * (e / 4) + 4 * quarter + e % 4;
-      p[e] = t < rg.to ? s[e / 4][e % 4] * factor : -INFINITY;
-      tmax = fmaxf(tmax, p[e]);
-    }
+    for (int e = 1; e < 8; ++e) tmax = fmaxf(tmax, s[e / 4][e % 4]);
+    tmax *= factor;
     if (__any(tmax > m + 4.0f)) {
       tmax = fmaxf(tmax, __shfl_xor(tmax, 16, 64));
       tmax = fmaxf(tmax, __shfl_xor(tmax, 32, 64));
       const float mn = fmaxf(m, tmax);
-      const float alpha = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
+      const float alpha = __builtin_amdgcn_exp2f(m - mn);         // 0 at the first tile
       m = mn;
-      l *= alpha;
+      total *= alpha;
 #pragma unroll
       for (int n = 0; n < kOut; ++n) acc[n] *= alpha;
     }
-    const float shift = m == -INFINITY ? 0.0f : kPBits - m;
+    const float shift = kPBits - m;
+    float p[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(fmaf(s[e / 4][e % 4], factor, shift));
+    if (t0 + kTile > rg.to) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[e] = t0 + 16 * (e / 4) + 4 * quarter + e % 4 < rg.to ? p[e] : 0.0f;
+    }
     h8 pf[kPieces];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float f = __builtin_amdgcn_exp2f(p[e] + shift);
-      l += f;
-      pf[0][e] = (_Float16)f;
-      if constexpr (F32) pf[1][e] = (_Float16)(f - (float)pf[0][e]);
+      pf[0][e] = (_Float16)p[e];
+      if constexpr (F32) pf[1][e] = (_Float16)(p[e] - (float)pf[0][e]);
     }
+#pragma unroll
+    for (int pc = 0; pc < kPieces; ++pc) total = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, pf[pc], total, 0, 0, 0);
     // output
     each<kOut / 2>([&](auto nn) {
       constexpr int P = decltype(nn)::value;
@@ -328,11 +357,10 @@ __global__ __launch_bounds__(kThreads) void k_attention(const Args a) {
         acc[2 * P + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, pf[pc], acc[2 * P + 1], 0, 0, 0);
       }
     });
-    if (more) load_v(gn, next);
+    load_v(gn, next);
     g[0] = gn[0], g[1] = gn[1];
   }
-  l += __shfl_xor(l, 16, 64);
-  l += __shfl_xor(l, 32, 64);
+  float l = total[0];
 
   // the four waves: a common maximum, then sums of the outputs in two halving steps
   __shared__ float sh_m[kWaves][kHeads], sh_l[kWaves][kHeads];
@@ -460,10 +488,10 @@ int splits_for(const CacheView& c, int64_t batch, int64_t share, int64_t width) 
 
 template <bool FOUR, int D, bool F32>
 void launch_typed(const Args& a, unsigned grid, unsigned join, hipStream_t stream) {
-  if (a.page_size % 16 == 0)
-    hipLaunchKernelGGL((k_attention<FOUR, D, F32, true>), dim3(grid), dim3(kThreads), 0, stream, a);
-  else
-    hipLaunchKernelGGL((k_attention<FOUR, D, F32, false>), dim3(grid), dim3(kThreads), 0, stream, a);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(kThreads), 0, stream, a); };
+  if (a.page_size % 16 == 0) go(k_attention<FOUR, D, F32, kOnePage>);
+  else if (a.page_size > 16) go(k_attention<FOUR, D, F32, kTwoPages>);
+  else go(k_attention<FOUR, D, F32, kAnyPages>);
   if (a.splits > 1) hipLaunchKernelGGL((k_attention_join<FOUR, D, F32>), dim3(join), dim3(kThreads), 0, stream, a);
 }
 
