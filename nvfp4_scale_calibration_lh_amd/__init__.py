@@ -478,7 +478,8 @@ def lh_matvec(X: torch.Tensor, code: torch.Tensor, fp4: torch.Tensor, amax: torc
     """Y [rows, cout]: X [rows, cin] times the NVFP4 weights (code [G, cout, cin/16], fp4 [G, cout, cin/2], amax
     [G]) of a scale sweep with normalization `norm`, the rows of each group (offsets [G+1]) against its
     matrix.  X is fp32, bf16, or torch.float8_e4m3fn with x_scale as lh_rms_norm_quant gives it (x_group 0:
-    [rows, 1], 128: [rows, ceil(cin/128)]); Y is fp32 for fp32 X, otherwise bf16."""
+    [rows, 1], 128: [rows, ceil(cin/128)]; without effect for the other types); Y is fp32 for fp32 X,
+    otherwise bf16."""
     _need(X, "X")
     if X.dim() != 2 or code.dim() != 3:
         raise ValueError("X must be [rows, cin] and code [G, cout, cin/16]")
@@ -498,8 +499,10 @@ def lh_matvec(X: torch.Tensor, code: torch.Tensor, fp4: torch.Tensor, amax: torc
         _need(x_scale, "x_scale", (rows, _scales(cin, x_group)), torch.float32)
     else:
         dtype = _dtype_code(X)
-        if x_scale is not None or x_group != 0:
-            raise ValueError("x_scale and x_group are for E4M3 rows")
+        if x_scale is not None:
+            raise ValueError("x_scale is for E4M3 rows")
+        _scales(cin, x_group)
+        x_group = 0                        # it says how x_scale is grouped, and there is none
     y_dtype = torch.float32 if dtype == LH_DTYPE_F32 else torch.bfloat16
     if Y is None:
         Y = _empty(rows, cout, dtype=y_dtype, device=device)

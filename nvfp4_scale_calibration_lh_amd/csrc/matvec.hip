@@ -250,7 +250,7 @@ struct Weights {
 // FULL: there are whole chunks (cin >= 128).  D: steps whose weights are held or on their way (one being multiplied, D - 1 in flight): a compute
 // unit needs some 40 KB in flight to keep its share of the memory's rate.
 // KEEP: one step covers k, and a wave keeps its elements of x as matrix operands over all its tiles;
-// otherwise it loads them again at each step.  GT: tiles whose sums meet in LDS together.
+// otherwise it loads them at each step.  GT: tiles whose sums meet in LDS together.
 // Rows past the last repeat it, as do channels: a column of the products depends on its own row alone
 // and is not stored, and repeating costs no mask.  Everything that is the same over a wave (chunk,
 // tile, base addresses) is kept scalar: at few rows the kernel is close to bound by issuing instructions.
@@ -312,9 +312,13 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_matvec(const Args a) {
       if constexpr (U % 2 == 1) w[U - 1][n].code = *(const v2u_a1*)(code + c_at + (U - 1) * (kChunk / 16));
     }
   };
-  Raw<X> raw[kSets][MT];
-  float scale[kSets][MT];
-  auto load_rows = [&](int first) __attribute__((always_inline)) {
+  // x is loaded a step ahead like the weights where the registers hold both
+  constexpr bool AHEAD = !KEEP && X != kXF32 && MT <= 2;
+  constexpr int kXSlots = AHEAD ? D : 1;
+  Raw<X> raws[kXSlots][kSets][MT];
+  float scales[kXSlots][kSets][MT];
+  auto load_rows = [&](Raw<X> (&raw)[kSets][MT], float (&scale)[kSets][MT], int n) __attribute__((always_inline)) {
+    const int first = first_chunk(KEEP ? 0 : min(n, total - 1) % steps);
 #pragma unroll
     for (int u = 0; u < kSets; ++u) {
       const int c = first + u * P;
@@ -368,17 +372,20 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_matvec(const Args a) {
   const float g = a.amax[pc.group] / a.gdiv;
   extern __shared__ float red[];
   frag kept[KEEP ? kSets : 1][MT][4][kPieces];
-  if constexpr (KEEP && FULL) load_rows(first_chunk(0));
+  if constexpr (KEEP && FULL) load_rows(raws[0], scales[0], 0);
   if constexpr (FULL) {
 #pragma unroll
-    for (int d = 0; d < D - 1; ++d) load_w(w[d], d);
+    for (int d = 0; d < D - 1; ++d) {
+      if constexpr (AHEAD) load_rows(raws[d], scales[d], d);
+      load_w(w[d], d);
+    }
   }
   if constexpr (KEEP && FULL) {
 #pragma unroll
     for (int u = 0; u < kSets; ++u)
 #pragma unroll
       for (int m = 0; m < MT; ++m)
-        each<4>([&](auto st) __attribute__((always_inline)) { frag_x<X, decltype(st)::value>(raw[u][m], kept[u][m][decltype(st)::value]); });
+        each<4>([&](auto st) __attribute__((always_inline)) { frag_x<X, decltype(st)::value>(raws[0][u][m], kept[u][m][decltype(st)::value]); });
   }
   auto clear = [&](v4f (&acc)[NT][MT]) __attribute__((always_inline)) {
 #pragma unroll
@@ -389,11 +396,14 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_matvec(const Args a) {
 #pragma unroll
   for (int t = 0; t < GT; ++t) clear(accs[t]);
   // one step with the weights in slot `at`; the slot before it, just used up, is filled again
-  auto one = [&](int n, v4f (&acc)[NT][MT], Weights (&at)[U][NT], Weights (&used)[U][NT]) __attribute__((always_inline)) {
+  auto one = [&](int n, v4f (&acc)[NT][MT], Weights (&at)[U][NT], Weights (&used)[U][NT], auto slot) __attribute__((always_inline)) {
+    constexpr int kNow = AHEAD ? decltype(slot)::value : 0, kNext = (kNow + D - 1) % kXSlots;
+    auto& raw = raws[kNow];
+    auto& scale = scales[kNow];
     const int tile = tile0 + (KEEP ? n : n / steps), step = KEEP ? 0 : n % steps;
     const int mine = step * stride + wave * U, first = FULL ? first_chunk(step) : 0;
     if constexpr (FULL) {
-      if constexpr (!KEEP) load_rows(first);
+      if constexpr (!KEEP) load_rows(raws[kNext], scales[kNext], AHEAD ? n + D - 1 : n);
       load_w(used, n + D - 1);
       v4f own[P][NT][MT];                              // of each column set
 #pragma unroll
@@ -530,7 +540,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_matvec(const Args a) {
       each<D>([&](auto dd) __attribute__((always_inline)) {
         constexpr int d = decltype(dd)::value;
         if (n + d < total) {
-          one(n + d, accs[0], w[d], w[(d + D - 1) % D]);
+          one(n + d, accs[0], w[d], w[(d + D - 1) % D], dd);
           if ((n + d + 1) % steps == 0) reduce(tile0 + (n + d) / steps, 1);
         }
       });
@@ -539,7 +549,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_matvec(const Args a) {
     for (int n = 0; n < total; n += GT) {
       each<GT>([&](auto dd) __attribute__((always_inline)) {
         constexpr int d = decltype(dd)::value;
-        if (n + d < total) one(n + d, accs[d], w[d % D], w[(d + D - 1) % D]);
+        if (n + d < total) one(n + d, accs[d], w[d % D], w[(d + D - 1) % D], dd);
       });
       reduce(tile0 + n, min(GT, total - n));
     }
@@ -571,19 +581,24 @@ void launch_tile(Args a, hipStream_t stream) {
 
 // One group: the smallest piece that holds its rows.  Several: pieces of 4 rows where most groups have
 // one or two (rows of popular groups then share a read of the weights only through the caches: 80 rows
-// over 512 groups 35 us against 43, 320 rows 93 against 76), otherwise of 16.
+// over 512 groups 35 us against 43, 320 rows 93 against 76) and for fp32 rows (320 rows 155 us against
+// 205), otherwise of 16.
 template <int X>
 void launch_x(const Args& a, hipStream_t stream) {
   const int chunks = a.cin / kChunk;
   const bool one = a.n_groups == 1;
-  const int64_t rows = one ? a.rows : (4 * a.rows <= a.n_groups ? 4 : 16);
+  const int64_t rows = one ? a.rows : (4 * a.rows <= a.n_groups || X == kXF32 ? 4 : 16);
   constexpr int kU = X == kXF32 ? 1 : 4;             // fp32 rows that fill the columns: 48 registers a chunk
   if (rows > 16 && chunks > 0) {
-    if constexpr (X == kXF32) {
-      launch_tile<X, 2, 2, 1, 1>(a, stream);
-    } else {
-      if (rows <= 32) launch_tile<X, 2, 2, 1, 1>(a, stream);
-      else launch_tile<X, 4, 2, 1, 1>(a, stream);
+    // more channels at a time share the loads of x, as long as every compute unit has a workgroup
+    const int tiles = (a.cout + 15) / 16;
+    if (rows <= 32 || X == kXF32) {
+      if (tiles > 512 && X != kXF32) launch_tile<X, 2, X == kXF32 ? 2 : 3, 1, 1>(a, stream);
+      else if (tiles > 256) launch_tile<X, 2, 2, 1, 1>(a, stream);
+      else launch_tile<X, 2, 1, 1, 1>(a, stream);
+    } else if constexpr (X != kXF32) {
+      if (tiles > 256) launch_tile<X, 4, 2, 1, 1>(a, stream);
+      else launch_tile<X, 4, 1, 1, 1>(a, stream);
     }
   } else if (chunks <= 8) {
     launch_tile<X, 1, 1, 1, 1>(a, stream);

@@ -519,7 +519,7 @@ def test_refusals():
                lambda: lh.lh_matvec(x, code, fp4[:, :, :16].contiguous(), amax),
                lambda: lh.lh_matvec(x.to(torch.float8_e4m3fn), code, fp4, amax),
                lambda: lh.lh_matvec(x, code, fp4, amax, x_scale=torch.ones(2, 1, device=DEV)),
-               lambda: lh.lh_matvec(x, code, fp4, amax, x_group=128),
+               lambda: lh.lh_matvec(x, code, fp4, amax, x_group=64),
                lambda: lh.lh_cache_write(cache, heads, heads.bfloat16(), slots),
                lambda: lh.lh_cache_write(cache, heads[:, :1], heads, slots),
                lambda: lh.lh_cache_write(cache, heads.transpose(1, 2), heads, slots),
