@@ -9,6 +9,11 @@
 // (k in any order, as long as both operands have the same).  The waves of a workgroup take 128
 // elements of k in turn and add their sums in LDS in a fixed order.
 //
+// 12288x4096: one bf16 row 10 us, sixteen E4M3 rows 11 us, 64 bf16 rows 44 us; 4096x12288 with five fp32
+// rows 16.5 us; 2048x2048 with one row 3.8 us; 320 bf16 rows over 512 experts of 1280x2560, 135 of them
+// hit, 76 us (242 MB, 3.2 TB/s); 98304x4096 with one row 50 us (4.5 TB/s).  Reading the weights alone in
+// this pattern takes 5.5 us at 12288x4096 (4.6 TB/s).
+//
 // E2M1 * E4M3 has at most 6 significant bits, so it is exact in bf16 (bf16 and fp32 x) and, its
 // range being [2^-10, 2688], in fp16 (E4M3 x, also exact in fp16).  fp32 x is split exactly into
 // three bf16 pieces.  Every product is exact; sums are fp32.
@@ -576,7 +581,8 @@ void launch_tile(Args a, hipStream_t stream) {
   if constexpr (MT == 1 && (X != kXF32 || U / P == 1))
     if (steps == 1)
       return a.run > 1 ? go(k_matvec<X, MT, NT, U, P, 2, true, true, kTogether>, kTogether) : go(k_matvec<X, MT, NT, U, P, 1, true, true, 1>, 1);
-  go(k_matvec<X, MT, NT, U, P, 2, false, true, 1>, 1);
+  // (of one row tile, only what launch_x sends more than one step of)
+  if constexpr (MT > 1 || U == 4 || (X == kXF32 && (U == 1 || U / P > 1))) go(k_matvec<X, MT, NT, U, P, 2, false, true, 1>, 1);
 }
 
 // One group: the smallest piece that holds its rows.  Several: pieces of 4 rows where most groups have
