@@ -6,8 +6,8 @@
 // Bound by reading the weights once (0.5625 bytes each), so the layout is the one they are stored
 // in: a lane reads 16 bytes (32 elements, two blocks) of one output channel, 16 channels by 128
 // elements a wave, as the A operand of 16x16x32 matrix instructions whose columns are the rows of x
-// (k in any order, as long as both operands have the same).  The waves of a workgroup take 128
-// elements of k in turn and add their sums in LDS in a fixed order.
+// (k in any order, as long as both operands have the same).  The waves of a workgroup share k among
+// them and add their sums in LDS in a fixed order.
 //
 // 12288x4096: one bf16 row 10 us, sixteen E4M3 rows 11 us, 64 bf16 rows 44 us; 4096x12288 with five fp32
 // rows 16.5 us; 2048x2048 with one row 3.8 us; 320 bf16 rows over 512 experts of 1280x2560, 135 of them
@@ -15,8 +15,8 @@
 // this pattern takes 5.5 us at 12288x4096 (4.6 TB/s).
 //
 // E2M1 * E4M3 has at most 6 significant bits, so it is exact in bf16 (bf16 and fp32 x) and, its
-// range being [2^-10, 2688], in fp16 (E4M3 x, also exact in fp16).  fp32 x is split exactly into
-// three bf16 pieces.  Every product is exact; sums are fp32.
+// range being [2^-10, 2688], in fp16 (E4M3 x, also exact in fp16).  fp32 x is split into three
+// bf16 pieces, exactly where the last is a normal number (|x| above 2^-109).  Every product is exact; sums are fp32.
 #include "lh_internal.hpp"
 
 #include <algorithm>
