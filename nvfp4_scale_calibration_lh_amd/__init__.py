@@ -127,14 +127,15 @@ def _stream(device: torch.device) -> int:
 
 
 def _need(t: torch.Tensor, name: str, shape=None, dtype=None):
+    if t.is_cuda and (shape is None or t.shape == shape) and (dtype is None or t.dtype is dtype) and t.is_contiguous():
+        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
 
 
 def _offsets(offsets: Optional[torch.Tensor], X: torch.Tensor):

@@ -494,23 +494,19 @@ int splits_for(const CacheView& c, int64_t batch, int64_t share, int64_t width) 
 }
 
 template <bool FOUR, int D, bool F32>
-void launch_typed(const Args& a, unsigned grid, unsigned join, hipStream_t stream) {
-  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(kThreads), 0, stream, a); };
-  if (a.page_size % 16 == 0) go(k_attention<FOUR, D, F32, kOnePage>);
-  else if (a.page_size > 16) go(k_attention<FOUR, D, F32, kTwoPages>);
-  else go(k_attention<FOUR, D, F32, kAnyPages>);
-  if (a.splits > 1) hipLaunchKernelGGL((k_attention_join<FOUR, D, F32>), dim3(join), dim3(kThreads), 0, stream, a);
+hipError_t launch_typed(const Args& a, unsigned grid, unsigned join, hipStream_t stream) {
+  const auto kernel = a.page_size % 16 == 0 ? k_attention<FOUR, D, F32, kOnePage>
+                      : a.page_size > 16    ? k_attention<FOUR, D, F32, kTwoPages>
+                                            : k_attention<FOUR, D, F32, kAnyPages>;
+  const hipError_t e = launch_kernel(kernel, dim3(grid), dim3(kThreads), 0, stream, a);
+  if (e != hipSuccess || a.splits <= 1) return e;
+  return launch_kernel(k_attention_join<FOUR, D, F32>, dim3(join), dim3(kThreads), 0, stream, a);
 }
 
 template <int D>
-void launch_dim(const Args& a, bool four, bool f32, unsigned grid, unsigned join, hipStream_t stream) {
-  if (four) {
-    if (f32) launch_typed<true, D, true>(a, grid, join, stream);
-    else launch_typed<true, D, false>(a, grid, join, stream);
-  } else {
-    if (f32) launch_typed<false, D, true>(a, grid, join, stream);
-    else launch_typed<false, D, false>(a, grid, join, stream);
-  }
+hipError_t launch_dim(const Args& a, bool four, bool f32, unsigned grid, unsigned join, hipStream_t stream) {
+  if (four) return f32 ? launch_typed<true, D, true>(a, grid, join, stream) : launch_typed<true, D, false>(a, grid, join, stream);
+  return f32 ? launch_typed<false, D, true>(a, grid, join, stream) : launch_typed<false, D, false>(a, grid, join, stream);
 }
 
 }  // namespace
@@ -550,10 +546,9 @@ hipError_t launch_attention(const CacheView& c, const void* q, bool bf16, int64_
   a.page_mul = (unsigned)(((uint64_t(1) << a.page_shift) + a.page_size - 1) / a.page_size);
   const unsigned grid = (unsigned)attention_grid(c, batch, share, width);
   const unsigned join = (unsigned)(batch * c.heads * share);
-  if (c.dim == 64) launch_dim<64>(a, c.four, !bf16, grid, join, stream);
-  else if (c.dim == 128) launch_dim<128>(a, c.four, !bf16, grid, join, stream);
-  else launch_dim<256>(a, c.four, !bf16, grid, join, stream);
-  return hipGetLastError();
+  if (c.dim == 64) return launch_dim<64>(a, c.four, !bf16, grid, join, stream);
+  if (c.dim == 128) return launch_dim<128>(a, c.four, !bf16, grid, join, stream);
+  return launch_dim<256>(a, c.four, !bf16, grid, join, stream);
 }
 
 }  // namespace lh

@@ -321,14 +321,9 @@ hipError_t launch_cache_write(const CacheView& c, const void* k, const void* v, 
   a.in_stride[0] = k_stride;
   a.in_stride[1] = v_stride;
   const dim3 grid((unsigned)((a.n_blocks + kThreads - 1) / kThreads), 2);
-  if (c.four) {
-    if (bf16) hipLaunchKernelGGL((k_cache_write<true, true>), grid, dim3(kThreads), 0, stream, a);
-    else hipLaunchKernelGGL((k_cache_write<false, true>), grid, dim3(kThreads), 0, stream, a);
-  } else {
-    if (bf16) hipLaunchKernelGGL((k_cache_write<true, false>), grid, dim3(kThreads), 0, stream, a);
-    else hipLaunchKernelGGL((k_cache_write<false, false>), grid, dim3(kThreads), 0, stream, a);
-  }
-  return hipGetLastError();
+  if (c.four)
+    return launch_kernel(bf16 ? k_cache_write<true, true> : k_cache_write<false, true>, grid, dim3(kThreads), 0, stream, a);
+  return launch_kernel(bf16 ? k_cache_write<true, false> : k_cache_write<false, false>, grid, dim3(kThreads), 0, stream, a);
 }
 
 hipError_t launch_cache_read(const CacheView& c, const int64_t* slots, int64_t tokens, void* k, void* v, bool bf16,
@@ -337,14 +332,9 @@ hipError_t launch_cache_read(const CacheView& c, const int64_t* slots, int64_t t
   a.out[0] = k;
   a.out[1] = v;
   const dim3 grid((unsigned)((a.n_blocks + kThreads - 1) / kThreads), 2);
-  if (c.four) {
-    if (bf16) hipLaunchKernelGGL((k_cache_read<true, true>), grid, dim3(kThreads), 0, stream, a);
-    else hipLaunchKernelGGL((k_cache_read<false, true>), grid, dim3(kThreads), 0, stream, a);
-  } else {
-    if (bf16) hipLaunchKernelGGL((k_cache_read<true, false>), grid, dim3(kThreads), 0, stream, a);
-    else hipLaunchKernelGGL((k_cache_read<false, false>), grid, dim3(kThreads), 0, stream, a);
-  }
-  return hipGetLastError();
+  if (c.four)
+    return launch_kernel(bf16 ? k_cache_read<true, true> : k_cache_read<false, true>, grid, dim3(kThreads), 0, stream, a);
+  return launch_kernel(bf16 ? k_cache_read<true, false> : k_cache_read<false, false>, grid, dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace lh

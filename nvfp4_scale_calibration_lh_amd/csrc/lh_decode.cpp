@@ -19,12 +19,14 @@ namespace {
 constexpr int64_t kMaxInt = 2147483647LL;
 constexpr int64_t kMaxCin = int64_t(1) << 24;
 
-bool e4m3_value(float x) {               // one of the 126 positive finite values
-  for (int k = 1; k <= 126; ++k) {
-    const int e = k >> 3, m = k & 7;
-    if (x == (e == 0 ? std::ldexp((float)m, -9) : std::ldexp(1.0f + (float)m / 8.0f, e - 7))) return true;
-  }
-  return false;
+// One of the 126 positive finite values: 3 bits below the leading one, or a multiple of 2^-9 (a search
+// through them took 0.3 us a call).
+bool e4m3_value(float x) {
+  if (!(x >= 0x1p-9f && x <= 448.0f)) return false;
+  if (x < 0x1p-6f) return x * 512.0f == std::floor(x * 512.0f);
+  uint32_t bits;
+  std::memcpy(&bits, &x, sizeof bits);
+  return (bits & 0xFFFFF) == 0;
 }
 
 lh_status check_rows(int64_t rows, int64_t cin) {

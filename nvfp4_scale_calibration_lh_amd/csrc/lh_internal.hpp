@@ -8,6 +8,14 @@
 
 namespace lh {
 
+// kernel(args) on the stream and its launch status.  hipLaunchKernel itself: the <<<>>> form passes
+// the grid through two more runtime calls (2.25 us of the host against 2.45).
+template <class A>
+inline hipError_t launch_kernel(void (*kernel)(A), dim3 grid, dim3 block, size_t lds, hipStream_t stream, A args) {
+  void* list[] = {&args};
+  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, list, lds, stream);
+}
+
 // Scratch of one launch_accumulate call: a work area (partial sums of row ranges that are added
 // across workgroups) and arrival counters.  The counters must be
 // zero when a call starts and are zero again when it ends.  launch_accumulate checks the sizes it

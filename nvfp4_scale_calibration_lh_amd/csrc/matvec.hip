@@ -563,7 +563,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_matvec(const Args a) {
 
 // Tiles of one workgroup: as many as leave about the waves that fit a compute unit's registers.
 template <int X, int MT, int NT, int U, int P>
-void launch_tile(Args a, hipStream_t stream) {
+hipError_t launch_tile(Args a, hipStream_t stream) {
   constexpr int kTogether = 4;
   const int rows = 16 * MT / P, chunks = std::max(a.cin / kChunk, 1), tiles = (a.cout + 16 * NT - 1) / (16 * NT);
   const int steps = (chunks + kMaxWaves * U - 1) / (kMaxWaves * U);
@@ -574,7 +574,7 @@ void launch_tile(Args a, hipStream_t stream) {
   a.run = (int)std::min<int64_t>((pieces * tiles + resident - 1) / resident, a.n_groups == 1 ? 8 : 16);
   const dim3 grid((unsigned)(pieces * ((tiles + a.run - 1) / a.run)));
   auto go = [&](auto kernel, int together) {
-    hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), (size_t)waves * MT * NT * together * 1024, stream, a);
+    return launch_kernel(kernel, grid, dim3(64 * waves), (size_t)waves * MT * NT * together * 1024, stream, a);
   };
   if constexpr (MT == 1 && NT == 1 && U == 1)
     if (a.cin < kChunk) return go(k_matvec<X, 1, 1, 1, 1, 1, true, false, 1>, 1);
@@ -582,7 +582,8 @@ void launch_tile(Args a, hipStream_t stream) {
     if (steps == 1)
       return a.run > 1 ? go(k_matvec<X, MT, NT, U, P, 2, true, true, kTogether>, kTogether) : go(k_matvec<X, MT, NT, U, P, 1, true, true, 1>, 1);
   // (of one row tile, only what launch_x sends more than one step of)
-  if constexpr (MT > 1 || U == 4 || (X == kXF32 && (U == 1 || U / P > 1))) go(k_matvec<X, MT, NT, U, P, 2, false, true, 1>, 1);
+  if constexpr (MT > 1 || U == 4 || (X == kXF32 && (U == 1 || U / P > 1))) return go(k_matvec<X, MT, NT, U, P, 2, false, true, 1>, 1);
+  return hipErrorInvalidValue;
 }
 
 // One group: the smallest piece that holds its rows.  Several: pieces of 4 rows where most groups have
@@ -590,7 +591,7 @@ void launch_tile(Args a, hipStream_t stream) {
 // over 512 groups 35 us against 43, 320 rows 93 against 76) and for fp32 rows (320 rows 155 us against
 // 205), otherwise of 16.
 template <int X>
-void launch_x(const Args& a, hipStream_t stream) {
+hipError_t launch_x(const Args& a, hipStream_t stream) {
   const int chunks = a.cin / kChunk;
   const bool one = a.n_groups == 1;
   const int64_t rows = one ? a.rows : (4 * a.rows <= a.n_groups || X == kXF32 ? 4 : 16);
@@ -599,27 +600,17 @@ void launch_x(const Args& a, hipStream_t stream) {
     // more channels at a time share the loads of x, as long as every compute unit has a workgroup
     const int tiles = (a.cout + 15) / 16;
     if (rows <= 32 || X == kXF32) {
-      if (tiles > 512 && X != kXF32) launch_tile<X, 2, X == kXF32 ? 2 : 3, 1, 1>(a, stream);
-      else if (tiles > 256) launch_tile<X, 2, 2, 1, 1>(a, stream);
-      else launch_tile<X, 2, 1, 1, 1>(a, stream);
-    } else if constexpr (X != kXF32) {
-      if (tiles > 256) launch_tile<X, 4, 2, 1, 1>(a, stream);
-      else launch_tile<X, 4, 1, 1, 1>(a, stream);
+      if (tiles > 512 && X != kXF32) return launch_tile<X, 2, X == kXF32 ? 2 : 3, 1, 1>(a, stream);
+      return tiles > 256 ? launch_tile<X, 2, 2, 1, 1>(a, stream) : launch_tile<X, 2, 1, 1, 1>(a, stream);
     }
-  } else if (chunks <= 8) {
-    launch_tile<X, 1, 1, 1, 1>(a, stream);
-  } else if (chunks <= 16) {
-    if (rows <= 8) launch_tile<X, 1, 1, 2, 2>(a, stream);
-    else launch_tile<X, 1, 1, 2, 1>(a, stream);
-  } else if (rows <= 4) {
-    launch_tile<X, 1, 1, 4, 4>(a, stream);
-  } else if (rows <= 8) {
-    launch_tile<X, 1, 1, 4, 2>(a, stream);
-  } else if (chunks <= 24) {                         // 6 to 8 waves where 4 chunks a wave would leave fewer
-    launch_tile<X, 1, 1, X == kXF32 ? 1 : 3, 1>(a, stream);
-  } else {
-    launch_tile<X, 1, 1, kU, 1>(a, stream);
+    if constexpr (X != kXF32) return tiles > 256 ? launch_tile<X, 4, 2, 1, 1>(a, stream) : launch_tile<X, 4, 1, 1, 1>(a, stream);
   }
+  if (chunks <= 8) return launch_tile<X, 1, 1, 1, 1>(a, stream);
+  if (chunks <= 16) return rows <= 8 ? launch_tile<X, 1, 1, 2, 2>(a, stream) : launch_tile<X, 1, 1, 2, 1>(a, stream);
+  if (rows <= 4) return launch_tile<X, 1, 1, 4, 4>(a, stream);
+  if (rows <= 8) return launch_tile<X, 1, 1, 4, 2>(a, stream);
+  // 6 to 8 waves where 4 chunks a wave would leave fewer
+  return chunks <= 24 ? launch_tile<X, 1, 1, X == kXF32 ? 1 : 3, 1>(a, stream) : launch_tile<X, 1, 1, kU, 1>(a, stream);
 }
 
 }  // namespace
@@ -641,10 +632,8 @@ hipError_t launch_matvec(const void* x, int x_type, const float* x_scale, int64_
   a.cin = (int)cin;
   a.x_scales = (int)x_scales;
   a.gdiv = gdiv;
-  if (x_type == kXBf16) launch_x<kXBf16>(a, stream);
-  else if (x_type == kXF32) launch_x<kXF32>(a, stream);
-  else launch_x<kXE4m3>(a, stream);
-  return hipGetLastError();
+  if (x_type == kXBf16) return launch_x<kXBf16>(a, stream);
+  return x_type == kXF32 ? launch_x<kXF32>(a, stream) : launch_x<kXE4m3>(a, stream);
 }
 
 }  // namespace lh

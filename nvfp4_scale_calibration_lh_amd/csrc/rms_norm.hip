@@ -270,18 +270,18 @@ __global__ __launch_bounds__(1024) void k_rms_norm_long(const Args a) {
 }
 
 template <bool BF16, bool RES>
-void launch_typed(const Args& a, hipStream_t stream) {
+hipError_t launch_typed(const Args& a, hipStream_t stream) {
   const int per = (a.units + kThreads - 1) / kThreads;
   auto go = [&](auto kernel, int rows, int threads) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)((a.rows + rows - 1) / rows)), dim3(threads), 0, stream, a);
+    return launch_kernel(kernel, dim3((unsigned)((a.rows + rows - 1) / rows)), dim3(threads), 0, stream, a);
   };
-  if (a.units <= 64) go(k_rms_norm<BF16, RES, 64, 1>, kThreads / 64, kThreads);
-  else if (a.units <= 128) go(k_rms_norm<BF16, RES, 64, 2>, kThreads / 64, kThreads);
-  else if (per <= 1) go(k_rms_norm<BF16, RES, kThreads, 1>, 1, kThreads);
-  else if (per <= 2) go(k_rms_norm<BF16, RES, kThreads, 2>, 1, kThreads);
-  else if (per <= 4) go(k_rms_norm<BF16, RES, kThreads, 4>, 1, kThreads);
-  else if (per <= 8) go(k_rms_norm<BF16, RES, kThreads, 8>, 1, kThreads);
-  else go(k_rms_norm_long<BF16, RES>, 1, 1024);
+  if (a.units <= 64) return go(k_rms_norm<BF16, RES, 64, 1>, kThreads / 64, kThreads);
+  if (a.units <= 128) return go(k_rms_norm<BF16, RES, 64, 2>, kThreads / 64, kThreads);
+  if (per <= 1) return go(k_rms_norm<BF16, RES, kThreads, 1>, 1, kThreads);
+  if (per <= 2) return go(k_rms_norm<BF16, RES, kThreads, 2>, 1, kThreads);
+  if (per <= 4) return go(k_rms_norm<BF16, RES, kThreads, 4>, 1, kThreads);
+  if (per <= 8) return go(k_rms_norm<BF16, RES, kThreads, 8>, 1, kThreads);
+  return go(k_rms_norm_long<BF16, RES>, 1, 1024);
 }
 
 }  // namespace
@@ -300,14 +300,8 @@ hipError_t launch_rms_norm(const void* x, const void* r, bool bf16, int64_t rows
   a.scales = grouped ? (int)((cin + kGroup - 1) / kGroup) : 1;
   a.eps = eps;
   a.inv_cin = 1.0f / (float)cin;
-  if (bf16) {
-    if (r) launch_typed<true, true>(a, stream);
-    else launch_typed<true, false>(a, stream);
-  } else {
-    if (r) launch_typed<false, true>(a, stream);
-    else launch_typed<false, false>(a, stream);
-  }
-  return hipGetLastError();
+  if (bf16) return r ? launch_typed<true, true>(a, stream) : launch_typed<true, false>(a, stream);
+  return r ? launch_typed<false, true>(a, stream) : launch_typed<false, false>(a, stream);
 }
 
 }  // namespace lh

@@ -44,3 +44,16 @@ def test_binding_refuses_cpu_tensors():
                lambda: lh.Cache.empty(2, 4, 1, 64, torch.ones(1), torch.ones(1), four_bit=True)):
         with pytest.raises(ValueError):
             fn()
+
+
+def test_scale_norm_is_any_positive_e4m3_value_and_nothing_else():
+    def status(norm):                            # no rows: the checks alone
+        return lh.lib().lh_matvec(None, lh.LH_DTYPE_BF16, None, 0, 0, 64, None, 1, 16, None, None, None, norm, None, None)
+    values = torch.arange(1, 127, dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+    inf = torch.tensor(float("inf"))
+    for v in values.tolist():
+        assert status(v) == lh.LH_OK, v
+        for other in (torch.nextafter(torch.tensor(v), inf), torch.nextafter(torch.tensor(v), -inf)):
+            assert status(float(other)) == lh.LH_ERR_INVALID_ARGUMENT, float(other)
+    for v in (0.0, -0.0, -448.0, 2.0 ** -10, 3 * 2.0 ** -10, 480.0, 512.0, 1e-45, 3e38, float("inf"), -float("inf"), float("nan")):
+        assert status(v) == lh.LH_ERR_INVALID_ARGUMENT, v
