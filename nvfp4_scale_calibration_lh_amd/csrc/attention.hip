@@ -42,9 +42,7 @@ constexpr int kHeads = 16;                   // query heads of one workgroup
 // Tokens below which a sequence is not split further: up to 512 one launch does (64 sequences of up to
 // 500 tokens 12.3 us against 19.1 with 256, 301 tokens 7.0 against 9.7)
 constexpr int kMinChunk = 512;
-// About this many workgroups in all where the sequences are long enough (2048: one of 16 x 16000 tokens
-// 34 us against 28, 48 of up to 8191 67 against 69)
-constexpr int kWorkgroups = 1024;
+constexpr int kResident = 1024;              // workgroups that the registers let run at a time
 constexpr float kPBits = 10.0f;              // p = 2^(s - m + kPBits)
 
 struct Args {
@@ -55,9 +53,11 @@ struct Args {
   const int* table;
   const int* lengths;
   void* o;
-  float* part;                               // [pair][split][2 + D][16]: m, l, then the outputs
+  float* part;                               // [unit][pair][2 + D][16]: m, l, then the outputs
   float scale_log2;                          // softmax scale * log2(e)
-  int heads, share, tiles, splits, width;
+  int heads, share, tiles, batch, width;
+  int splits;                                // parts of each sequence; 0: all are cut to one length, by
+  unsigned budget_mul;                       // 2^32 / budget rounded up
   int64_t n_pages;
   unsigned page_size, page_mul, page_shift;  // n / page_size = n * page_mul >> page_shift, n < 2^31
 };
@@ -113,19 +113,61 @@ __device__ inline h2 scale_of(const Bytes<B>& b) {
   return h2{s[I & 1], s[I & 1]};
 }
 
-// The tokens [from, to) of one sequence that one split takes, and how many splits it has.
-struct Range {
-  int from, to, splits;
-};
-__device__ inline Range range_of(int len, int split, int splits) {
-  int chunk = (len + splits - 1) / splits;
-  chunk = max((chunk + kStep - 1) / kStep * kStep, kMinChunk);
-  return {min(split * chunk, len), min(split * chunk + chunk, len), (len + chunk - 1) / chunk};
-}
 __device__ inline int length_of(const Args& a, int64_t b) {
   const int64_t most = (int64_t)a.width * a.page_size;
   const int len = a.lengths[b];
   return len < 0 ? 0 : (len > most ? (int)most : len);
+}
+
+// Inclusive sum over the lanes up to this one: within rows of 16, then the rows before.
+__device__ inline unsigned scan(unsigned v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);     // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);     // lane 15 of rows 0, 2 to rows 1, 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);     // lane 31 to rows 2, 3
+  return v;
+}
+
+// One unit of work: the tokens [from, to) of sequence b, one of its `splits` parts, whose first is unit `base`.
+struct Unit {
+  int b, len, from, to, splits, base;
+};
+
+// The unit-th part over all sequences in order, or sequence b if b >= 0; splits is 0 past the last part.
+// Up to 64 sequences are cut to parts of one length, from the tokens of all of them, so that uneven
+// sequences keep the compute units evenly busy (48 of up to 8191 tokens in NVFP4 62 us, in E4M3 92, against
+// 70 and 102 where each was cut into as many parts as the others); every wave finds its part by a
+// scan over its lanes.  More sequences get the same number of parts each: they even out, and a scan
+// would be several dependent loads (300 sequences of one head 57 us with one, 53 without).
+__device__ inline Unit find_unit(const Args& a, int unit, int b) {
+  if (a.splits > 0) {
+    const int seq = b >= 0 ? b : unit / a.splits, base = seq * a.splits, len = length_of(a, seq);
+    const int part = max(((len + a.splits - 1) / a.splits + kStep - 1) / kStep * kStep, kMinChunk);
+    const int splits = max((len + part - 1) / part, 1), at = unit - base;
+    if (b < 0 && at >= splits) return {0, 0, 0, 0, 0, 0};
+    const int64_t from = (int64_t)at * part, to = from + part;
+    return {seq, len, (int)min(from, (int64_t)len), (int)min(to, (int64_t)len), splits, base};
+  }
+  const int lane = threadIdx.x & 63;
+  const int len = lane < a.batch ? length_of(a, lane) : 0;
+  const unsigned steps = ((unsigned)len + kStep - 1) / kStep;
+  const unsigned all = (unsigned)__builtin_amdgcn_readlane((int)scan(steps), 63);
+  // steps of a part: all / budget rounded up (or one more), so that the parts are at most budget and one a sequence
+  const unsigned most = max(__umulhi(all - 1, a.budget_mul) + 1, (unsigned)(kMinChunk / kStep));
+  // steps / most rounded up: the quotient is at most budget < 2^12, so the product is less than one away from it
+  unsigned n = (unsigned)((float)steps * __builtin_amdgcn_rcpf((float)most));
+  const int left = (int)(steps - n * most);
+  n = n + (left > 0) + (left > 0 && (unsigned)left > most);
+  n = lane < a.batch ? max(n, 1u) : 0;
+  const unsigned upto = scan(n);
+  if (b < 0 && unit >= __builtin_amdgcn_readlane((int)upto, 63)) return {0, 0, 0, 0, 0, 0};
+  const int owner = b >= 0 ? b : __ffsll((unsigned long long)__ballot((unsigned)unit < upto)) - 1;
+  const int seq_len = __builtin_amdgcn_readlane(len, owner), splits = __builtin_amdgcn_readlane((int)n, owner);
+  const int base = __builtin_amdgcn_readlane((int)upto, owner) - splits;
+  const int64_t from = (int64_t)(unit - base) * most * kStep, to = from + (int64_t)most * kStep;
+  return {owner, seq_len, (int)min(from, (int64_t)seq_len), (int)min(to, (int64_t)seq_len), splits, base};
 }
 
 // Where the 16 tokens of a group lie: in one page (16 | page_size), in at most two (page_size > 16), the
@@ -145,16 +187,13 @@ __global__ __launch_bounds__(kThreads, D <= 128 && !F32 ? 4 : 1) void k_attentio
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, quarter = lane >> 4;
 
-  unsigned id = blockIdx.x;
-  const int split = id % a.splits;
-  id /= a.splits;
-  const int tile = id % a.tiles;
-  id /= a.tiles;
-  const int kvh = id % a.heads;
-  const int64_t b = id / a.heads;
-  const int len = length_of(a, b);
-  const Range rg = range_of(len, split, a.splits);
-  if (split > 0 && rg.from >= rg.to) return;            // split 0 of an empty sequence writes zeros
+  // heads fastest: a compute die has the same share of every sequence
+  const unsigned pairs = (unsigned)(a.heads * a.tiles), unit = blockIdx.x / pairs, pair = blockIdx.x % pairs;
+  const int kvh = pair % a.heads, tile = pair / a.heads;
+  const Unit rg = find_unit(a, (int)unit, -1);
+  if (rg.splits == 0) return;                           // an empty sequence has one part, which writes zeros
+  const int64_t b = rg.b;
+  const int len = rg.len;
 
   const int head = tile * kHeads + i;                   // of this lane's column, within the share
   const bool live_head = head < a.share;
@@ -421,7 +460,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 && !F32 ? 4 : 1) void k_attentio
       }
     return;
   }
-  float* part = a.part + (((b * a.heads + kvh) * a.tiles + tile) * (int64_t)a.splits + split) * (kHeads * (D + 2));
+  float* part = a.part + (int64_t)blockIdx.x * (kHeads * (D + 2));
   if (quarter == 0) part[i] = top, part[kHeads + i] = l;
   float* out = part + 2 * kHeads + i * D + d0;
 #pragma unroll
@@ -437,17 +476,19 @@ __global__ __launch_bounds__(kThreads, D <= 128 && !F32 ? 4 : 1) void k_attentio
 template <bool FOUR, int D, bool F32>
 __global__ __launch_bounds__(kThreads) void k_attention_join(const Args a) {
   constexpr int kPart = kHeads * (D + 2), kRuns = kThreads / (D / 4);
-  __shared__ float weight[kWorkgroups];
+  __shared__ float weight[2 * kResident];               // a sequence has at most `budget` parts
   __shared__ float red[2][kWaves];
   __shared__ v4f sum[kRuns][D / 4];
   const int64_t b = blockIdx.x / (unsigned)(a.heads * a.share);
   const int h = blockIdx.x % (unsigned)(a.heads * a.share), kvh = h / a.share, head = h % a.share;
-  const int splits = range_of(length_of(a, b), 0, a.splits).splits;
+  const Unit rg = find_unit(a, 0, (int)b);
+  const int splits = rg.splits;
   if (splits <= 1) return;
-  const int tile = head / kHeads, i = head % kHeads;
-  const float* part = a.part + (((b * a.heads + kvh) * a.tiles + tile) * (int64_t)a.splits) * kPart + i;
+  const int tile = head / kHeads, i = head % kHeads, pairs = a.heads * a.tiles;
+  const float* part = a.part + ((int64_t)rg.base * pairs + tile * a.heads + kvh) * kPart + i;
+  const int64_t next = (int64_t)pairs * kPart;          // from one part of the sequence to the next
   float top = -INFINITY;
-  for (int s = threadIdx.x; s < splits; s += kThreads) top = fmaxf(top, weight[s] = part[(int64_t)s * kPart]);
+  for (int s = threadIdx.x; s < splits; s += kThreads) top = fmaxf(top, weight[s] = part[s * next]);
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
   if ((threadIdx.x & 63) == 0) red[0][threadIdx.x >> 6] = top;
@@ -458,7 +499,7 @@ __global__ __launch_bounds__(kThreads) void k_attention_join(const Args a) {
   for (int s = threadIdx.x; s < splits; s += kThreads) {        // this thread's own entries
     const float f = weight[s] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(weight[s] - top);
     weight[s] = f;
-    l = fmaf(part[(int64_t)s * kPart + kHeads], f, l);
+    l = fmaf(part[s * next + kHeads], f, l);
   }
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) l += __shfl_xor(l, o, 64);
@@ -471,7 +512,7 @@ __global__ __launch_bounds__(kThreads) void k_attention_join(const Args a) {
   const v4f* out = (const v4f*)(part - i + 2 * kHeads + i * D) + d4;
   v4f o = {0, 0, 0, 0};
 #pragma unroll 4
-  for (int s = run; s < splits; s += kRuns) o += weight[s] * out[(int64_t)s * (kPart / 4)];
+  for (int s = run; s < splits; s += kRuns) o += weight[s] * out[s * (next / 4)];
   sum[run][d4] = o;
   __syncthreads();
   if (run != 0) return;
@@ -487,10 +528,23 @@ __global__ __launch_bounds__(kThreads) void k_attention_join(const Args a) {
   }
 }
 
-int splits_for(const CacheView& c, int64_t batch, int64_t share, int64_t width) {
-  const int64_t pairs = std::max<int64_t>(batch * c.heads * ((share + kHeads - 1) / kHeads), 1);
-  const int64_t most = std::max<int64_t>((width * c.page_size + kMinChunk - 1) / kMinChunk, 1);
-  return (int)std::min<int64_t>((kWorkgroups + pairs - 1) / pairs, most);
+// How the sequences are cut: `splits` parts each, or 0 and together `budget` parts and one a sequence for
+// each head.  A part that is alone on its sequence is finished by its workgroup, so sequences that
+// fill the card are not cut (128 of up to 3000 tokens on 8 heads 56 us, cut 68).  Few long sequences are
+// cut to what is resident at a time, more of them to half of that, so that the last parts end together (7 of up
+// to 60000 tokens 67.0 us against 69.2, 48 of up to 8191 61 against 67).
+struct Cut {
+  int splits, budget;
+  int64_t units;                             // parts for each head, at most
+};
+Cut cut_for(const CacheView& c, int64_t batch, int64_t share, int64_t width) {
+  const int64_t pairs = c.heads * ((share + kHeads - 1) / kHeads), most = std::max<int64_t>((width * c.page_size + kMinChunk - 1) / kMinChunk, 1);
+  if (batch > 64 || batch * pairs >= kResident || most == 1) {
+    const int64_t all = std::max<int64_t>(batch * pairs, 1), splits = std::min((kResident + all - 1) / all, most);
+    return {(int)splits, 0, batch * splits};
+  }
+  const int64_t one = kResident / pairs, budget = batch * 8 <= one ? one - batch : 2 * one;
+  return {0, (int)budget, std::min(batch + budget, batch * most)};
 }
 
 template <bool FOUR, int D, bool F32>
@@ -499,7 +553,7 @@ hipError_t launch_typed(const Args& a, unsigned grid, unsigned join, hipStream_t
                       : a.page_size > 16    ? k_attention<FOUR, D, F32, kTwoPages>
                                             : k_attention<FOUR, D, F32, kAnyPages>;
   const hipError_t e = launch_kernel(kernel, dim3(grid), dim3(kThreads), 0, stream, a);
-  if (e != hipSuccess || a.splits <= 1) return e;
+  if (e != hipSuccess || a.splits == 1) return e;
   return launch_kernel(k_attention_join<FOUR, D, F32>, dim3(join), dim3(kThreads), 0, stream, a);
 }
 
@@ -512,11 +566,11 @@ hipError_t launch_dim(const Args& a, bool four, bool f32, unsigned grid, unsigne
 }  // namespace
 
 int64_t attention_grid(const CacheView& c, int64_t batch, int64_t share, int64_t width) {
-  return batch * c.heads * ((share + kHeads - 1) / kHeads) * splits_for(c, batch, share, width);
+  return c.heads * ((share + kHeads - 1) / kHeads) * cut_for(c, batch, share, width).units;
 }
 
 int64_t attention_workspace(const CacheView& c, int64_t batch, int64_t share, int64_t width) {
-  if (splits_for(c, batch, share, width) <= 1) return 0;
+  if (cut_for(c, batch, share, width).splits == 1) return 0;
   return attention_grid(c, batch, share, width) * kHeads * (c.dim + 2) * (int64_t)sizeof(float);
 }
 
@@ -536,7 +590,10 @@ hipError_t launch_attention(const CacheView& c, const void* q, bool bf16, int64_
   a.heads = (int)c.heads;
   a.share = (int)share;
   a.tiles = (int)((share + kHeads - 1) / kHeads);
-  a.splits = splits_for(c, batch, share, width);
+  a.batch = (int)batch;
+  const Cut cut = cut_for(c, batch, share, width);
+  a.splits = cut.splits;
+  a.budget_mul = cut.splits > 0 ? 0 : (unsigned)((uint64_t(1) << 32) / cut.budget + ((uint64_t(1) << 32) % cut.budget != 0));
   a.width = (int)width;
   a.n_pages = c.n_pages;
   a.page_size = (unsigned)c.page_size;

@@ -408,6 +408,40 @@ def test_attention_one_long_sequence():
     check_attention(o, q, values, 1, 2, 64, 0.125)
 
 
+def uneven(n, most, seed):
+    """n lengths up to `most`, a few of them empty and one longer than all others together would suggest."""
+    r = np.random.default_rng(seed)
+    lens = (most * r.random(n) ** 3).astype(int)
+    lens[r.permutation(n)[:n // 8]] = 0
+    lens[n // 3] = 4 * most
+    return lens.tolist()
+
+
+# (lengths, heads, share): up to 64 sequences cut to one length, by what is resident or by twice that; more
+# than 64 with equal counts; enough to fill the card uncut; key-value heads in more than one tile
+CUTS = [(uneven(64, 1200, 1), 1, 2), (uneven(63, 700, 2), 3, 1), (uneven(65, 600, 3), 1, 2), (uneven(200, 500, 4), 1, 1),
+        (uneven(5, 2000, 5), 40, 1), ([2111], 96, 1), ([1300, 0, 2700], 3, 17), ([513, 0], 1, 1), (uneven(130, 300, 6), 8, 1)]
+
+
+@pytest.mark.parametrize("lens,heads,share", CUTS, ids=lambda v: f"{len(v)}x{max(v)}" if isinstance(v, list) else str(v))
+@pytest.mark.parametrize("four", [True, False])
+def test_attention_cuts_of_uneven_sequences(lens, heads, share, four):
+    note(f"attention cuts {len(lens)} sequences up to {max(lens)} heads {heads} share {share} four {four}")
+    cache, table, lengths, q, values = attention_case(lens, heads, share, 64, 16, four, "bf16", len(lens) + heads)
+    o = lh.lh_paged_attention(q.to(DEV), cache, table, lengths, scale=0.125)
+    check_attention(o, q, values, heads, share, 64, 0.125)
+    again = lh.lh_paged_attention(q.to(DEV), cache, table, lengths, scale=0.125)
+    assert torch.equal(o, again)
+
+
+def test_attention_all_empty_under_a_wide_table():
+    note("attention 64 empty sequences, table of 3 pages of 512")
+    cache, table, lengths, q, _ = attention_case([0] * 64, 2, 1, 64, 512, True, "bf16", 9)
+    for lens in (lengths, lengths - 7):
+        o = lh.lh_paged_attention(q.to(DEV), cache, table, lens, scale=0.125)
+        assert torch.equal(o, torch.zeros_like(o))
+
+
 def test_attention_lengths_outside_the_table():
     """A negative length is 0 and one past the table ends with it; a page outside the cache reads page 0."""
     note("attention, lengths and pages out of range")
