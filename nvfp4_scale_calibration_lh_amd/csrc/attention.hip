@@ -7,8 +7,8 @@
 // over workgroups whose partial (maximum, sum, output) a second kernel joins.  Within a workgroup
 // the four waves take 32-token tiles in turn, each with a running maximum and sum of its own, and
 // meet in LDS at the end.  NVFP4, head dimension 128: 4 sequences of 131001 tokens, 64 heads on 8,
-// 117 us (604 MB, 5.2 TB/s) and 5 us for the join; 48 sequences of up to 8191 tokens, 32 heads on 8, 62
-// us (234 MB, 3.8 TB/s) and 5 us; 301 tokens of one sequence in E4M3 6.6 us.
+// 114 us (604 MB, 5.3 TB/s) and 5 us for the join; 48 sequences of up to 8191 tokens, 32 heads on 8, 55
+// us (234 MB, 4.3 TB/s) and 5 us; 301 tokens of one sequence in E4M3 6.6 us.
 //
 // A tile is two matrix products without any exchange between lanes:
 //   S^T = K Q^T   A = 16 tokens of K, B = the heads' q; the result's lane (head, quarter) holds
@@ -57,7 +57,8 @@ struct Args {
   float scale_log2;                          // softmax scale * log2(e)
   int heads, share, tiles, batch, width;
   int splits;                                // parts of each sequence; 0: all are cut to one length, by
-  unsigned budget_mul;                       // 2^32 / budget rounded up
+  unsigned budget_mul, least_mul;            // 2^32 / budget rounded up; that of the budget for which `units` suffice
+  int units;                                 // parts of all sequences, at most
   int64_t n_pages;
   unsigned page_size, page_mul, page_shift;  // n / page_size = n * page_mul >> page_shift, n < 2^31
 };
@@ -137,11 +138,15 @@ struct Unit {
 
 // The unit-th part over all sequences in order, or sequence b if b >= 0; splits is 0 past the last part.
 // Up to 64 sequences are cut to parts of one length, from the tokens of all of them, so that uneven
-// sequences keep the compute units evenly busy (48 of up to 8191 tokens in NVFP4 62 us, in E4M3 92, against
+// sequences keep the compute units evenly busy (48 of up to 8191 tokens in NVFP4 61 us, in E4M3 91, against
 // 70 and 102 where each was cut into as many parts as the others); every wave finds its part by a
 // scan over its lanes.  More sequences get the same number of parts each: they even out, and a scan
 // would be several dependent loads (300 sequences of one head 57 us with one, 53 without).
 __device__ inline Unit find_unit(const Args& a, int unit, int b) {
+  if (a.splits == 1) {                                  // without the divisions below
+    const int seq = b >= 0 ? b : unit, len = length_of(a, seq);
+    return {seq, len, 0, len, 1, seq};
+  }
   if (a.splits > 0) {
     const int seq = b >= 0 ? b : unit / a.splits, base = seq * a.splits, len = length_of(a, seq);
     const int part = max(((len + a.splits - 1) / a.splits + kStep - 1) / kStep * kStep, kMinChunk);
@@ -154,14 +159,19 @@ __device__ inline Unit find_unit(const Args& a, int unit, int b) {
   const int len = lane < a.batch ? length_of(a, lane) : 0;
   const unsigned steps = ((unsigned)len + kStep - 1) / kStep;
   const unsigned all = (unsigned)__builtin_amdgcn_readlane((int)scan(steps), 63);
-  // steps of a part: all / budget rounded up (or one more), so that the parts are at most budget and one a sequence
-  const unsigned most = max(__umulhi(all - 1, a.budget_mul) + 1, (unsigned)(kMinChunk / kStep));
-  // steps / most rounded up: the quotient is at most budget < 2^12, so the product is less than one away from it
-  unsigned n = (unsigned)((float)steps * __builtin_amdgcn_rcpf((float)most));
-  const int left = (int)(steps - n * most);
-  n = n + (left > 0) + (left > 0 && (unsigned)left > most);
-  n = lane < a.batch ? max(n, 1u) : 0;
-  const unsigned upto = scan(n);
+  unsigned most, n, upto;
+  auto cut = [&](unsigned budget_mul) __attribute__((always_inline)) {
+    // steps of a part: all / budget rounded up (or one more), so that the parts are at most budget and one a sequence
+    most = max(__umulhi(all - 1, budget_mul) + 1, (unsigned)(kMinChunk / kStep));
+    // steps / most rounded up: the quotient is at most budget < 2^12, so the product is less than one away from it
+    n = (unsigned)((float)steps * __builtin_amdgcn_rcpf((float)most));
+    const int left = (int)(steps - n * most);
+    n = n + (left > 0) + (left > 0 && (unsigned)left > most);
+    n = lane < a.batch ? max(n, 1u) : 0;
+    upto = scan(n);
+  };
+  cut(a.budget_mul);
+  if (__builtin_amdgcn_readlane((int)upto, 63) > a.units) cut(a.least_mul);
   if (b < 0 && unit >= __builtin_amdgcn_readlane((int)upto, 63)) return {0, 0, 0, 0, 0, 0};
   const int owner = b >= 0 ? b : __ffsll((unsigned long long)__ballot((unsigned)unit < upto)) - 1;
   const int seq_len = __builtin_amdgcn_readlane(len, owner), splits = __builtin_amdgcn_readlane((int)n, owner);
@@ -528,23 +538,24 @@ __global__ __launch_bounds__(kThreads) void k_attention_join(const Args a) {
   }
 }
 
-// How the sequences are cut: `splits` parts each, or 0 and together `budget` parts and one a sequence for
-// each head.  A part that is alone on its sequence is finished by its workgroup, so sequences that
+// How the sequences are cut: `splits` parts each, or 0 and all to one length, into `budget` parts and up to
+// one more a sequence, or if those are more than `units`, into `least` and one a sequence.  A part that is alone on its sequence is finished by its workgroup, so sequences that
 // fill the card are not cut (128 of up to 3000 tokens on 8 heads 56 us, cut 68).  Few long sequences are
 // cut to what is resident at a time, more of them to half of that, so that the last parts end together (7 of up
-// to 60000 tokens 67.0 us against 69.2, 48 of up to 8191 61 against 67).
+// to 60000 tokens 64 us against 69, 48 of up to 8191 61 against 67).
 struct Cut {
-  int splits, budget;
+  int splits, budget, least;
   int64_t units;                             // parts for each head, at most
 };
 Cut cut_for(const CacheView& c, int64_t batch, int64_t share, int64_t width) {
   const int64_t pairs = c.heads * ((share + kHeads - 1) / kHeads), most = std::max<int64_t>((width * c.page_size + kMinChunk - 1) / kMinChunk, 1);
   if (batch > 64 || batch * pairs >= kResident || most == 1) {
     const int64_t all = std::max<int64_t>(batch * pairs, 1), splits = std::min((kResident + all - 1) / all, most);
-    return {(int)splits, 0, batch * splits};
+    return {(int)splits, 0, 0, batch * splits};
   }
-  const int64_t one = kResident / pairs, budget = batch * 8 <= one ? one - batch : 2 * one;
-  return {0, (int)budget, std::min(batch + budget, batch * most)};
+  const int64_t one = kResident / pairs;
+  if (batch * 8 <= one) return {0, (int)one, (int)(one - batch), std::min(one, batch * most)};
+  return {0, (int)(2 * one), (int)(2 * one), std::min(2 * one + batch, batch * most)};
 }
 
 template <bool FOUR, int D, bool F32>
@@ -593,7 +604,8 @@ hipError_t launch_attention(const CacheView& c, const void* q, bool bf16, int64_
   a.batch = (int)batch;
   const Cut cut = cut_for(c, batch, share, width);
   a.splits = cut.splits;
-  a.budget_mul = cut.splits > 0 ? 0 : (unsigned)((uint64_t(1) << 32) / cut.budget + ((uint64_t(1) << 32) % cut.budget != 0));
+  auto inverse = [](int n) { return (unsigned)(((uint64_t(1) << 32) + n - 1) / n); };
+  if (cut.splits == 0) a.budget_mul = inverse(cut.budget), a.least_mul = inverse(cut.least), a.units = (int)cut.units;
   a.width = (int)width;
   a.n_pages = c.n_pages;
   a.page_size = (unsigned)c.page_size;
