@@ -422,6 +422,8 @@ lh_status lh_cache_read(const lh_cache* cache, const int64_t* slots, int64_t tok
  * read; a page outside the cache is read as page 0.  head_dim is 64, 128 or 256.
  * K and V enter exactly; q is held to 2^-40 of its head's largest element (fp32: to 2^-22 of each
  * element too), p to fp16 (fp32: two fp16 pieces), and maxima, sums and outputs are fp32.
+ * Two calls with the same arguments give the same bits; where a sequence is cut depends on all
+ * lengths of the batch, so beside other sequences its last bits may differ.
  * workspace: device memory of at least lh_paged_attention_workspace bytes (16-byte aligned; NULL if
  * that is 0) that no other call uses until this one has run.
  * Errors: UNSUPPORTED for an unknown dtype or format, or another head_dim; INVALID_ARGUMENT as
