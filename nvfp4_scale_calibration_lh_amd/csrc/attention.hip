@@ -7,7 +7,7 @@
 // over workgroups whose partial (maximum, sum, output) a second kernel joins.  Within a workgroup
 // the four waves take 32-token tiles in turn, each with a running maximum and sum of its own, and
 // meet in LDS at the end.  NVFP4, head dimension 128: 4 sequences of 131001 tokens, 64 heads on 8,
-// 114 us (604 MB, 5.3 TB/s) and 5 us for the join; 48 sequences of up to 8191 tokens, 32 heads on 8, 55
+// 115 us (604 MB, 5.2 TB/s) and 5 us for the join; 48 sequences of up to 8191 tokens, 32 heads on 8, 54
 // us (234 MB, 4.3 TB/s) and 5 us; 301 tokens of one sequence in E4M3 6.6 us.
 //
 // A tile is two matrix products without any exchange between lanes:
