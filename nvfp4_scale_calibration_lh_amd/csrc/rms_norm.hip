@@ -72,8 +72,9 @@ __device__ inline v4u add_unit(const v4u x, const v4u r) {
   return o;
 }
 
-// E4M3 bytes of y / s.  |y| <= 448 s (1 + 2^-22), so the quotient rounds to at most 448.  A scale
-// below 2^-100 is raised with y by 2^60, so that its reciprocal stays finite; s = 0 gives 0.
+// E4M3 bytes of y / s, at most 448: a subnormal s may lie far below max|y| / 448 (the quotient reaches 671),
+// and the conversion does not saturate.  A scale below 2^-100 is raised with y by 2^60, so that its
+// reciprocal stays finite; s = 0 gives 0.
 template <int N>
 __device__ inline void quantise(const float* y, float s, unsigned* out) {
   const float up = s < 0x1p-100f ? 0x1p60f : 1.0f;
@@ -82,7 +83,7 @@ __device__ inline void quantise(const float* y, float s, unsigned* out) {
   for (int w = 0; w < N / 4; ++w) {
     float t[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) t[k] = y[4 * w + k] * up * inv;
+    for (int k = 0; k < 4; ++k) t[k] = __builtin_amdgcn_fmed3f(y[4 * w + k] * up * inv, -448.0f, 448.0f);
     const int v = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false);
     out[w] = (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], v, true);
   }
