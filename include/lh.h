@@ -30,7 +30,8 @@
  *     on different streams are ordered through an event, so two calls never use it at once.
  *   - Return: LH_OK, or an error code with a message available from lh_last_error().  Argument
  *     checks run before any launch.  Faults inside kernels surface at the caller's next
- *     synchronization, as usual in HIP.  NaN or Inf in any input gives undefined results.
+ *     synchronization, as usual in HIP.  NaN or Inf in any input gives undefined results where an
+ *     entry point does not say otherwise.
  *
  * Numerics
  *   - Accumulation reads bf16 or fp32 values exactly, multiplies them exactly (bf16) or in fp32
@@ -325,6 +326,10 @@ lh_status lh_absmax(const void* W, lh_dtype w_dtype, int64_t n_groups, int64_t e
  * receives h; it is required with R, must be NULL without, and may be X or R itself.
  * q [rows, cin] E4M3 bytes; q_scale [rows] or [rows, ceil(cin/128)] fp32.  All 16-byte aligned
  * but q_scale.  Sums are fp32; a row of zeros (with eps = 0, too) gives q = 0.
+ * A NaN in a row of h makes all scales of the row NaN, an infinity the scale of its run (the other
+ * channels become 0); one in gamma makes its run's scale NaN or infinite.  q is 0 where the scale is
+ * not finite.  The sum of squares keeps fp32's range: a row over it (elements near 2^60) gives zeros, and
+ * with eps = 0 one under it (near 2^-60) loses bits and then gives zeros.
  * Errors: INVALID_ARGUMENT for rows < 0 or over 2^31-1, cin <= 0 or cin % 16 or cin > 2^24, a group
  * other than 0 and 128, a bad eps, R without summed or the reverse, NULL required pointers,
  * misaligned, non-device or mixed-device pointers.

@@ -74,23 +74,28 @@ __device__ inline v4u add_unit(const v4u x, const v4u r) {
 
 // E4M3 bytes of y / s, at most 448: a subnormal s may lie far below max|y| / 448 (the quotient reaches 671),
 // and the conversion does not saturate.  A scale below 2^-100 is raised with y by 2^60, so that its
-// reciprocal stays finite; s = 0 gives 0.
+// reciprocal stays finite; a scale that is 0, infinite or NaN gives 0.
 template <int N>
 __device__ inline void quantise(const float* y, float s, unsigned* out) {
   const float up = s < 0x1p-100f ? 0x1p60f : 1.0f;
-  const float inv = s == 0.0f ? 0.0f : 1.0f / (s * up);
+  const bool live = s > 0.0f && s < INFINITY;
+  const float inv = live ? 1.0f / (s * up) : 0.0f;
 #pragma unroll
   for (int w = 0; w < N / 4; ++w) {
     float t[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) t[k] = __builtin_amdgcn_fmed3f(y[4 * w + k] * up * inv, -448.0f, 448.0f);
     const int v = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false);
-    out[w] = (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], v, true);
+    out[w] = live ? (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], v, true) : 0u;
   }
 }
 
-// 1 / sqrt(v); 0 for a row of zeros without eps, whose y is 0 and not 0 times infinity.
-__device__ inline float inv_rms(float v) { return v > 0.0f ? 1.0f / sqrtf(v) : 0.0f; }
+// 1 / sqrt(v); 0 for a row of zeros without eps, whose y is 0 and not 0 times infinity; NaN for a row that
+// holds one.
+__device__ inline float inv_rms(float v) { return v == 0.0f ? 0.0f : 1.0f / sqrtf(v); }
+
+// The larger of the two, NaN if either is: a scale over a NaN is NaN, and so is what is read through it.
+__device__ inline float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 
 __device__ inline float wave_sum(float v) {
 #pragma unroll
@@ -99,7 +104,7 @@ __device__ inline float wave_sum(float v) {
 }
 __device__ inline float wave_max(float v) {
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+  for (int o = 32; o >= 1; o >>= 1) v = larger(v, __shfl_xor(v, o, 64));
   return v;
 }
 
@@ -159,13 +164,13 @@ __global__ __launch_bounds__(kThreads) void k_rms_norm(const Args a) {
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       y[j][k] = y[j][k] * rstd * g[k];
-      m = fmaxf(m, fabsf(y[j][k]));
+      m = larger(m, fabsf(y[j][k]));
     }
     if (a.scales == 1) {
-      top = fmaxf(top, m);
+      top = larger(top, m);
     } else {                           // this unit's 128 channels
 #pragma unroll
-      for (int o = kGroup / N / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+      for (int o = kGroup / N / 2; o >= 1; o >>= 1) m = larger(m, __shfl_xor(m, o, 64));
       const float s = m * kInv448;
       if (u < a.units) {
         unsigned out[N / 4];
@@ -185,7 +190,7 @@ __global__ __launch_bounds__(kThreads) void k_rms_norm(const Args a) {
     __syncthreads();
     top = red[1][0];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, red[1][w]);
+    for (int w = 1; w < kWaves; ++w) top = larger(top, red[1][w]);
   }
   const float s = top * kInv448;
   if (t == 0) a.s[row] = s;
@@ -235,18 +240,18 @@ __global__ __launch_bounds__(1024) void k_rms_norm_long(const Args a) {
     float m = 0.0f;
     for (int k = 0; k < N; ++k) {
       y[k] = y[k] * rstd * g[k];
-      m = fmaxf(m, fabsf(y[k]));
+      m = larger(m, fabsf(y[k]));
     }
     return m;
   };
   float s = 0.0f, y[8];
   if (a.scales == 1) {
     float top = 0.0f;
-    for (int u = threadIdx.x; u < a.units; u += T) top = fmaxf(top, normed(load(u), u, y));
+    for (int u = threadIdx.x; u < a.units; u += T) top = larger(top, normed(load(u), u, y));
     top = wave_max(top);
     if ((threadIdx.x & 63) == 0) red[1][threadIdx.x >> 6] = top;
     __syncthreads();
-    for (int w = 0; w < T / 64; ++w) s = fmaxf(s, red[1][w]);
+    for (int w = 0; w < T / 64; ++w) s = larger(s, red[1][w]);
     s = s * kInv448;
     if (threadIdx.x == 0) a.s[blockIdx.x] = s;
   }
@@ -255,7 +260,7 @@ __global__ __launch_bounds__(1024) void k_rms_norm_long(const Args a) {
     const v4u v = load(u);
     float m = normed(v, u, y);
     if (a.scales != 1) {
-      for (int o = kGroup / N / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+      for (int o = kGroup / N / 2; o >= 1; o >>= 1) m = larger(m, __shfl_xor(m, o, 64));
       s = m * kInv448;
       if (u < a.units && u % (kGroup / N) == 0) a.s[(int64_t)blockIdx.x * a.scales + u / (kGroup / N)] = s;
     }

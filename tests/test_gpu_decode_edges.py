@@ -1,4 +1,5 @@
-"""Edges of the decode-step operators on the GPU, against the float64 oracle: scales under fp32's normal numbers."""
+"""Edges of the decode-step operators on the GPU, against the float64 oracle: scales under fp32's normal numbers,
+infinities and NaN."""
 import numpy as np
 import pytest
 import torch
@@ -60,3 +61,42 @@ def test_norm_of_rows_with_subnormal_scales(cin, dtype, group):
     held = np.clip(y, -448 * wide, 448 * wide)
     tol = np.maximum(np.abs(y) * 2.0 ** -4, wide * 2.0 ** -10) * (1 + 2 ** -10) + 2 * rel * np.abs(y) + TINY
     assert np.all(np.abs(got * wide - held) <= tol)
+
+
+@pytest.mark.parametrize("cin", [256, 2064, 16400])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("residual", [True, False])
+def test_norm_shows_infinities_and_nan(cin, dtype, group, residual):
+    """h / sqrt(mean h^2 + eps) is NaN everywhere for a row with a NaN, and for one with an infinity NaN there and 0
+    elsewhere.  The other rows are those of a call without them, and gamma's NaN or infinity stays in its run."""
+    note(f"norm with infinities and NaN, {cin} {dtype} group {group} residual {residual}")
+    t, g, rows, at = TYPES[dtype], gen(cin + 1), 9, cin - 70
+    x = torch.randn(rows, cin, generator=g).to(t)
+    r = torch.randn(rows, cin, generator=g).to(t) if residual else None
+    gamma = (1 + 0.2 * torch.randn(cin, generator=g)).to(t)
+
+    def call(x, gamma):
+        q, s, h = lh.lh_rms_norm_quant(x.to(DEV), gamma.to(DEV), None if r is None else r.to(DEV), group=group)
+        return f64(q.float()), f64(s), h
+
+    good_q, good_s, _ = call(x, gamma)
+    bad = x.clone()
+    bad[1, at], bad[3, at], bad[6, at] = float("nan"), float("inf"), -float("inf")
+    q, s, h = call(bad, gamma)
+    run = at // 128 if group else 0
+    others = [i for i in range(rows) if i not in (1, 3, 6)]
+    assert np.array_equal(q[others], good_q[others]) and np.array_equal(s[others], good_s[others])
+    assert np.isnan(s[1]).all() and (q[[1, 3, 6]] == 0).all()
+    for i in (3, 6):
+        assert np.isnan(s[i, run]) and (np.delete(s[i], run) == 0).all()
+    if residual:
+        assert torch.isnan(h[1, at]) and h[3, at] == float("inf") and h[6, at] == -float("inf")
+
+    for value in (float("nan"), float("inf")):
+        gm = gamma.clone()
+        gm[at] = value
+        q, s, _ = call(x, gm)
+        keep = np.arange(cin) // 128 != run if group else np.zeros(cin, bool)
+        assert not np.isfinite(s[:, run]).any() and np.array_equal(np.delete(s, run, 1), np.delete(good_s, run, 1))
+        assert np.array_equal(q[:, keep], good_q[:, keep]) and (q[:, ~keep] == 0).all()
