@@ -321,7 +321,8 @@ lh_status lh_absmax(const void* W, lh_dtype w_dtype, int64_t n_groups, int64_t e
  *   h[t,i] = X[t,i] + R[t,i] rounded to dtype          (h = X when R is NULL)
  *   y[t,i] = h[t,i] / sqrt(mean_i h[t,i]^2 + eps) * gamma[i]                        (in fp32)
  *   per row (group = 0) or per 128 channels of a row (group = 128, the last run may be shorter):
- *     scale = max|y| * fp32(1/448),  q = the E4M3 value nearest to y / scale (0 where scale = 0)
+ *     scale = max|y| * fp32(1/448),  q = the E4M3 value nearest to y / scale, the exact quotient of the
+ *     two fp32 numbers, ties to the even code (0 where scale = 0)
  * X, R [rows, cin] of dtype; gamma [cin] of dtype; eps >= 0 and finite.  summed [rows, cin] of dtype
  * receives h; it is required with R, must be NULL without, and may be X or R itself.
  * q [rows, cin] E4M3 bytes; q_scale [rows] or [rows, ceil(cin/128)] fp32.  All 16-byte aligned

@@ -16,6 +16,7 @@
 // lane, 8191 tokens of 8 x 128 took 16 us to write, bound by instructions.  Now 11.8 us (43 MB, 3.6
 // TB/s) and 10.4 us to read back; 30011 tokens of 4 x 64 in E4M3 11.0 and 10.4 us.
 #include "acc_stream.hpp"
+#include "e4m3.hpp"
 #include "lh_internal.hpp"
 
 #include <algorithm>
@@ -96,20 +97,6 @@ __device__ inline void split(const Args& a, int64_t i, int64_t* token, unsigned*
   *token = group * kTokens + row % kTokens;
 }
 
-// E4M3 code of a / (f s) between codes lo and lo + 1: the sign of f m s - a (m their midpoint, so f m
-// has at most 7 significant bits for f = 1 or 6) is exact in one fma; a tie goes to the even code.
-template <int F>
-__device__ inline unsigned e4m3_resolve(float a, float s, unsigned lo) {
-  const float x = __builtin_amdgcn_cvt_f32_fp8((int)lo, 0), y = __builtin_amdgcn_cvt_f32_fp8((int)lo + 1, 0);
-  const float d = fmaf(0.5f * F * (x + y), s, -a);
-  return d < 0.0f ? lo + 1 : (d > 0.0f ? lo : lo + (lo & 1));
-}
-
-// The reciprocal and its neighbours that bracket an exact quotient: through the 1-ulp hardware
-// reciprocal (and the rounding of 6 g) a quotient is within 2^-21 of the exact one, so what it rounds
-// to when pushed up and down by 2^-19 differs only where the exact decision has to be taken.
-constexpr float kUp = 1.0000019073486328125f, kDown = 0.9999980926513671875f;
-
 // E4M3 code of a block's scale, top / (6 g); g in [2^-100, 2^100].
 __device__ inline unsigned block_code(float top, float g) {
   const float t = top * __builtin_amdgcn_rcpf(6.0f * g);
@@ -122,28 +109,9 @@ __device__ inline unsigned block_code(float top, float g) {
 __device__ inline v4u e4m3_codes(const float* x, float s, bool fast) {
   v4u out = {0, 0, 0, 0};
   if (fast) {
-    const float is = __builtin_amdgcn_rcpf(s), iu = is * kUp, id = is * kDown;
+    const float is = __builtin_amdgcn_rcpf(s);
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      auto pack = [&](float f) {
-        float t[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) t[k] = fminf(fmaxf(x[4 * w + k] * f, -448.0f), 448.0f);
-        const int v = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false);
-        return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], v, true);
-      };
-      unsigned up = pack(iu);
-      const unsigned dn = pack(id);
-      if (up != dn) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const unsigned cu = (up >> (8 * k)) & 127u, cd = (dn >> (8 * k)) & 127u;
-          if (cu != cd)
-            up = (up & ~(127u << (8 * k))) | (e4m3_resolve<1>(fabsf(x[4 * w + k]), s, cd) << (8 * k));
-        }
-      }
-      out[w] = up;
-    }
+    for (int w = 0; w < 4; ++w) out[w] = e4m3_word(x + 4 * w, s, is);
   } else {
 #pragma unroll
     for (int k = 0; k < 16; ++k) {

@@ -1,6 +1,7 @@
 // Root-mean-square norm of a residual stream, with the residual's addition and an E4M3 output:
 //   h = round(x + r) in the input type (h = x without r),  y = h / sqrt(mean h^2 + eps) * gamma,
-//   per row or per 128 channels of it: s = max|y| * fp32(1/448), q = E4M3 nearest to y / s.
+//   per row or per 128 channels of it: s = max|y| * fp32(1/448), q = E4M3 nearest to the exact y / s, ties to
+//   the even code.
 //
 // HBM-bound: a row is read once and kept in registers between its two reductions (the sum of
 // squares, then the largest |y|), so the kernel moves the input, h, q and the scales once.  A row
@@ -11,6 +12,7 @@
 // (a 2 GiB copy runs at 4.9 TB/s; part of this working set stays in the memory-side cache); one row of
 // 4096 2.8 us, the floor of a launch.  Sums are fp32.  The only roundings to fewer bits are h (the carried residual has the
 // input's type, and the norm is of what is carried) and q.
+#include "e4m3.hpp"
 #include "lh_internal.hpp"
 
 #include <algorithm>
@@ -72,21 +74,22 @@ __device__ inline v4u add_unit(const v4u x, const v4u r) {
   return o;
 }
 
-// E4M3 bytes of y / s, at most 448: a subnormal s may lie far below max|y| / 448 (the quotient reaches 671),
-// and the conversion does not saturate.  A scale below 2^-100 is raised with y by 2^60, so that its
-// reciprocal stays finite; a scale that is 0, infinite or NaN gives 0.
+// E4M3 bytes nearest to y / s (ties to the even code), at most 448: a subnormal s may lie far below max|y| / 448
+// (the quotient reaches 671).  A scale out of the range of e4m3_word is brought there with y by a power of
+// two, which changes no decision: a y that loses bits by it is 2^-60 of s at most.  A scale that is 0, infinite
+// or NaN gives 0.
 template <int N>
 __device__ inline void quantise(const float* y, float s, unsigned* out) {
-  const float up = s < 0x1p-100f ? 0x1p60f : 1.0f;
   const bool live = s > 0.0f && s < INFINITY;
-  const float inv = live ? 1.0f / (s * up) : 0.0f;
+  const float by = s < 0x1p-100f ? 0x1p60f : (s > 0x1p100f ? 0x1p-60f : 1.0f);
+  const float sb = live ? s * by : 1.0f, is = __builtin_amdgcn_rcpf(sb);
 #pragma unroll
   for (int w = 0; w < N / 4; ++w) {
     float t[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) t[k] = __builtin_amdgcn_fmed3f(y[4 * w + k] * up * inv, -448.0f, 448.0f);
-    const int v = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false);
-    out[w] = live ? (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], v, true) : 0u;
+    for (int k = 0; k < 4; ++k) t[k] = y[4 * w + k] * by;
+    const unsigned v = e4m3_word(t, sb, is);
+    out[w] = live ? v : 0u;
   }
 }
 

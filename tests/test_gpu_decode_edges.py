@@ -1,5 +1,5 @@
 """Edges of the decode-step operators on the GPU, against the float64 oracle: scales under fp32's normal numbers,
-infinities and NaN."""
+infinities and NaN, and decisions at midpoints."""
 import numpy as np
 import pytest
 import torch
@@ -100,3 +100,35 @@ def test_norm_shows_infinities_and_nan(cin, dtype, group, residual):
         keep = np.arange(cin) // 128 != run if group else np.zeros(cin, bool)
         assert not np.isfinite(s[:, run]).any() and np.array_equal(np.delete(s, run, 1), np.delete(good_s, run, 1))
         assert np.array_equal(q[:, keep], good_q[:, keep]) and (q[:, ~keep] == 0).all()
+
+
+@pytest.mark.parametrize("dtype,cin", [("bf16", 256), ("bf16", 2048), ("bf16", 32768), ("f32", 256), ("f32", 2048), ("f32", 16384)])
+@pytest.mark.parametrize("group", [0, 128])
+def test_norm_writes_the_code_nearest_to_the_quotient(dtype, cin, group):
+    """Rows of +-2^k have a reciprocal root mean square of 2^-k and y = +-gamma without a rounding, so scale and the exact
+    quotient are known: gamma holds every midpoint of the E4M3 grid times the scale, with its neighbours in fp32."""
+    note(f"norm, midpoints, {cin} {dtype} group {group}")
+    t, width = TYPES[dtype], group or cin
+    vals = decode.e4m3_values(np.arange(127))
+    mids = (vals[1:] + vals[:-1]) / 2
+    r = np.random.default_rng(cin + group)
+    gamma, at = np.zeros(cin, np.float32), 0
+    exponents = [0, -3, -97, -105, -120, 60, 105, 115, 5, -20] if group else [(-112 if cin == 2048 else 1)]
+    for k, c in enumerate(range(0, cin, width)):
+        top = float(torch.tensor(r.uniform(1, 2) * 2.0 ** exponents[k % len(exponents)]).to(t))
+        s = np.float32(np.float32(top) * np.float32(1 / 448.0))
+        m = np.resize(np.roll(mids, -at), width // 3).astype(np.float64) * np.float64(s)
+        at += width // 3
+        m = m.astype(np.float32)
+        run = np.concatenate([[np.float32(top)], m, np.nextafter(m, np.float32(0)), np.nextafter(m, np.float32(np.inf))])
+        gamma[c:c + width] = np.minimum(np.resize(run, width), np.float32(top))
+    gamma = torch.from_numpy(gamma).to(t)
+    g = gen(cin)
+    h = torch.where(torch.rand(5, cin, generator=g) < 0.5, -1.0, 1.0) * torch.tensor([[1.0], [0.25], [64.0], [2.0 ** -9], [2.0 ** 20]])
+    q, scale, _ = lh.lh_rms_norm_quant(h.to(t).to(DEV), gamma.to(DEV), eps=0.0, group=group)
+    y = np.sign(f64(h)) * f64(gamma)
+    want = (np.abs(gamma.float().numpy()).reshape(-1, width).max(1) * np.float32(1 / 448.0)).astype(np.float32)
+    assert np.array_equal(scale.cpu().numpy(), np.tile(want, (5, 1)))
+    codes = decode.e4m3_codes(y / np.repeat(want.astype(np.float64), width))
+    got = q.view(torch.uint8).cpu().numpy()
+    assert np.array_equal(got, codes), f"{(got != codes).sum()} of {got.size} codes differ"
