@@ -346,6 +346,7 @@ lh_status lh_rms_norm_quant(const void* X, const void* R, lh_dtype dtype, int64_
  *   Wq[g][c][k] = E2M1(nibble) * v_code * g_g,  g_g = fp32(global_amax[g] / (6 * scale_norm)),
  * that is lh_dequantize_ex's weights before their rounding.  Products are exact and sums fp32, in a
  * fixed order; g_g multiplies the sum, which is rounded once to Y's type.
+ * Infinities and NaN in a row of X give what the row's sums of products are, and change no other row.
  * scale_code [n_groups, cout, cin/16], fp4 [n_groups, cout, cin/2] (8-byte aligned), global_amax
  * [n_groups], scale_norm as in lh_sweep_options.
  * X [rows, cin], 16-byte aligned: F32, BF16, or E4M3 bytes with x_scale fp32, one per row (x_group = 0,

@@ -174,7 +174,7 @@ __device__ inline void frag_x(const Raw<X>& r, typename Frag<X>::type* f) {
     for (int e = 0; e < 8; ++e) {                    // truncated pieces: 8 + 8 + 8 bits
       const float x = __uint_as_float(r.v[2 * S + e / 4][e % 4]);
       const float hi = __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
-      const float r1 = x - hi;
+      const float r1 = x == hi ? 0.0f : x - hi;      // an infinity is its first piece, not infinity minus infinity
       const float mid = __uint_as_float(__float_as_uint(r1) & 0xFFFF0000u);
       f[0][e] = __builtin_bit_cast(__bf16, (unsigned short)(__float_as_uint(hi) >> 16));
       f[1][e] = __builtin_bit_cast(__bf16, (unsigned short)(__float_as_uint(mid) >> 16));

@@ -132,3 +132,52 @@ def test_norm_writes_the_code_nearest_to_the_quotient(dtype, cin, group):
     codes = decode.e4m3_codes(y / np.repeat(want.astype(np.float64), width))
     got = q.view(torch.uint8).cpu().numpy()
     assert np.array_equal(got, codes), f"{(got != codes).sum()} of {got.size} codes differ"
+
+
+# -------------------------------------------------------------------------------------- the products
+def weights(groups, cout, cin, seed):
+    r = np.random.default_rng(seed)
+    code = r.integers(1, 127, (groups, cout, cin // 16)).astype(np.uint8)
+    fp4 = r.integers(0, 256, (groups, cout, cin // 2)).astype(np.uint8)
+    amax = (0.1 + r.random(groups)).astype(np.float32)
+    return code, fp4, amax
+
+
+def on_gpu(*arrays):
+    return [torch.from_numpy(a).to(DEV) for a in arrays]
+
+
+@pytest.mark.parametrize("rows", [1, 5, 9, 17, 33])
+@pytest.mark.parametrize("cin", [48, 144, 2064, 4112])
+@pytest.mark.parametrize("x", ["bf16", "f32"])
+def test_matvec_of_infinities_and_nan(rows, cin, x):
+    """A row with an infinity gives plus or minus infinity by the weight's sign, NaN where the weight is 0; with two of them
+    or a NaN, what their sum is.  The other rows are those of a call without."""
+    note(f"matvec with infinities and NaN, {rows}x{cin} {x}")
+    cout = 40
+    code, fp4, amax = weights(1, cout, cin, cin)
+    w = decode.weights(code[0], fp4[0], amax[0])
+    t = torch.randn(rows, cin, generator=gen(rows)).to(TYPES[x])
+    args = on_gpu(code, fp4, amax)
+    good = lh.lh_matvec(t.to(DEV), *args).cpu()
+    for row, put in ((0, {3: "inf"}), (rows - 1, {cin - 1: "-inf"}), (rows // 2, {1: "inf", cin - 2: "inf"}),
+                     (0, {5: "nan"}), (rows - 1, {0: "inf", 17: "-inf"})):
+        bad = t.clone()
+        for at, v in put.items():
+            bad[row, at] = float(v)
+        got = lh.lh_matvec(bad.to(DEV), *args).cpu()
+        with np.errstate(invalid="ignore"):
+            want = np.stack([f64(bad[row, list(put)]) * w[c, list(put)] for c in range(cout)]).sum(1)
+        others = [r for r in range(rows) if r != row]
+        assert torch.equal(got[others], good[others])
+        assert np.array_equal(f64(got[row]), want, equal_nan=True), put
+
+
+def test_matvec_keeps_a_nan_of_any_payload():
+    note("matvec, NaN payloads")
+    code, fp4, amax = on_gpu(*weights(1, 24, 160, 2))
+    for bits in (0x7F800001, 0x7FC00000, -1, -0x7FFFFF):            # the last: 0xFF800001
+        t = torch.randn(3, 160, generator=gen(4))
+        t.view(torch.int32)[1, 40] = bits
+        y = lh.lh_matvec(t.to(DEV), code, fp4, amax).cpu()
+        assert torch.isnan(y[1]).all() and torch.isfinite(y[[0, 2]]).all()
