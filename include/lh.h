@@ -376,7 +376,8 @@ lh_status lh_matvec(const void* X, lh_dtype x_dtype, const float* x_scale, int64
  *                   group, with g a product by the rounded reciprocal (GPU tensor libraries
  *                   evaluate amax / 2688 that way; codes made there by this rule are the same)
  * k_amax, v_amax [n_heads] fp32 device: the calibrated largest magnitude per head (>= 0, finite;
- * see lh_absmax); larger elements saturate.  Codes are 16-byte, scales 4-byte aligned.
+ * see lh_absmax); larger elements and infinities saturate.  A NaN is held as a NaN code (E4M3) or as the
+ * NaN scale of its 16 elements (NVFP4) and reads back as NaN.  Codes are 16-byte, scales 4-byte aligned.
  */
 typedef enum {
   LH_CACHE_E4M3 = 0,

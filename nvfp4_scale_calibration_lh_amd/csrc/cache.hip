@@ -8,7 +8,8 @@
 //          even code, saturating at 448); the value is fp32(E4M3 * s)
 //   NVFP4: per 16 elements v = E4M3 nearest to max|x| / (6 g), g = fp32(amax * fp32(1/2688)), and
 //          nibbles E2M1 nearest to |x| / s, s = fp32(v g): the input quantizer's rule on this g
-// Every rounding decision is the one of the exact quotient.
+// Every rounding decision is the one of the exact quotient.  Infinities saturate like any large element; a NaN is
+// held as a NaN code, in E2M1, which has none, as a NaN scale of its block.
 //
 // Bound by memory where the instructions allow it: a lane owns a 16-element block (32 bytes of bf16),
 // consecutive lanes own consecutive blocks, and keys and values go in one launch (blockIdx.y).  Indices
@@ -187,6 +188,9 @@ __global__ __launch_bounds__(kThreads) void k_cache_write(const Args a) {
   const int64_t row = place(a, token, head);
   if (row < 0) return;
   const int64_t to = row + u;
+  bool nan = false;
+#pragma unroll
+  for (int k = 0; k < 16; k += 2) nan |= __builtin_isunordered(x[k], x[k + 1]);
   if constexpr (FOUR) {
     const float g = cache_unit(amax, true);
     const bool fast = g >= 0x1p-100f && g <= 0x1p100f;
@@ -199,10 +203,16 @@ __global__ __launch_bounds__(kThreads) void k_cache_write(const Args a) {
     const float s = __builtin_amdgcn_cvt_f32_fp8((int)code, 0) * g;
     const v2u nib = {e2m1_nibbles(x, s, fast), e2m1_nibbles(x + 8, s, fast)};
     ((v2u*)a.codes[kv])[to] = nib;
-    a.scales[kv][to] = (uint8_t)code;
+    a.scales[kv][to] = nan ? 0x7F : (uint8_t)code;
   } else {
     const float s = cache_unit(amax, false);
-    ((v4u*)a.codes[kv])[to] = e4m3_codes(x, s, s >= 0x1p-100f && s <= 0x1p100f);
+    v4u codes = e4m3_codes(x, s, s >= 0x1p-100f && s <= 0x1p100f);
+    if (nan) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        if (x[k] != x[k]) codes[k / 4] |= 0x7Fu << (8 * (k % 4));
+    }
+    ((v4u*)a.codes[kv])[to] = codes;
   }
 }
 

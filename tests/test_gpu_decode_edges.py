@@ -181,3 +181,53 @@ def test_matvec_keeps_a_nan_of_any_payload():
         t.view(torch.int32)[1, 40] = bits
         y = lh.lh_matvec(t.to(DEV), code, fp4, amax).cpu()
         assert torch.isnan(y[1]).all() and torch.isfinite(y[[0, 2]]).all()
+
+
+# ----------------------------------------------------------------------------------------- the cache
+def make_cache(pages, page, heads, dim, four, amax):
+    return lh.Cache.empty(pages, page, heads, dim, amax[0].to(DEV), amax[1].to(DEV), four_bit=four)
+
+
+@pytest.mark.parametrize("four", [True, False])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("amax", [3.0, 1e-34])
+def test_cache_holds_nan_and_saturates_infinities(four, dtype, amax):
+    """A NaN reads back as NaN, alone in E4M3 and with its 16 elements in NVFP4; an infinity is written as the largest finite
+    number would be; everything else is as without them.  Attention over a held NaN gives NaN to the heads that read it."""
+    note(f"cache of NaN and infinities, four {four} {dtype} amax {amax}")
+    tokens, heads, dim, t = 37, 2, 64, TYPES[dtype]
+    x = (torch.randn(2, tokens, heads, dim, generator=gen(6)) * amax / 3).to(t)
+    plain = x.clone()
+    big = torch.finfo(t).max
+    put = [(0, 3, 0, 5, "nan"), (0, 3, 0, 40, "-nan"), (1, 20, 1, 63, "nan"), (0, 9, 1, 0, "inf"), (1, 9, 1, 17, "-inf"), (1, 36, 0, 2, "nan")]
+    for i, tok, h, d, v in put:
+        x[i, tok, h, d] = float("nan") if "nan" in v else float(v)
+        if "nan" not in v:
+            plain[i, tok, h, d] = big if v == "inf" else -big
+    a = (torch.full((heads,), amax), torch.full((heads,), amax))
+    slots = torch.randperm(48, generator=gen(1))[:tokens].to(DEV)
+    back, caches = [], []
+    for data in (x, plain):
+        cache = make_cache(3, 16, heads, dim, four, a)
+        lh.lh_cache_write(cache, data[0].to(DEV), data[1].to(DEV), slots)
+        back.append(torch.stack(lh.lh_cache_read(cache, slots, dtype=torch.float32)).cpu())
+        caches.append(cache)
+    nan = torch.zeros(x.shape, dtype=torch.bool)
+    for i, tok, h, d, v in put:
+        if "nan" in v:
+            nan[i, tok, h, slice(d // 16 * 16, d // 16 * 16 + 16) if four else d] = True
+    assert torch.equal(torch.isnan(back[0]), nan)
+    assert torch.equal(back[0][~nan], back[1][~nan])
+    assert torch.isfinite(back[1]).all()
+
+    # tokens 0..36 in order, by pages of one token: head 0 meets the NaN of K, or of V past it; head 1 that of V
+    pages = {n: getattr(caches[0], n) for n in ("k", "v", "k_scale", "v_scale")}
+    def by_token(p):                     # noqa: E306
+        return None if p is None else p.permute(0, 2, 1, 3).reshape(48, heads, 1, -1).contiguous()
+    one = lh.Cache(by_token(pages["k"]), by_token(pages["v"]), caches[0].k_amax, caches[0].v_amax, by_token(pages["k_scale"]), by_token(pages["v_scale"]))
+    q = torch.randn(3, 2 * heads, dim, generator=gen(2)).to(t).to(DEV)
+    table = slots.to(torch.int32).expand(3, tokens).contiguous()
+    o = lh.lh_paged_attention(q, one, table, torch.tensor([3, 20, 37], dtype=torch.int32, device=DEV), scale=0.125).float().cpu()
+    assert torch.isfinite(o[0]).all() and torch.isfinite(o[1, 2:]).all()
+    assert torch.isnan(o[1, :2]).all() and torch.isnan(o[2, :2]).all()
+    assert torch.isnan(o[2, 2:]).any(-1).all()
