@@ -436,7 +436,7 @@ lh_status lh_cache_read(const lh_cache* cache, const int64_t* slots, int64_t tok
  * that is 0) that no other call uses until this one has run.
  * Errors: UNSUPPORTED for an unknown dtype or format, or another head_dim; INVALID_ARGUMENT as
  * lh_cache_write, n_q_heads not a positive multiple of n_heads, batch < 0, max_pages < 0,
- * max_pages * page_size over 2^31-1, a scale that is not finite, a short workspace.
+ * max_pages * page_size over 2^31-4096, a scale that is not finite, a short workspace.
  */
 lh_status lh_paged_attention(const lh_cache* cache, const void* Q, int64_t q_stride, lh_dtype dtype,
                              int64_t batch, int64_t n_q_heads, const int32_t* block_table,

@@ -38,6 +38,7 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kTile = 32;                    // tokens a wave takes at a time
 constexpr int kStep = kTile * kWaves;        // tokens a workgroup takes at a time
+static_assert(2 * kStep <= (int64_t(1) << 31) - kMaxContext, "positions fit 32 bits a step past the last token");
 constexpr int kHeads = 16;                   // query heads of one workgroup
 // Tokens below which a sequence is not split further: up to 512 one launch does (64 sequences of up to
 // 500 tokens 12.3 us against 19.1 with 256, 301 tokens 7.0 against 9.7)

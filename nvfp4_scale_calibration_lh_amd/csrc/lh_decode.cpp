@@ -190,7 +190,7 @@ lh_status check_attention(const lh::CacheView& c, int64_t batch, int64_t n_q_hea
   if (c.dim != 64 && c.dim != 128 && c.dim != 256) return fail(LH_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256 for attention (got %lld)", (long long)c.dim);
   if (n_q_heads < 1 || n_q_heads % c.heads) return fail(LH_ERR_INVALID_ARGUMENT, "n_q_heads must be a positive multiple of the cache's %lld heads (got %lld)", (long long)c.heads, (long long)n_q_heads);
   if (batch < 0) return fail(LH_ERR_INVALID_ARGUMENT, "batch must be >= 0 (got %lld)", (long long)batch);
-  if (max_pages < 0 || max_pages > kMaxInt / c.page_size) return fail(LH_ERR_INVALID_ARGUMENT, "max_pages * page_size must be in [0, 2^31-1]");
+  if (max_pages < 0 || max_pages > lh::kMaxContext / c.page_size) return fail(LH_ERR_INVALID_ARGUMENT, "max_pages * page_size must be in [0, 2^31-4096]");
   if (batch > kMaxInt / n_q_heads || lh::attention_grid(c, batch, n_q_heads / c.heads, max_pages) > kMaxInt)
     return fail(LH_ERR_INVALID_ARGUMENT, "too many sequences for one call");
   return LH_OK;

@@ -110,6 +110,10 @@ hipError_t launch_cache_write(const CacheView& c, const void* k, const void* v, 
 hipError_t launch_cache_read(const CacheView& c, const int64_t* slots, int64_t tokens, void* k, void* v, bool bf16,
                              hipStream_t stream);
 
+// Tokens of a sequence that attention takes at most: its positions are 32-bit, and a wave looks up to a step past
+// the last one.
+constexpr int64_t kMaxContext = (int64_t(1) << 31) - 4096;
+
 // Attention of one token per sequence; `share` query heads per key-value head.  attention_grid is
 // the launch's workgroups, attention_workspace its scratch in bytes (0: none).
 int64_t attention_grid(const CacheView& c, int64_t batch, int64_t share, int64_t width);
