@@ -21,6 +21,7 @@
 // p is made as 2^(s - m + 10) with m within 4 of the running maximum, so it stays under 2^14 and
 // tokens 2^-24 below the largest keep all fp16 bits; for fp32 it is two pieces as well.  Sums,
 // maxima and outputs are fp32.
+#include "attention_cut.hpp"
 #include "lh_internal.hpp"
 
 #include <algorithm>
@@ -37,12 +38,11 @@ typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kTile = 32;                    // tokens a wave takes at a time
-constexpr int kStep = kTile * kWaves;        // tokens a workgroup takes at a time
+constexpr int kStep = kAttentionStep;        // tokens a workgroup takes at a time
+static_assert(kStep == kTile * kWaves, "a step is a tile of every wave");
 static_assert(2 * kStep <= (int64_t(1) << 31) - kMaxContext, "positions fit 32 bits a step past the last token");
 constexpr int kHeads = 16;                   // query heads of one workgroup
-// Tokens below which a sequence is not split further: up to 512 one launch does (64 sequences of up to
-// 500 tokens 12.3 us against 19.1 with 256, 301 tokens 7.0 against 9.7)
-constexpr int kMinChunk = 512;
+constexpr int kMinChunk = kAttentionMinChunk;
 constexpr int kResident = 1024;              // workgroups that the registers let run at a time
 constexpr float kPBits = 10.0f;              // p = 2^(s - m + kPBits)
 
@@ -150,10 +150,10 @@ __device__ inline Unit find_unit(const Args& a, int unit, int b) {
   }
   if (a.splits > 0) {
     const int seq = b >= 0 ? b : unit / a.splits, base = seq * a.splits, len = length_of(a, seq);
-    const int part = max(((len + a.splits - 1) / a.splits + kStep - 1) / kStep * kStep, kMinChunk);
-    const int splits = max((len + part - 1) / part, 1), at = unit - base;
+    const EvenParts parts = even_parts(len, a.splits);
+    const int splits = (int)parts.count, at = unit - base;
     if (b < 0 && at >= splits) return {0, 0, 0, 0, 0, 0};
-    const int64_t from = (int64_t)at * part, to = from + part;
+    const int64_t from = (int64_t)at * parts.size, to = from + parts.size;
     return {seq, len, (int)min(from, (int64_t)len), (int)min(to, (int64_t)len), splits, base};
   }
   const int lane = threadIdx.x & 63;

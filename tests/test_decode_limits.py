@@ -1,7 +1,12 @@
 """Limits of the decode-step entry points and host arithmetic at them, without a GPU."""
 import ctypes
+import os
+import subprocess
+import tempfile
 
 import pytest
+
+import test_host_sanitize as base
 
 lh = pytest.importorskip("nvfp4_scale_calibration_lh_amd")
 
@@ -25,3 +30,12 @@ def test_attention_leaves_room_past_the_last_position(page):
         message = lh.lib().lh_last_error().decode()
         assert status == lh.LH_ERR_INVALID_ARGUMENT
         assert ("device" if fits else "max_pages") in message, message
+
+
+@pytest.mark.skipif(not os.path.exists(base.HIPCC), reason="hipcc is not installed")
+def test_parts_of_a_sequence_cover_it():
+    with tempfile.TemporaryDirectory() as d:
+        exe = os.path.join(d, "cut")
+        base._run([base.HIPCC, *base.COMMON, *base.SAN, "-x", "hip", os.path.join(base.ROOT, "tests", "host", "attention_cut_checks.cpp"), "-o", exe])
+        p = subprocess.run([exe], capture_output=True, text=True, timeout=60, env=dict(os.environ, ASAN_OPTIONS="detect_leaks=0"))
+        assert p.returncode == 0 and "ok: 0 failures" in p.stdout, p.stdout + p.stderr
