@@ -258,8 +258,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 && !F32 ? 4 : 1) void k_attentio
   const int last = len - 1;
   // The first row of a page in the codes, in tokens of one head; a page outside the cache is page 0.
   auto page_base = [&](int page) {
-    const int64_t p = (unsigned)page < (uint64_t)a.n_pages ? page : 0;
-    return (p * a.heads + kvh) * a.page_size;
+    return (page_or_first(page, a.n_pages) * a.heads + kvh) * a.page_size;
   };
   auto divide = [&](unsigned n) { return (unsigned)(((uint64_t)n * a.page_mul) >> a.page_shift); };
   // 16 tokens from t16 on: the row of the first, how many follow it up to the sequence's last token, and

@@ -10,6 +10,12 @@ constexpr int kAttentionStep = 128;          // tokens a workgroup takes at a ti
 // 500 tokens 12.3 us against 19.1 with 256, 301 tokens 7.0 against 9.7)
 constexpr int kAttentionMinChunk = 512;
 
+// An entry of a block table as a page of the cache: itself, or 0 outside it.  A negative one is outside caches of over
+// 2^32 pages, too.
+__host__ __device__ inline int64_t page_or_first(int page, int64_t n_pages) {
+  return (uint64_t)(int64_t)page < (uint64_t)n_pages ? page : 0;
+}
+
 // A sequence of len >= 0 tokens in at most `splits` parts of one size, a multiple of the step: the size and how many
 // there are (one of an empty sequence).  Unsigned, since len and a part add up to more than 2^31.
 struct EvenParts {

@@ -1,4 +1,4 @@
-// Host checks of how attention cuts a sequence into parts of one size, built with UndefinedBehaviorSanitizer
+// Host checks of how attention cuts a sequence into parts of one size and reads its table, built with UndefinedBehaviorSanitizer
 // (tests/test_decode_limits.py).
 #include <cstdint>
 #include <cstdio>
@@ -18,6 +18,14 @@ int main() {
                       size * count >= len && (len == 0 || size * (count - 1) < len);
       if (!ok) {
         std::fprintf(stderr, "FAIL %lld tokens in %d: %lld of %lld\n", (long long)len, splits, (long long)count, (long long)size);
+        ++failures;
+      }
+    }
+  for (int64_t pages : {int64_t(1), int64_t(3), int64_t(2147483647), int64_t(1) << 32, int64_t(1) << 40})
+    for (int64_t page : {int64_t(0), int64_t(1), int64_t(2), int64_t(3), int64_t(2147483647), int64_t(-1), int64_t(-7), -(int64_t(1) << 31)}) {
+      const int64_t got = lh::page_or_first((int)page, pages), want = page >= 0 && page < pages ? page : 0;
+      if (got != want) {
+        std::fprintf(stderr, "FAIL page %lld of %lld: %lld\n", (long long)page, (long long)pages, (long long)got);
         ++failures;
       }
     }

@@ -33,7 +33,7 @@ def test_attention_leaves_room_past_the_last_position(page):
 
 
 @pytest.mark.skipif(not os.path.exists(base.HIPCC), reason="hipcc is not installed")
-def test_parts_of_a_sequence_cover_it():
+def test_parts_of_a_sequence_cover_it_and_pages_are_in_the_cache():
     with tempfile.TemporaryDirectory() as d:
         exe = os.path.join(d, "cut")
         base._run([base.HIPCC, *base.COMMON, *base.SAN, "-x", "hip", os.path.join(base.ROOT, "tests", "host", "attention_cut_checks.cpp"), "-o", exe])
