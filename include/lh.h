@@ -399,8 +399,9 @@ typedef struct {
  * cache: HOST struct, read during the call.  K, V: element (t, head, i) at t * stride + head *
  * head_dim + i, strides in elements (at least n_heads * head_dim), so they may be parts of a wider
  * projection's rows; 16-byte aligned, strides multiples of 16 bytes.
- * slots [tokens] int64 device; a slot outside [0, n_pages * page_size) is skipped.  Slots named
- * twice in one call end with one of their tokens (either), head by head.
+ * slots [tokens] int64 device; a slot outside [0, n_pages * page_size) is skipped.  A slot named
+ * twice in one call is left with unspecified contents (its blocks' codes and scales are written apart, so
+ * they may be of either token, and a block may mix them); all other slots are as asked.
  * Errors: UNSUPPORTED for an unknown dtype or format; INVALID_ARGUMENT for n_pages, page_size,
  * n_heads or head_dim < 1, head_dim % 16, head_dim > 65536, n_heads * head_dim over 2^27,
  * page_size over 2^31-1, over 2^40 slots, a launch of over 2^31-1 workgroups, tokens < 0, bad strides, NULL required pointers or block scales that do not fit the

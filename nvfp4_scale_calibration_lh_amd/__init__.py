@@ -574,7 +574,8 @@ def _heads(t: torch.Tensor, name: str, heads: int, dim: int, dtype=None, tokens=
 
 def lh_cache_write(cache: Cache, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor) -> None:
     """Quantizes K, V [tokens, n_heads, head_dim] (fp32 or bf16; tokens may lie apart, as parts of a projection's
-    rows do) into the cache at slots [tokens] int64 (page * page_size + place; outside the cache: skipped)."""
+    rows do) into the cache at slots [tokens] int64 (page * page_size + place; outside the cache: skipped; named
+    twice in a call: contents unspecified)."""
     ks = _heads(K, "K", cache.n_heads, cache.head_dim)
     tokens = K.shape[0]
     vs = _heads(V, "V", cache.n_heads, cache.head_dim, K.dtype, tokens)

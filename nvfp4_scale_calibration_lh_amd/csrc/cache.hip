@@ -11,6 +11,9 @@
 // Every rounding decision is the one of the exact quotient.  Infinities saturate like any large element; a NaN is
 // held as a NaN code, in E2M1, which has none, as a NaN scale of its block.
 //
+// A lane writes its block's codes and scale by two plain stores, unordered against those of other lanes: slots of
+// one call are different ones, or their contents are unspecified.
+//
 // Bound by memory where the instructions allow it: a lane owns a 16-element block (32 bytes of bf16),
 // consecutive lanes own consecutive blocks, and keys and values go in one launch (blockIdx.y).  Indices
 // are split by multiplications with reciprocals from the host: with 32-bit divisions and 8 elements a

@@ -231,3 +231,26 @@ def test_cache_holds_nan_and_saturates_infinities(four, dtype, amax):
     assert torch.isfinite(o[0]).all() and torch.isfinite(o[1, 2:]).all()
     assert torch.isnan(o[1, :2]).all() and torch.isnan(o[2, :2]).all()
     assert torch.isnan(o[2, 2:]).any(-1).all()
+
+
+@pytest.mark.parametrize("four", [True, False])
+@pytest.mark.parametrize("dim", [96, 128, 272])
+def test_cache_slots_named_twice_disturb_no_other(four, dim):
+    """Tokens 3, 40 and 77 share a slot, whose contents are unspecified; every other one holds its token."""
+    note(f"cache, a slot named three times, dim {dim} four {four}")
+    heads, tokens = 3, 90
+    x = torch.randn(2, tokens, heads, dim, generator=gen(dim)).to(DEV)
+    a = (torch.full((heads,), 4.0), torch.full((heads,), 4.0))
+    slots = torch.randperm(7 * 16, generator=gen(9))[:tokens].to(DEV)
+    apart = make_cache(7, 16, heads, dim, four, a)
+    lh.lh_cache_write(apart, x[0], x[1], slots)
+    shared = slots.clone()
+    shared[40] = shared[77] = shared[3]
+    cache = make_cache(7, 16, heads, dim, four, a)
+    lh.lh_cache_write(cache, x[0], x[1], shared)
+    keep = torch.ones(tokens, dtype=torch.bool)
+    keep[[3, 40, 77]] = False
+    for got, want in zip(lh.lh_cache_read(cache, slots[keep.to(DEV)]), lh.lh_cache_read(apart, slots[keep.to(DEV)])):
+        assert torch.equal(got, want)
+    for got in lh.lh_cache_read(cache, slots[[40, 77]]):
+        assert torch.count_nonzero(got) == 0                       # not named any more: as they were
