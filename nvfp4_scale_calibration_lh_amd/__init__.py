@@ -517,7 +517,22 @@ def lh_matvec(X: torch.Tensor, code: torch.Tensor, fp4: torch.Tensor, amax: torc
 class Cache:
     """A paged key-value cache: its code tensors k, v [n_pages, n_heads, page_size, head_dim] uint8 (E4M3) or
     [..., head_dim/2] with block scales k_scale, v_scale [..., head_dim/16] uint8 (NVFP4), and the calibrated
-    amax per head k_amax, v_amax [n_heads] fp32.  `Cache.empty` makes the tensors."""
+    amax per head k_amax, v_amax [n_heads] fp32.  `Cache.empty` makes the tensors.
+
+    The tensors' addresses are read here once (reading them at each call would cost it 0.6 us), so the attributes cannot be
+    assigned or deleted afterwards: copy into the tensors, or make another Cache, which costs no device work."""
+
+    _FIXED = frozenset(("k", "v", "k_amax", "v_amax", "k_scale", "v_scale", "n_pages", "n_heads", "page_size", "head_dim", "struct", "ref"))
+
+    def __setattr__(self, name, value):
+        if name in self._FIXED and name in self.__dict__:
+            raise AttributeError(f"{name} of a Cache is fixed; copy into its tensors, or make another Cache")
+        object.__setattr__(self, name, value)
+
+    def __delattr__(self, name):
+        if name in self._FIXED:
+            raise AttributeError(f"{name} of a Cache is fixed; make another Cache")
+        object.__delattr__(self, name)
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_amax: torch.Tensor, v_amax: torch.Tensor,
                  k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None):
@@ -539,11 +554,11 @@ class Cache:
             scales = (pages, heads, page_size, dim // 16)
             _need(k_scale, "k_scale", scales, torch.uint8)
             _need(v_scale, "v_scale", scales, torch.uint8)
-        self.k, self.v, self.k_amax, self.v_amax, self.k_scale, self.v_scale = k, v, k_amax, v_amax, k_scale, v_scale
-        self.n_pages, self.n_heads, self.page_size, self.head_dim = pages, heads, page_size, dim
-        self.struct = CacheStruct(LH_CACHE_FP4 if four else LH_CACHE_E4M3, pages, page_size, heads, dim, k.data_ptr(),
-                                  v.data_ptr(), _ptr(k_scale), _ptr(v_scale), k_amax.data_ptr(), v_amax.data_ptr())
-        self.ref = ctypes.byref(self.struct)
+        struct = CacheStruct(LH_CACHE_FP4 if four else LH_CACHE_E4M3, pages, page_size, heads, dim, k.data_ptr(),
+                             v.data_ptr(), _ptr(k_scale), _ptr(v_scale), k_amax.data_ptr(), v_amax.data_ptr())
+        # past __setattr__, which would cost a microsecond
+        self.__dict__.update(k=k, v=v, k_amax=k_amax, v_amax=v_amax, k_scale=k_scale, v_scale=v_scale, n_pages=pages,
+                             n_heads=heads, page_size=page_size, head_dim=dim, struct=struct, ref=ctypes.byref(struct))
 
     @classmethod
     def empty(cls, n_pages: int, page_size: int, n_heads: int, head_dim: int, k_amax: torch.Tensor, v_amax: torch.Tensor, *,

@@ -254,3 +254,22 @@ def test_cache_slots_named_twice_disturb_no_other(four, dim):
         assert torch.equal(got, want)
     for got in lh.lh_cache_read(cache, slots[[40, 77]]):
         assert torch.count_nonzero(got) == 0                       # not named any more: as they were
+
+
+def test_cache_attributes_are_fixed():
+    """The kernels read the tensors that the Cache was made with; another one is refused, its values can be copied."""
+    note("cache, attributes assigned")
+    cache = make_cache(2, 16, 1, 64, True, (torch.ones(1), torch.ones(1)))
+    kept = {n: getattr(cache, n) for n in ("k", "v", "k_amax", "v_amax", "k_scale", "v_scale", "n_pages", "n_heads", "page_size", "head_dim")}
+    for name, value in kept.items():
+        with pytest.raises(AttributeError, match=name):
+            setattr(cache, name, value.clone() if torch.is_tensor(value) else value + 1)
+        with pytest.raises(AttributeError, match=name):
+            delattr(cache, name)
+        assert getattr(cache, name) is value
+    cache.label = "layer 3"                                        # the caller's own are not in the way
+    x, slots = torch.full((1, 1, 64), 8.0, device=DEV), torch.zeros(1, dtype=torch.int64, device=DEV)
+    for amax, held in ((1.0, 1.0), (4.0, 4.0)):                    # every element saturates
+        cache.k_amax.copy_(torch.tensor([amax]))
+        lh.lh_cache_write(cache, x, x, slots)
+        assert abs(float(lh.lh_cache_read(cache, slots, dtype=torch.float32)[0].max()) - held) <= 2 ** -22 * held
