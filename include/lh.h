@@ -331,7 +331,8 @@ lh_status lh_absmax(const void* W, lh_dtype w_dtype, int64_t n_groups, int64_t e
  * channels become 0); one in gamma makes its run's scale NaN or infinite.  q is 0 where the scale is
  * not finite.  The sum of squares keeps fp32's range: a row over it (elements near 2^60) gives zeros, and
  * with eps = 0 one under it (near 2^-60) loses bits and then gives zeros.
- * Errors: INVALID_ARGUMENT for rows < 0 or over 2^31-1, cin <= 0 or cin % 16 or cin > 2^24, a group
+ * Errors: INVALID_ARGUMENT for rows < 0 or more than a launch takes (2^26-4 rows of up to 1024 bf16 or 512
+ * fp32 channels, 2^24-1 of up to 16384 or 8192, 2^22-1 longer ones), cin <= 0 or cin % 16 or cin > 2^24, a group
  * other than 0 and 128, a bad eps, R without summed or the reverse, NULL required pointers,
  * misaligned, non-device or mixed-device pointers.
  */
@@ -356,7 +357,7 @@ lh_status lh_rms_norm_quant(const void* X, const void* R, lh_dtype dtype, int64_
  * Groups as everywhere; a group without rows is skipped.  Any number of rows works; the weights are
  * read again for every 64 rows (16 per group with several groups).
  * Errors: INVALID_ARGUMENT for the shapes of lh_accumulate and lh_scale_sweep, cin > 2^24, a launch of
- * over 2^31-1 workgroups, scale_norm that is not a positive finite E4M3 value, x_scale or x_group
+ * 2^32 or more work-items, scale_norm that is not a positive finite E4M3 value, x_scale or x_group
  * that do not fit the type, NULL required pointers, misaligned, non-device or mixed-device pointers.
  */
 lh_status lh_matvec(const void* X, lh_dtype x_dtype, const float* x_scale, int64_t x_group, int64_t rows,
@@ -404,8 +405,8 @@ typedef struct {
  * they may be of either token, and a block may mix them); all other slots are as asked.
  * Errors: UNSUPPORTED for an unknown dtype or format; INVALID_ARGUMENT for n_pages, page_size,
  * n_heads or head_dim < 1, head_dim % 16, head_dim > 65536, n_heads * head_dim over 2^27,
- * page_size over 2^31-1, over 2^40 slots, a launch of over 2^31-1 workgroups, tokens < 0, bad strides, NULL required pointers or block scales that do not fit the
- * format, misaligned, non-device or mixed-device pointers.
+ * page_size over 2^31-1, over 2^40 slots, a launch of 2^32 or more work-items (one for 16 elements),
+ * tokens < 0, bad strides, NULL required pointers or block scales that do not fit the format, misaligned, non-device or mixed-device pointers.
  */
 lh_status lh_cache_write(const lh_cache* cache, const void* K, int64_t k_stride, const void* V,
                          int64_t v_stride, lh_dtype dtype, int64_t tokens, const int64_t* slots,
@@ -437,7 +438,8 @@ lh_status lh_cache_read(const lh_cache* cache, const int64_t* slots, int64_t tok
  * that is 0) that no other call uses until this one has run.
  * Errors: UNSUPPORTED for an unknown dtype or format, or another head_dim; INVALID_ARGUMENT as
  * lh_cache_write, n_q_heads not a positive multiple of n_heads, batch < 0, max_pages < 0,
- * max_pages * page_size over 2^31-4096, a scale that is not finite, a short workspace.
+ * max_pages * page_size over 2^31-4096, a launch of 2^32 or more work-items (256 for a sequence's 16 query
+ * heads of a key-value head), a scale that is not finite, a short workspace.
  */
 lh_status lh_paged_attention(const lh_cache* cache, const void* Q, int64_t q_stride, lh_dtype dtype,
                              int64_t batch, int64_t n_q_heads, const int32_t* block_table,

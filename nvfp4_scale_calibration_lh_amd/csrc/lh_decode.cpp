@@ -73,6 +73,12 @@ lh_status check_stride(int64_t stride, int64_t least, lh_dtype dtype, const char
   return LH_OK;
 }
 
+// Status of a call whose launch returned e.
+lh_status launched(hipError_t e, const char* what) {
+  if (e == hipErrorInvalidConfiguration) return fail(LH_ERR_INVALID_ARGUMENT, "%s: too large for one call (2^32 work-items or more)", what);
+  return e == hipSuccess ? ok() : hip_fail(e, what);
+}
+
 }  // namespace
 
 extern "C" {
@@ -98,8 +104,7 @@ lh_status lh_rms_norm_quant(const void* X, const void* R, lh_dtype dtype, int64_
   if ((st = guard.enter(dev)) != LH_OK) return st;
   const hipError_t e = lh::launch_rms_norm(X, R, dtype == LH_DTYPE_BF16, rows, cin, gamma, eps, group != 0, summed, q, q_scale,
                                            reinterpret_cast<hipStream_t>(stream));
-  if (e != hipSuccess) return hip_fail(e, "norm launch");
-  return ok();
+  return launched(e, "norm launch");
 }
 
 lh_status lh_matvec(const void* X, lh_dtype x_dtype, const float* x_scale, int64_t x_group, int64_t rows,
@@ -132,8 +137,7 @@ lh_status lh_matvec(const void* X, lh_dtype x_dtype, const float* x_scale, int64
   const hipError_t e = lh::launch_matvec(X, eight ? 2 : (x_dtype == LH_DTYPE_F32 ? 1 : 0), x_scale, x_group ? (cin + 127) / 128 : 1, rows,
                                          cin, cout, n_groups > 1 ? group_offsets : nullptr, n_groups, scale_code, fp4, global_amax,
                                          6.0f * scale_norm, Y, reinterpret_cast<hipStream_t>(stream));
-  if (e != hipSuccess) return hip_fail(e, "matvec launch");
-  return ok();
+  return launched(e, "matvec launch");
 }
 
 lh_status lh_cache_write(const lh_cache* cache, const void* K, int64_t k_stride, const void* V,
@@ -157,8 +161,7 @@ lh_status lh_cache_write(const lh_cache* cache, const void* K, int64_t k_stride,
   if ((st = guard.enter(dev)) != LH_OK) return st;
   const hipError_t e = lh::launch_cache_write(c, K, V, dtype == LH_DTYPE_BF16, tokens, k_stride, v_stride, slots,
                                               reinterpret_cast<hipStream_t>(stream));
-  if (e != hipSuccess) return hip_fail(e, "cache write launch");
-  return ok();
+  return launched(e, "cache write launch");
 }
 
 lh_status lh_cache_read(const lh_cache* cache, const int64_t* slots, int64_t tokens, lh_dtype dtype,
@@ -178,8 +181,7 @@ lh_status lh_cache_read(const lh_cache* cache, const int64_t* slots, int64_t tok
   DeviceGuard guard;
   if ((st = guard.enter(dev)) != LH_OK) return st;
   const hipError_t e = lh::launch_cache_read(c, slots, tokens, K, V, dtype == LH_DTYPE_BF16, reinterpret_cast<hipStream_t>(stream));
-  if (e != hipSuccess) return hip_fail(e, "cache read launch");
-  return ok();
+  return launched(e, "cache read launch");
 }
 
 }  // extern "C"
@@ -232,8 +234,7 @@ lh_status lh_paged_attention(const lh_cache* cache, const void* Q, int64_t q_str
   if ((st = guard.enter(dev)) != LH_OK) return st;
   const hipError_t e = lh::launch_attention(c, Q, dtype == LH_DTYPE_BF16, batch, share, q_stride, block_table, max_pages, lengths, scale, O,
                                             workspace, reinterpret_cast<hipStream_t>(stream));
-  if (e != hipSuccess) return hip_fail(e, "attention launch");
-  return ok();
+  return launched(e, "attention launch");
 }
 
 }  // extern "C"

@@ -273,3 +273,35 @@ def test_cache_attributes_are_fixed():
         cache.k_amax.copy_(torch.tensor([amax]))
         lh.lh_cache_write(cache, x, x, slots)
         assert abs(float(lh.lh_cache_read(cache, slots, dtype=torch.float32)[0].max()) - held) <= 2 ** -22 * held
+
+
+# ----------------------------------------------------------------------------------- launches' limits
+def test_norm_of_as_many_rows_as_a_launch_takes():
+    rows, cin = 2 ** 26, 16
+    note(f"norm of {rows} rows, refused, and of 4 fewer")
+    x = torch.empty(rows, cin, dtype=torch.bfloat16, device=DEV)
+    gamma = torch.ones(cin, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(lh.LHError) as e:
+        lh.lh_rms_norm_quant(x, gamma)
+    assert e.value.code == lh.LH_ERR_INVALID_ARGUMENT and "too large" in e.value.message
+    x[-5:] = torch.randn(5, cin, generator=gen(3)).bfloat16()
+    x[:5] = x[-5:]
+    q, s, _ = lh.lh_rms_norm_quant(x[:-4], gamma)
+    assert torch.equal(s[-1], s[0]) and torch.equal(q[-1].view(torch.uint8), q[0].view(torch.uint8)) and float(s[0]) > 0
+
+
+def test_attention_of_more_sequences_than_a_launch_takes():
+    batch, heads = 2 ** 21, 8
+    note(f"attention of {batch} sequences of {heads} heads, refused, and of one fewer, all but one empty")
+    cache = make_cache(2, 16, heads, 64, True, (torch.ones(heads), torch.ones(heads)))
+    cache.v.fill_(0x22)                                            # 1.0
+    cache.v_scale.fill_(0x38)                                      # 1.0
+    q = torch.empty(batch, heads, 64, dtype=torch.bfloat16, device=DEV)
+    table, lengths = torch.ones(batch, 1, dtype=torch.int32, device=DEV), torch.zeros(batch, dtype=torch.int32, device=DEV)
+    with pytest.raises(lh.LHError) as e:
+        lh.lh_paged_attention(q, cache, table, lengths, scale=0.125)
+    assert e.value.code == lh.LH_ERR_INVALID_ARGUMENT and "too large" in e.value.message
+    q[-2] = 0
+    lengths[-2] = 11
+    o = lh.lh_paged_attention(q[:-1], cache, table[:-1], lengths[:-1], scale=0.125)
+    assert torch.count_nonzero(o[:-1]) == 0 and bool((o[-1] == torch.tensor(1 / 2688.0).bfloat16().to(DEV)).all())
