@@ -5,26 +5,11 @@ import pytest
 import torch
 
 from oracle import decode
+from test_gpu_decode import DEV, TYPES, U, f64, gen, lh, make_cache, note, weights
 
 pytestmark = pytest.mark.gpu
 
-lh = pytest.importorskip("nvfp4_scale_calibration_lh_amd")
-DEV = torch.device("cuda:0") if torch.cuda.is_available() else None
-TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
-U = 2.0 ** -24                       # fp32 unit roundoff
 TINY = 2.0 ** -149                   # the smallest fp32 number
-
-
-def note(msg):
-    print(f"[case] {msg}", flush=True)
-
-
-def gen(seed):
-    return torch.Generator().manual_seed(seed)
-
-
-def f64(t):
-    return t.detach().cpu().double().numpy()
 
 
 # ----------------------------------------------------------------------------------------- the norm
@@ -135,14 +120,6 @@ def test_norm_writes_the_code_nearest_to_the_quotient(dtype, cin, group):
 
 
 # -------------------------------------------------------------------------------------- the products
-def weights(groups, cout, cin, seed):
-    r = np.random.default_rng(seed)
-    code = r.integers(1, 127, (groups, cout, cin // 16)).astype(np.uint8)
-    fp4 = r.integers(0, 256, (groups, cout, cin // 2)).astype(np.uint8)
-    amax = (0.1 + r.random(groups)).astype(np.float32)
-    return code, fp4, amax
-
-
 def on_gpu(*arrays):
     return [torch.from_numpy(a).to(DEV) for a in arrays]
 
@@ -184,10 +161,6 @@ def test_matvec_keeps_a_nan_of_any_payload():
 
 
 # ----------------------------------------------------------------------------------------- the cache
-def make_cache(pages, page, heads, dim, four, amax):
-    return lh.Cache.empty(pages, page, heads, dim, amax[0].to(DEV), amax[1].to(DEV), four_bit=four)
-
-
 @pytest.mark.parametrize("four", [True, False])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("amax", [3.0, 1e-34])
