@@ -160,6 +160,22 @@ def test_matvec_keeps_a_nan_of_any_payload():
         assert torch.isnan(y[1]).all() and torch.isfinite(y[[0, 2]]).all()
 
 
+def test_matvec_of_the_smallest_fp32_rows():
+    """The three bf16 pieces of an fp32 element hold it to within 2^-133, the smallest bf16 number, and exactly from 2^-110 on."""
+    rows, cin, cout = 6, 272, 24
+    note("matvec of fp32 rows from 2^-149 to 2^-100")
+    code, fp4, _ = weights(1, cout, cin, 8)
+    amax = np.array([2.0 ** 110], np.float32)
+    x = torch.randn(rows, cin, generator=gen(8)) * torch.tensor([2.0 ** -e for e in (100, 111, 118, 126, 133, 145)])[:, None]
+    y = f64(lh.lh_matvec(x.to(DEV), *on_gpu(code, fp4, amax)))
+    w = decode.weights(code[0], fp4[0], amax[0])
+    held = np.where(np.abs(f64(x)) >= 2.0 ** -110, 0.0, 2.0 ** -133)
+    tol = 2 * (cin + 8) * U * (np.abs(f64(x)) @ np.abs(w).T) + held @ np.abs(w).T
+    # a sum of products under fp32's normal numbers is itself held to 2^-149 a term, times the matrix' scale
+    tol = tol + cin * TINY * float(amax[0] / np.float32(2688.0))
+    assert np.all(np.abs(y - f64(x) @ w.T) <= tol)
+
+
 # ----------------------------------------------------------------------------------------- the cache
 @pytest.mark.parametrize("four", [True, False])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -278,3 +294,39 @@ def test_attention_of_more_sequences_than_a_launch_takes():
     lengths[-2] = 11
     o = lh.lh_paged_attention(q[:-1], cache, table[:-1], lengths[:-1], scale=0.125)
     assert torch.count_nonzero(o[:-1]) == 0 and bool((o[-1] == torch.tensor(1 / 2688.0).bfloat16().to(DEV)).all())
+
+
+# ----------------------------------------------------------------------------------------- attention
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("four", [True, False])
+def test_attention_holds_q_to_a_part_of_its_largest_element(dtype, four):
+    """Two tokens, equal but for element 1 of K, which is 1 and 0; V is 1 and 0, so o is the logistic function of scale * q1 and
+    gives q1 back as it was held.  q's largest element meets zeros of K.  The bound is 2^-39 of it, and nothing at all (for
+    fp32 2^-22 of q1) for elements from 2^-31 of it on."""
+    note(f"attention, q far apart, four {four} {dtype}")
+    t, one = TYPES[dtype], 0x38                                    # E4M3's 1, also a scale's
+    amax = 2688.0 if four else 448.0
+    cache = make_cache(1, 2, 1, 64, four, (torch.tensor([amax]), torch.tensor([amax])))
+    for tensor, scales, at in ((cache.k, cache.k_scale, 1), (cache.v, cache.v_scale, slice(0, 64))):
+        values = torch.zeros(64, dtype=torch.uint8)
+        values[at] = 2 if four else one
+        tensor[0, 0, 0] = (values[0::2] | (values[1::2] << 4) if four else values).to(DEV)
+        if four:
+            scales.fill_(one)
+    table, lengths = torch.zeros(1, 1, dtype=torch.int32, device=DEV), torch.tensor([2], dtype=torch.int32, device=DEV)
+    for top in (2.0 ** 14, 1.99 * 2.0 ** 14, 2.0 ** 40, 3e-20):
+        for e in (-10, -22, -29, -31, -33, -35, -37, -38):
+            for f in (1.0, 1.296875, 1.5, 1.703125, -1.9921875):
+                q = torch.zeros(1, 1, 64, dtype=torch.float64)
+                q[0, 0, 0], q[0, 0, 1] = top, f * 2.0 ** e * top
+                q = q.to(t)
+                q0, q1 = float(q[0, 0, 0]), float(q[0, 0, 1])
+                scale = float(np.float32(1.0 / abs(q1)))
+                o = float(lh.lh_paged_attention(q.to(DEV), cache, table, lengths, scale=scale)[0, 0, 0])
+                held = np.log(o / (1 - o)) / scale
+                # o is off by its type's rounding and a few fp32 ones; d log(o / (1 - o)) = do / (o (1 - o))
+                off = ((2.0 ** -9 if dtype == "bf16" else 0) + (2.0 ** -11 if dtype == "bf16" else 2.0 ** -21) + 16 * U) * o / (o * (1 - o)) / scale
+                bound = 0.0 if abs(q1) >= 2.0 ** -31 * q0 else 2.0 ** -39 * q0
+                if dtype == "f32":
+                    bound = max(2.0 ** -39 * q0, 2.0 ** -22 * abs(q1))
+                assert abs(held - q1) <= bound + off, (top, e, f, held / q1, bound / abs(q1), off / abs(q1))
