@@ -345,8 +345,8 @@ lh_status lh_rms_norm_quant(const void* X, const void* R, lh_dtype dtype, int64_
  * decode step's tokens, drafted tokens, small batches):
  *   Y[t,c] = sum_k Wq[g][c][k] x[t,k] for the rows t of group g,
  *   Wq[g][c][k] = E2M1(nibble) * v_code * g_g,  g_g = fp32(global_amax[g] / (6 * scale_norm)),
- * that is lh_dequantize_ex's weights before their rounding.  Products are exact and sums fp32, in a
- * fixed order; g_g multiplies the sum, which is rounded once to Y's type.
+ * that is lh_dequantize_ex's weights before their rounding.  Products are exact (an fp32 element under
+ * 2^-110 enters to within 2^-133) and sums fp32, in a fixed order; g_g multiplies the sum, which is rounded once to Y's type.
  * Infinities and NaN in a row of X give what the row's sums of products are, and change no other row.
  * scale_code [n_groups, cout, cin/16], fp4 [n_groups, cout, cin/2] (8-byte aligned), global_amax
  * [n_groups], scale_norm as in lh_sweep_options.
@@ -355,7 +355,8 @@ lh_status lh_rms_norm_quant(const void* X, const void* R, lh_dtype dtype, int64_
  * writes them; x_scale is NULL and x_group 0 for the other types.
  * Y [rows, cout]: F32 for F32 rows, BF16 otherwise.
  * Groups as everywhere; a group without rows is skipped.  Any number of rows works; the weights are
- * read again for every 64 rows (16 per group with several groups).
+ * read again for every 64 rows (32 of fp32), with several groups for every 16 rows of a group (4 of fp32, and
+ * where 4 * rows <= n_groups).
  * Errors: INVALID_ARGUMENT for the shapes of lh_accumulate and lh_scale_sweep, cin > 2^24, a launch of
  * 2^32 or more work-items, scale_norm that is not a positive finite E4M3 value, x_scale or x_group
  * that do not fit the type, NULL required pointers, misaligned, non-device or mixed-device pointers.
@@ -430,8 +431,10 @@ lh_status lh_cache_read(const lh_cache* cache, const int64_t* slots, int64_t tok
  * lengths [batch] int32 device.  A length is taken as between 0 and max_pages * page_size; a
  * sequence of length 0 gives zeros.  Entries of the table past a sequence's last page are not
  * read; a page outside the cache is read as page 0.  head_dim is 64, 128 or 256.
- * K and V enter exactly; q is held to 2^-40 of its head's largest element (fp32: to 2^-22 of each
- * element too), p to fp16 (fp32: two fp16 pieces), and maxima, sums and outputs are fp32.
+ * K and V enter exactly; q is held to 2^-39 of its head's largest element (bf16: exactly from 2^-31 of it
+ * on; fp32: to 2^-22 of each element too), p to fp16 (fp32: two fp16 pieces), and maxima, sums and outputs
+ * are fp32.  A NaN or an infinity in a head's q gives that head NaN, a NaN key or value of the sequence's
+ * tokens the outputs that depend on it.
  * Two calls with the same arguments give the same bits; where a sequence is cut depends on all
  * lengths of the batch, so beside other sequences its last bits may differ.
  * workspace: device memory of at least lh_paged_attention_workspace bytes (16-byte aligned; NULL if

@@ -17,7 +17,8 @@
 // Every code is exact in fp16: E2M1 times its E4M3 block scale has at most 6 significant bits in
 // [2^-10, 2688], E4M3 has 4 in [2^-9, 448]; the heads' global scales multiply scores and outputs.
 // q is multiplied by the power of two that brings its head's largest element to [2^14, 2^15):
-// bf16 then fits fp16 exactly down to 2^-40 of that element, fp32 is held as two fp16 pieces.
+// bf16 then fits fp16 exactly down to 2^-31 of that element and to within 2^-39 of it below, fp32 is held as
+// two fp16 pieces.
 // p is made as 2^(s - m + 10) with m within 4 of the running maximum, so it stays under 2^14 and
 // tokens 2^-24 below the largest keep all fp16 bits; for fp32 it is two pieces as well.  Sums,
 // maxima and outputs are fp32.

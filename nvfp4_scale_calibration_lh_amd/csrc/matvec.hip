@@ -16,7 +16,8 @@
 //
 // E2M1 * E4M3 has at most 6 significant bits, so it is exact in bf16 (bf16 and fp32 x) and, its
 // range being [2^-10, 2688], in fp16 (E4M3 x, also exact in fp16).  fp32 x is split into three
-// bf16 pieces, exactly where the last is a normal number (|x| above 2^-109).  Every product is exact; sums are fp32.
+// bf16 pieces, exactly from 2^-110 on; a smaller x loses its bits under 2^-133, the smallest bf16 number (the
+// matrix instructions take subnormal numbers).  Every product is exact; sums are fp32.
 #include "lh_internal.hpp"
 
 #include <algorithm>

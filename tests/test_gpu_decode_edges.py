@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from oracle import decode
-from test_gpu_decode import DEV, TYPES, U, f64, gen, lh, make_cache, note, weights
+from test_gpu_decode import DEV, TYPES, U, attention_case, f64, gen, lh, make_cache, note, weights
 
 pytestmark = pytest.mark.gpu
 
@@ -158,6 +158,23 @@ def test_matvec_keeps_a_nan_of_any_payload():
         t.view(torch.int32)[1, 40] = bits
         y = lh.lh_matvec(t.to(DEV), code, fp4, amax).cpu()
         assert torch.isnan(y[1]).all() and torch.isfinite(y[[0, 2]]).all()
+
+
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("cin", [144, 2064, 4112])
+def test_matvec_of_nan_codes_and_scales(group, cin):
+    """A NaN code or a NaN scale of an E4M3 row, as the norm writes it, makes the row NaN and no other."""
+    note(f"matvec with NaN codes, cin {cin} group {group}")
+    rows = 6
+    args = on_gpu(*weights(1, 40, cin, 1))
+    q = (torch.randn(rows, cin, generator=gen(cin)) * 20).to(torch.float8_e4m3fn)
+    s = torch.rand(rows, -(-cin // 128) if group else 1, generator=gen(3)) + 0.5
+    good = lh.lh_matvec(q.to(DEV), *args, x_scale=s.to(DEV), x_group=group).cpu()
+    bq, bs = q.clone(), s.clone()
+    bq.view(torch.uint8)[1, cin - 3], bs[4, -1] = 0xFF, float("nan")
+    bq.view(torch.uint8)[4] = 0                                    # the codes under it are 0
+    got = lh.lh_matvec(bq.to(DEV), *args, x_scale=bs.to(DEV), x_group=group).cpu()
+    assert torch.isnan(got[[1, 4]]).all() and torch.equal(got[[0, 2, 3, 5]], good[[0, 2, 3, 5]])
 
 
 def test_matvec_of_the_smallest_fp32_rows():
@@ -330,3 +347,19 @@ def test_attention_holds_q_to_a_part_of_its_largest_element(dtype, four):
                 if dtype == "f32":
                     bound = max(2.0 ** -39 * q0, 2.0 ** -22 * abs(q1))
                 assert abs(held - q1) <= bound + off, (top, e, f, held / q1, bound / abs(q1), off / abs(q1))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("four", [True, False])
+def test_attention_of_queries_with_nan_and_infinities(dtype, four):
+    """Such a head gives NaN, the others what they give without it; an empty sequence gives 0 all the same."""
+    note(f"attention, NaN and infinite q, four {four} {dtype}")
+    cache, table, lengths, q, _ = attention_case([700, 0, 33], 2, 4, 64, 16, four, dtype, 12)
+    good = lh.lh_paged_attention(q.to(DEV), cache, table, lengths, scale=0.125)
+    bad = q.clone()
+    bad[0, 1, 5], bad[0, 6, 63], bad[1, 0, 0], bad[2, 3, 9] = float("nan"), float("inf"), float("nan"), -float("inf")
+    o = lh.lh_paged_attention(bad.to(DEV), cache, table, lengths, scale=0.125)
+    nan = torch.zeros(3, 8, dtype=torch.bool, device=DEV)
+    nan[0, 1] = nan[0, 6] = nan[2, 3] = True
+    assert torch.isnan(o[nan]).all() and torch.equal(o[~nan], good[~nan])
+    assert torch.count_nonzero(o[1]) == 0
