@@ -106,7 +106,7 @@ __device__ inline unsigned block_code(float top, float g) {
   const float t = top * __builtin_amdgcn_rcpf(6.0f * g);
   const unsigned c = (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(fminf(t * kUp, 448.0f), fminf(t * kDown, 448.0f), 0, false);
   const unsigned up = c & 255u, dn = (c >> 8) & 255u;
-  return up == dn ? up : e4m3_resolve<6>(top, g, dn);
+  return up == dn ? up : e4m3_resolve6(top, g, dn);
 }
 
 // Sixteen signed E4M3 bytes of x / s.  s outside [2^-100, 2^100] (not fast) decides on float64 quotients.
