@@ -8,7 +8,9 @@
 // the four waves take 32-token tiles in turn, each with a running maximum and sum of its own, and
 // meet in LDS at the end.  NVFP4, head dimension 128: 4 sequences of 131001 tokens, 64 heads on 8,
 // 115 us (604 MB, 5.2 TB/s) and 5 us for the join; 48 sequences of up to 8191 tokens, 32 heads on 8, 54
-// us (234 MB, 4.3 TB/s) and 5 us; 301 tokens of one sequence in E4M3 6.6 us.
+// us (234 MB, 4.3 TB/s) and 5 us; 301 tokens of one sequence in E4M3 6.6 us.  Whole calls of the two long cases: 59 and
+// 120 us in NVFP4, 89 and 193 in E4M3; with fp32 q and o 64 and 127, 89 and 193, off the 64-bit result by 4.5e-7 and
+// 6.4e-7 of it (products and sums in plain fp32: 8.8e-7 and 2.3e-6), with bf16 by its rounding, 1.7e-3.
 //
 // A tile is two matrix products without any exchange between lanes:
 //   S^T = K Q^T   A = 16 tokens of K, B = the heads' q; the result's lane (head, quarter) holds
@@ -140,8 +142,8 @@ struct Unit {
 
 // The unit-th part over all sequences in order, or sequence b if b >= 0; splits is 0 past the last part.
 // Up to 64 sequences are cut to parts of one length, from the tokens of all of them, so that uneven
-// sequences keep the compute units evenly busy (48 of up to 8191 tokens in NVFP4 61 us, in E4M3 91, against
-// 70 and 102 where each was cut into as many parts as the others); every wave finds its part by a
+// sequences keep the compute units evenly busy (48 of up to 8191 tokens in NVFP4 59 us, in E4M3 89, against
+// 68 and 100 where each was cut into as many parts as the others); every wave finds its part by a
 // scan over its lanes.  More sequences get the same number of parts each: they even out, and a scan
 // would be several dependent loads (300 sequences of one head 57 us with one, 53 without).
 __device__ inline Unit find_unit(const Args& a, int unit, int b) {
@@ -543,7 +545,7 @@ __global__ __launch_bounds__(kThreads) void k_attention_join(const Args a) {
 // one more a sequence, or if those are more than `units`, into `least` and one a sequence.  A part that is alone on its sequence is finished by its workgroup, so sequences that
 // fill the card are not cut (128 of up to 3000 tokens on 8 heads 56 us, cut 68).  Few long sequences are
 // cut to what is resident at a time, more of them to half of that, so that the last parts end together (7 of up
-// to 60000 tokens 64 us against 69, 48 of up to 8191 61 against 67).
+// to 60000 tokens 61 us against 65, 48 of up to 8191 59 against 66).
 struct Cut {
   int splits, budget, least;
   int64_t units;                             // parts for each head, at most

@@ -17,8 +17,8 @@
 // Bound by memory where the instructions allow it: a lane owns a 16-element block (32 bytes of bf16),
 // consecutive lanes own consecutive blocks, and keys and values go in one launch (blockIdx.y).  Indices
 // are split by multiplications with reciprocals from the host: with 32-bit divisions and 8 elements a
-// lane, 8191 tokens of 8 x 128 took 16 us to write, bound by instructions.  Now 11.8 us (43 MB, 3.6
-// TB/s) and 10.4 us to read back; 30011 tokens of 4 x 64 in E4M3 11.0 and 10.4 us.
+// lane, 8191 tokens of 8 x 128 took 16 us to write, bound by instructions.  Now 12.3 us (43 MB, 3.5
+// TB/s) and 11.8 us to read back; 30011 tokens of 4 x 64 in E4M3 11.4 and 11.8 us (traced medians).
 #include "acc_stream.hpp"
 #include "e4m3.hpp"
 #include "lh_internal.hpp"

@@ -9,9 +9,9 @@
 // (k in any order, as long as both operands have the same).  The waves of a workgroup share k among
 // them and add their sums in LDS in a fixed order.
 //
-// 12288x4096: one bf16 row 10 us, sixteen E4M3 rows 11 us, 64 bf16 rows 44 us; 4096x12288 with five fp32
-// rows 16.5 us; 2048x2048 with one row 3.8 us; 320 bf16 rows over 512 experts of 1280x2560, 135 of them
-// hit, 76 us (242 MB, 3.2 TB/s); 98304x4096 with one row 50 us (4.5 TB/s).  Reading the weights alone in
+// 12288x4096: one bf16 row 9.3 us, sixteen E4M3 rows 11 us, 32 bf16 rows 19 us, 64 44 us; 4096x12288 with five fp32
+// rows 16.5 us; 2048x2048 with one row 4.4 us traced; 320 bf16 rows over 512 experts of 1280x2560, 135 of them
+// hit, 77 us (242 MB, 3.1 TB/s); 98304x4096 with one row 50 us (4.5 TB/s).  Reading the weights alone in
 // this pattern takes 5.5 us at 12288x4096 (4.6 TB/s).
 //
 // E2M1 * E4M3 has at most 6 significant bits, so it is exact in bf16 (bf16 and fp32 x) and, its
@@ -571,7 +571,11 @@ hipError_t launch_tile(Args a, hipStream_t stream) {
   const int waves = (chunks + U * steps - 1) / (U * steps);
   const int64_t pieces = a.n_groups == 1 ? (a.rows + rows - 1) / rows : a.rows / rows + std::min(a.n_groups, a.rows);
   const int64_t resident = kComputeUnits * std::max((U <= 2 ? 16 : 8) / waves, 1) * (a.n_groups == 1 ? 1 : 4);
-  // 8 tiles were better than 4 or 16 for one large matrix, 16 than 8 for several (the rows of x are fetched less often)
+  // 8 tiles were better than 4 or 16 for one large matrix, 16 than 8 or 32 for several (more fetch the rows of x less
+  // often, fewer even out better): 512 experts of 1280x2560 with 320 rows 75 us against 89 and 85, 384 of 1536x2560 with
+  // 256 76, 82, 86, 256 of 2048x2048 with 512 81, 92, 83, 128 of 4096x1024 with 256 53, 60, 52.  Four times the
+  // workgroups that are resident were better than twice or eight times that for 256 of 1280x2560 with 64 rows
+  // (28 us, 33, 31) and within 4% of the best elsewhere.
   a.run = (int)std::min<int64_t>((pieces * tiles + resident - 1) / resident, a.n_groups == 1 ? 8 : 16);
   // Of several matrices, whole sets of the tiles whose sums meet in LDS together, so that a workgroup's start is shared,
   // if every compute unit still has one (48 rows over 64 of 1280x1280 16.9 us without, 11.1 with; 32 over 128 of
