@@ -43,7 +43,9 @@
  *
  * The entry points of a decode step (lh_rms_norm_quant, lh_matvec, lh_cache_write, lh_cache_read,
  * lh_paged_attention) run what the calibration leaves behind: 8-bit rows for quantized products,
- * products with the calibrated NVFP4 weights, and a key-value cache in the same formats.  They keep
+ * products with the calibrated NVFP4 weights, and a key-value cache in the same formats.  Those around it
+ * (lh_cache_extend, lh_rotary, lh_route, lh_moe, lh_adapter) grow the cache's sequences, turn queries and keys by
+ * their positions, choose experts and run them, and add low-rank adapters to a product.  All of them keep
  * no state, allocate nothing and may be captured into a HIP graph.
  *
  * Citations are to the pages this library follows: "Add activation-aware local Hessian scale
@@ -59,7 +61,7 @@
 extern "C" {
 #endif
 
-#define LH_VERSION 7
+#define LH_VERSION 8
 
 typedef enum {
   LH_OK = 0,
@@ -455,6 +457,105 @@ lh_status lh_paged_attention(const lh_cache* cache, const void* Q, int64_t q_str
  */
 int64_t lh_paged_attention_workspace(const lh_cache* cache, int64_t batch, int64_t n_q_heads,
                                      int64_t max_pages);
+
+/*
+ * Growth of a paged cache's sequences by one step's tokens: block tables, lengths and free pages on the
+ * device, and for each row of new tokens its slot (for lh_cache_write), position (for lh_rotary) and sequence.
+ * With request b of length l = lengths[b] (taken as between 0 and max_pages * page_size), n = new_tokens[b]
+ * (NULL: 1 for every request), up(x) = x / page_size rounded up, and the stack free_pages[0 .. c), c =
+ * free_count[0] (taken as between 0 and capacity), its top at c - 1:
+ *   n < 0  takes back the last min(-n, l) tokens: the request's length becomes l' = max(l + n, 0), and the pages
+ *          up(l') .. up(l) - 1 of its table go on the stack, in the order of requests and pages (those past
+ *          `capacity` are lost).  All of them are on the stack before any page is taken, the top then at a - 1.
+ *   n > 0  asks for n tokens, rows offsets[b] .. offsets[b] + n - 1, and needs up(l + n) - up(l) pages.  It is
+ *          granted if l + n <= max_pages * page_size, its rows end by max_tokens, and either it needs no page or the
+ *          needs of all requests up to it that meet those two conditions come to at most a: first come, first
+ *          served.  It then takes its pages from the top, the first for its lowest tokens, and its length
+ *          becomes l + n.  Otherwise its length and pages stay as they are.
+ * block_table [batch, max_pages] int32: entries of new pages are written, all others stay as they are.
+ * free_pages [capacity] int32: c .. c + the pages given back are written; new_count[0] is what is then held.
+ * slots [max_tokens] int64, positions and sequence [max_tokens] int32: for each row the token's slot and position (both
+ * -1 where the request was not granted) and its request; behind the last row of the batch all three are -1.
+ * offsets [batch + 1] int32: the first row of each request, whether granted or not, at most max_tokens.
+ * new_lengths may be lengths and new_count free_count, for an update in place; with others in their place, two
+ * calls with the same arguments do the same.  No other arguments may overlap.
+ * Page numbers are handed on as they are.  workspace: device memory of at least lh_cache_extend_workspace bytes (16-byte
+ * aligned; NULL if that is 0) that no other call uses until this one has run.
+ * Errors: INVALID_ARGUMENT for batch outside [0, 2^28-1], page_size < 1, max_pages < 0, max_pages * page_size over
+ * 2^31-4096, max_tokens or capacity outside [0, 2^31-1], NULL required pointers, a short workspace, misaligned,
+ * non-device or mixed-device pointers.
+ */
+lh_status lh_cache_extend(int32_t* block_table, int64_t batch, int64_t max_pages, int64_t page_size,
+                          const int32_t* lengths, const int32_t* new_tokens, int32_t* free_pages,
+                          int64_t capacity, const int32_t* free_count, int64_t max_tokens, int64_t* slots,
+                          int32_t* positions, int32_t* sequence, int32_t* offsets, int32_t* new_lengths,
+                          int32_t* new_count, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that lh_cache_extend needs for these sizes (a host computation; 0 for ones that it refuses). */
+int64_t lh_cache_extend_workspace(int64_t batch, int64_t max_tokens);
+
+/*
+ * Angles per position of rotary positions, f_j = theta^(-2j / rot_dim) for j < rot_dim / 2, scaled for contexts
+ * longer than the one they were trained for; computed in 64 bits on the host and rounded once to fp32:
+ *   PLAIN   f_j
+ *   LINEAR  f_j / factor (positions interpolated)
+ *   BASE    f_j with theta * factor^(rot_dim / (rot_dim - 2)) for theta
+ *   PARTS   f_j (k + (1 - k) / factor), k = (t - low_turns) / (high_turns - low_turns) clamped to [0, 1], t =
+ *           original_context * f_j / (2 pi) the turns over the trained context: fast angles stay, slow ones are interpolated
+ * frequencies [rot_dim / 2] and scale: HOST memory; *scale is what lh_rotary's scale is meant to be, 0.1 ln(factor) + 1 for
+ * PARTS and 1 otherwise.
+ * Errors: UNSUPPORTED for an unknown scaling; INVALID_ARGUMENT for theta not positive and finite, rot_dim odd or
+ * outside [2, 65536] (below 4 with BASE), factor < 1 or not finite (but with PLAIN), original_context < 1 or not 0 <=
+ * low_turns < high_turns < infinity with PARTS, NULL pointers.
+ */
+typedef enum {
+  LH_ROTARY_PLAIN = 0,
+  LH_ROTARY_LINEAR = 1,
+  LH_ROTARY_BASE = 2,
+  LH_ROTARY_PARTS = 3,
+  LH_ROTARY_RANGE_MIN_ = -2147483647 - 1, /* not scalings; see lh_dtype */
+  LH_ROTARY_RANGE_MAX_ = 2147483647
+} lh_rotary_scaling;
+
+lh_status lh_rotary_frequencies(double theta, int64_t rot_dim, lh_rotary_scaling scaling, double factor,
+                                int64_t original_context, double low_turns, double high_turns,
+                                float* frequencies, float* scale);
+
+/*
+ * Rotary positions: the pairs of the first rot_dim elements of every head of Q and K, turned by their token's angles
+ *   (a, b) -> scale * (a cos w - b sin w, a sin w + b cos w),   w = positions[t] * frequencies[j]
+ * for pair j < rot_dim / 2: elements (j, j + rot_dim / 2), or (2j, 2j + 1) if interleaved.  With `inverse`, -w for w, which is
+ * the transpose: it takes a gradient back through the rotation.  Other elements are copied.  A token of negative position
+ * is copied as it is, scale or not (a row without a token, see lh_cache_extend).
+ * Q: element (t, h, i) at t * q_stride + h * head_dim + i, t < tokens; K and the outputs in the same way, so each may be part of
+ * wider rows.  Q_out may be Q and K_out K (with equal strides), for a turn in place; otherwise they overlap no input.
+ * All of dtype, 16-byte aligned, strides multiples of 16 bytes.  n_k_heads may be 0 (K and K_out NULL).
+ * positions [tokens] int32, frequencies [rot_dim / 2] fp32 (see lh_rotary_frequencies), both device.
+ * The angle is the exact product, reduced in 64-bit arithmetic (positions up to 2^31-1 lose nothing); sine and cosine
+ * are fp32 to within 2^-23, products and sums fp32, rounded once to dtype.
+ * Errors: UNSUPPORTED for an unknown dtype; INVALID_ARGUMENT for tokens outside [0, 2^31-1], head_dim < 1, over 65536 or
+ * not a multiple of 16, rot_dim odd or outside [2, head_dim], n_q_heads < 1, n_k_heads < 0, heads * head_dim over
+ * 2^27, a scale that is not finite, bad strides, a launch of 2^32 or more work-items (at most one for 2 elements), NULL
+ * required pointers, misaligned, non-device or mixed-device pointers.
+ */
+lh_status lh_rotary(const void* Q, int64_t q_stride, int64_t n_q_heads, const void* K, int64_t k_stride,
+                    int64_t n_k_heads, lh_dtype dtype, int64_t tokens, int64_t head_dim, int64_t rot_dim,
+                    const int32_t* positions, const float* frequencies, int32_t interleaved,
+                    int32_t inverse, float scale, void* Q_out, int64_t q_out_stride, void* K_out,
+                    int64_t k_out_stride, void* stream);
+
+/*
+ * The choice of experts for each token: ids[t] are the topk largest of logits[t], in descending order, equal ones by
+ * ascending index, and weights[t] their softmax weights times `scale`:
+ *   p_e = exp(logits[t,e] - m) / sum over all experts, or over the chosen ones if renormalize;  m the largest logit
+ * A logit of -infinity or NaN is never chosen and has weight 0; where fewer than topk are left, ids are -1 and weights 0
+ * (lh_moe skips those).  Where m is +infinity, the logits equal to it count as 1 and all others as 0.
+ * logits [tokens, n_experts] of dtype; ids [tokens, topk] int32, weights [tokens, topk] fp32.  Sums are fp32.
+ * Errors: UNSUPPORTED for an unknown dtype; INVALID_ARGUMENT for tokens outside [0, 2^31-1], n_experts outside [1, 4096], topk
+ * outside [1, 64] or over n_experts, a scale that is not finite, NULL required pointers, non-device or mixed-device pointers.
+ */
+lh_status lh_route(const void* logits, lh_dtype dtype, int64_t tokens, int64_t n_experts, int64_t topk,
+                   int32_t renormalize, float scale, int32_t* ids, float* weights, void* stream);
 
 /* Message of the last error on the calling thread ("" if none); valid until its next call. */
 const char* lh_last_error(void);

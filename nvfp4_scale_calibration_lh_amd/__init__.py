@@ -22,11 +22,13 @@ LIB_PATH = os.environ.get("LH_LIBRARY") or os.path.join(_PKG, "liblh.so")
 LH_OK, LH_ERR_INVALID_ARGUMENT, LH_ERR_UNSUPPORTED, LH_ERR_HIP = 0, 1, 2, 3
 LH_DTYPE_F32, LH_DTYPE_BF16, LH_DTYPE_E4M3 = 0, 1, 2
 LH_CACHE_E4M3, LH_CACHE_FP4 = 0, 1
+ROTARY_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "parts": 3}
 
 EXPORTED = ("lh_accumulate", "lh_accumulate_noalloc", "lh_accumulate_act_aware", "lh_accumulate_act_aware_fq", "lh_activation_fake_quant",
             "lh_accumulate_sweep", "lh_dequantize", "lh_dequantize_ex", "lh_scale_sweep", "lh_scale_sweep_ex", "lh_scale_sweep_diag",
             "lh_scale_sweep_diag_ex", "lh_scale_sweep_mse", "lh_absmax", "lh_rms_norm_quant", "lh_matvec", "lh_cache_write",
-            "lh_cache_read", "lh_paged_attention", "lh_paged_attention_workspace", "lh_last_error", "lh_version")
+            "lh_cache_read", "lh_paged_attention", "lh_paged_attention_workspace", "lh_cache_extend", "lh_cache_extend_workspace",
+           "lh_rotary", "lh_rotary_frequencies", "lh_route", "lh_last_error", "lh_version")
 MAX_MULTIPLIERS = 128
 
 
@@ -81,13 +83,21 @@ def lib() -> ctypes.CDLL:
         h.lh_cache_read.argtypes = [vp, vp, i64, i32, vp, vp, vp]
         h.lh_paged_attention.argtypes = [vp, vp, i64, i32, i64, i64, vp, i64, vp, f32, vp, vp, i64, vp]
         h.lh_paged_attention_workspace.argtypes = [vp, i64, i64, i64]
+        h.lh_cache_extend.argtypes = [vp, i64, i64, i64, vp, vp, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, vp]
+        h.lh_cache_extend_workspace.argtypes = [i64, i64]
+        f64 = ctypes.c_double
+        h.lh_rotary_frequencies.argtypes = [f64, i64, i32, f64, i64, f64, f64, vp, vp]
+        h.lh_rotary.argtypes = [vp, i64, i64, vp, i64, i64, i32, i64, i64, i64, vp, vp, i32, i32, f32, vp, i64, vp, i64, vp]
+        h.lh_route.argtypes = [vp, i32, i64, i64, i64, i32, f32, vp, vp, vp]
         for f in ("lh_accumulate", "lh_accumulate_noalloc", "lh_accumulate_act_aware", "lh_accumulate_act_aware_fq",
                   "lh_activation_fake_quant", "lh_scale_sweep", "lh_scale_sweep_ex", "lh_scale_sweep_diag_ex",
                   "lh_dequantize_ex", "lh_accumulate_sweep",
                   "lh_scale_sweep_diag", "lh_scale_sweep_mse", "lh_absmax", "lh_dequantize", "lh_rms_norm_quant",
-                  "lh_matvec", "lh_cache_write", "lh_cache_read", "lh_paged_attention"):
+                  "lh_matvec", "lh_cache_write", "lh_cache_read", "lh_paged_attention", "lh_cache_extend",
+                  "lh_rotary_frequencies", "lh_rotary", "lh_route"):
             getattr(h, f).restype = ctypes.c_int
-        h.lh_paged_attention_workspace.restype = ctypes.c_int64
+        for f in ("lh_paged_attention_workspace", "lh_cache_extend_workspace"):
+            getattr(h, f).restype = ctypes.c_int64
         h.lh_last_error.argtypes = []
         h.lh_last_error.restype = ctypes.c_char_p
         h.lh_version.argtypes = []
@@ -654,3 +664,134 @@ def lh_paged_attention(Q: torch.Tensor, cache: Cache, block_table: torch.Tensor,
     _check(lib().lh_paged_attention(cache.ref, Q.data_ptr(), stride, _dtype_code(Q), batch, heads, block_table.data_ptr(), pages,
                                     lengths.data_ptr(), scale, O.data_ptr(), _ptr(workspace), nbytes, _stream(device)))
     return O
+
+
+def lh_cache_extend_workspace(batch: int, max_tokens: int) -> int:
+    """Bytes of workspace that lh_cache_extend needs for these sizes."""
+    return int(lib().lh_cache_extend_workspace(batch, max_tokens))
+
+
+def lh_cache_extend(block_table: torch.Tensor, lengths: torch.Tensor, new_tokens: Optional[torch.Tensor], free_pages: torch.Tensor,
+                    free_count: torch.Tensor, *, page_size: int, max_tokens: int, new_lengths: Optional[torch.Tensor] = None,
+                    new_count: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+                    positions: Optional[torch.Tensor] = None, sequence: Optional[torch.Tensor] = None,
+                    offsets: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """(slots, positions, sequence, offsets, new_lengths, new_count): room in the cache for new_tokens [batch] (None: one each;
+    negative: that many are taken back) more tokens of each request.  block_table [batch, max_pages] and the stack
+    free_pages [capacity], of which free_count [1] are held, are updated in place (all int32); the new lengths [batch] and
+    count [1] are new tensors, or lengths and free_count themselves if given as such.  slots [max_tokens] int64, positions and
+    sequence [max_tokens] int32 are for the rows of new tokens, request after request from row offsets[b] on; rows behind the last hold -1, and
+    a request that finds no room keeps its length and has slots and positions of -1."""
+    if block_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("block_table must be [batch, max_pages] and free_pages [capacity]")
+    batch, pages = block_table.shape
+    device, i32 = block_table.device, torch.int32
+    _need(block_table, "block_table", dtype=i32)
+    _need(lengths, "lengths", (batch,), i32)
+    if new_tokens is not None:
+        _need(new_tokens, "new_tokens", (batch,), i32)
+    _need(free_pages, "free_pages", dtype=i32)
+    _need(free_count, "free_count", (1,), i32)
+    if max_tokens < 0:
+        raise ValueError("max_tokens must be >= 0")
+    if slots is None:
+        slots = _empty(max_tokens, dtype=torch.int64, device=device)
+    else:
+        _need(slots, "slots", (max_tokens,), torch.int64)
+    given = (positions, sequence, offsets, new_lengths, new_count)
+    sizes = (max_tokens, max_tokens, batch + 1, batch, 1)
+    if any(t is None for t in given):       # one allocation for all that are wanted
+        made = _empty(sum(n for n, t in zip(sizes, given) if t is None), dtype=i32, device=device)
+        made = iter(made.split_with_sizes([n for n, t in zip(sizes, given) if t is None]))
+    out = []
+    for name, n, t in zip(("positions", "sequence", "offsets", "new_lengths", "new_count"), sizes, given):
+        if t is None:
+            t = next(made)
+        else:
+            _need(t, name, (n,), i32)
+        out.append(t)
+    positions, sequence, offsets, new_lengths, new_count = out
+    nbytes = 0
+    if workspace is not None:
+        _need(workspace, "workspace", dtype=torch.uint8)
+        nbytes = workspace.numel()
+    else:
+        nbytes = lib().lh_cache_extend_workspace(batch, max_tokens)
+        if nbytes:
+            workspace = _empty(nbytes, dtype=torch.uint8, device=device)
+    _check(lib().lh_cache_extend(block_table.data_ptr(), batch, pages, page_size, lengths.data_ptr(), _ptr(new_tokens), free_pages.data_ptr(),
+                                 free_pages.shape[0], free_count.data_ptr(), max_tokens, slots.data_ptr(), positions.data_ptr(),
+                                 sequence.data_ptr(), offsets.data_ptr(), new_lengths.data_ptr(), new_count.data_ptr(), _ptr(workspace),
+                                 nbytes, _stream(device)))
+    return slots, positions, sequence, offsets, new_lengths, new_count
+
+
+def lh_rotary_frequencies(rot_dim: int, *, theta: float = 10000.0, scaling: str = "plain", factor: float = 1.0, original_context: int = 0,
+                          low_turns: float = 1.0, high_turns: float = 32.0, device=None) -> Tuple[torch.Tensor, float]:
+    """(frequencies [rot_dim / 2] fp32 on `device` (the current GPU), scale) for lh_rotary: theta^(-2j / rot_dim), and 1, for scaling
+    "plain"; "linear", "base" and "parts" stretch them for contexts `factor` times as long ("parts" by the turns over original_context)."""
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"scaling must be one of {', '.join(ROTARY_SCALINGS)}")
+    out = torch.empty(max(rot_dim, 0) // 2, dtype=torch.float32)
+    scale = ctypes.c_float()
+    _check(lib().lh_rotary_frequencies(theta, rot_dim, ROTARY_SCALINGS[scaling], factor, original_context, low_turns, high_turns,
+                                       out.data_ptr(), ctypes.byref(scale)))
+    return out.to("cuda" if device is None else device), scale.value
+
+
+def lh_rotary(Q: torch.Tensor, K: Optional[torch.Tensor], positions: torch.Tensor, frequencies: torch.Tensor, *,
+              interleaved: bool = False, inverse: bool = False, scale: float = 1.0, out_q: Optional[torch.Tensor] = None,
+              out_k: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """(out_q, out_k): Q [tokens, n_q_heads, head_dim] and K [tokens, n_k_heads, head_dim] or None (fp32 or bf16; tokens may lie apart)
+    with the first 2 * len(frequencies) elements of each head turned by positions [tokens] int32 times frequencies fp32, pair j in
+    elements (j, j + half) or (2j, 2j + 1).  out_q and out_k may be Q and K themselves.  `inverse` turns back, which is what a
+    gradient needs.  Tokens of negative position are copied."""
+    if Q.dim() != 3 or frequencies.dim() != 1:
+        raise ValueError("Q must be [tokens, n_q_heads, head_dim] and frequencies [rot_dim / 2]")
+    tokens, heads, dim = Q.shape
+    device, dtype = Q.device, Q.dtype
+    qs = _heads(Q, "Q", heads, dim)
+    _need(positions, "positions", (tokens,), torch.int32)
+    _need(frequencies, "frequencies", dtype=torch.float32)
+    if out_q is None:
+        out_q, qos = _empty(tokens, heads, dim, dtype=dtype, device=device), heads * dim
+    else:
+        qos = qs if out_q is Q else _heads(out_q, "out_q", heads, dim, dtype, tokens)
+    k_heads, ks, kos = 0, 0, 0
+    if K is not None:
+        if K.dim() != 3:
+            raise ValueError("K must be [tokens, n_k_heads, head_dim]")
+        k_heads = K.shape[1]
+        ks = _heads(K, "K", k_heads, dim, dtype, tokens)
+        if out_k is None:
+            out_k, kos = _empty(tokens, k_heads, dim, dtype=dtype, device=device), k_heads * dim
+        else:
+            kos = ks if out_k is K else _heads(out_k, "out_k", k_heads, dim, dtype, tokens)
+    elif out_k is not None:
+        raise ValueError("out_k is for K")
+    _check(lib().lh_rotary(Q.data_ptr(), qs, heads, _ptr(K), ks, k_heads, _dtype_code(Q), tokens, dim, 2 * frequencies.shape[0],
+                           positions.data_ptr(), frequencies.data_ptr(), interleaved, inverse, scale, out_q.data_ptr(), qos,
+                           _ptr(out_k), kos, _stream(device)))
+    return out_q, out_k
+
+
+def lh_route(logits: torch.Tensor, topk: int, *, renormalize: bool = True, scale: float = 1.0, ids: Optional[torch.Tensor] = None,
+             weights: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(ids, weights) [tokens, topk] int32 and fp32: the topk largest of logits [tokens, n_experts] (fp32 or bf16) in descending
+    order, ties by index, and their softmax weights over the chosen (renormalize) or over all, times scale.  Logits of -inf
+    and NaN are not chosen; where fewer are left, ids are -1 and weights 0."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [tokens, n_experts]")
+    _need(logits, "logits")
+    tokens, experts = logits.shape
+    if ids is None:
+        ids = _empty(tokens, max(topk, 0), dtype=torch.int32, device=logits.device)
+    else:
+        _need(ids, "ids", (tokens, topk), torch.int32)
+    if weights is None:
+        weights = _empty(tokens, max(topk, 0), dtype=torch.float32, device=logits.device)
+    else:
+        _need(weights, "weights", (tokens, topk), torch.float32)
+    _check(lib().lh_route(logits.data_ptr(), _dtype_code(logits), tokens, experts, topk, renormalize, scale, ids.data_ptr(),
+                          weights.data_ptr(), _stream(logits.device)))
+    return ids, weights

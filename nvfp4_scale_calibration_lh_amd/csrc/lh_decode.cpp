@@ -19,16 +19,6 @@ namespace {
 constexpr int64_t kMaxInt = 2147483647LL;
 constexpr int64_t kMaxCin = int64_t(1) << 24;
 
-// One of the 126 positive finite values: 3 bits below the leading one, or a multiple of 2^-9 (a search
-// through them took 0.3 us a call).
-bool e4m3_value(float x) {
-  if (!(x >= 0x1p-9f && x <= 448.0f)) return false;
-  if (x < 0x1p-6f) return x * 512.0f == std::floor(x * 512.0f);
-  uint32_t bits;
-  std::memcpy(&bits, &x, sizeof bits);
-  return (bits & 0xFFFFF) == 0;
-}
-
 lh_status check_rows(int64_t rows, int64_t cin) {
   if (rows < 0 || rows > kMaxInt) return fail(LH_ERR_INVALID_ARGUMENT, "rows must be in [0, 2^31-1] (got %lld)", (long long)rows);
   if (cin <= 0 || cin % 16 || cin > kMaxCin)
@@ -64,19 +54,6 @@ lh_status check_tokens(const lh::CacheView& c, int64_t tokens) {
   if (tokens < 0) return fail(LH_ERR_INVALID_ARGUMENT, "tokens must be >= 0 (got %lld)", (long long)tokens);
   if (tokens > kMaxInt * 256 / (c.heads * (c.dim / 16)) - 16) return fail(LH_ERR_INVALID_ARGUMENT, "too many tokens for one call");
   return LH_OK;
-}
-
-lh_status check_stride(int64_t stride, int64_t least, lh_dtype dtype, const char* name) {
-  if (stride < least || stride % (dtype == LH_DTYPE_BF16 ? 8 : 4))
-    return fail(LH_ERR_INVALID_ARGUMENT, "%s must be at least %lld elements and a multiple of 16 bytes (got %lld)", name,
-                (long long)least, (long long)stride);
-  return LH_OK;
-}
-
-// Status of a call whose launch returned e.
-lh_status launched(hipError_t e, const char* what) {
-  if (e == hipErrorInvalidConfiguration) return fail(LH_ERR_INVALID_ARGUMENT, "%s: too large for one call (2^32 work-items or more)", what);
-  return e == hipSuccess ? ok() : hip_fail(e, what);
 }
 
 }  // namespace

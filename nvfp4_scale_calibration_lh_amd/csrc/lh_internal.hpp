@@ -126,4 +126,35 @@ hipError_t launch_attention(const CacheView& c, const void* q, bool bf16, int64_
                             const int* table, int64_t width, const int* lengths, float scale, void* o, void* work,
                             hipStream_t stream);
 
+// Growth of a paged cache's sequences (lh_cache_extend): pointers and sizes as there, asked may be NULL.
+// extend_workspace is the scratch in bytes (0: none).
+struct ExtendView {
+  int* table;
+  const int *lengths, *asked;
+  int* stack;
+  const int* count;
+  int64_t* slots;
+  int *positions, *sequence, *offsets, *new_lengths, *new_count;
+  int64_t batch, width, page, capacity, rows;
+};
+int64_t extend_workspace(int64_t batch, int64_t rows);
+hipError_t launch_extend(const ExtendView& v, void* work, hipStream_t stream);
+
+// Rotary positions of q (and k with k_heads > 0) into qo, ko, which may be q and k.
+struct RotaryView {
+  const void *q, *k;
+  void *qo, *ko;
+  const int* positions;
+  const float* frequencies;
+  int64_t tokens, q_heads, k_heads, dim, rot, q_stride, k_stride, qo_stride, ko_stride;
+  float scale;
+  bool interleaved, inverse;
+};
+hipError_t launch_rotary(const RotaryView& v, bool bf16, hipStream_t stream);
+
+// The topk largest logits of each token and their softmax weights; experts <= kMaxExperts, topk <= 64.
+constexpr int64_t kMaxExperts = 4096;
+hipError_t launch_route(const void* logits, bool bf16, int64_t tokens, int64_t experts, int64_t topk, bool renormalize,
+                        float scale, int* ids, float* weights, hipStream_t stream);
+
 }  // namespace lh
