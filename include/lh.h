@@ -557,6 +557,37 @@ lh_status lh_rotary(const void* Q, int64_t q_stride, int64_t n_q_heads, const vo
 lh_status lh_route(const void* logits, lh_dtype dtype, int64_t tokens, int64_t n_experts, int64_t topk,
                    int32_t renormalize, float scale, int32_t* ids, float* weights, void* stream);
 
+/*
+ * A mixture-of-experts layer on NVFP4 expert weights as lh_scale_sweep writes them, for a few tokens:
+ *   Y[t] = sum_j weights[t,j] * D_e (silu(G_e x_t) * U_e x_t),   e = ids[t,j],   silu(g) = g / (1 + exp(-g))
+ * G_e and U_e are the first and the last `inner` rows of expert e's gate_up matrix, D_e its down matrix; a choice outside
+ * [0, n_experts) adds nothing, a token without choices gives zeros, one chosen twice has the sum of its weights.
+ * gate_up_code [n_experts, 2 * inner, hidden/16], gate_up_fp4 [n_experts, 2 * inner, hidden/2], down_code [n_experts, hidden,
+ * inner/16], down_fp4 [n_experts, hidden, inner/2] (both fp4 8-byte aligned), amax [n_experts] each, scale_norm as in
+ * lh_sweep_options.  ids and weights [tokens, topk] int32 and fp32, as lh_route gives them.
+ * X [tokens, hidden], x_scale and x_group as in lh_matvec; Y [tokens, hidden] F32 for F32 rows, BF16 otherwise.
+ * Weights and rows enter exactly (fp32 elements as in lh_matvec); what comes between the two products is held to 2^-17 of itself
+ * (fp32 rows: 2^-24); sums are fp32, in a fixed order, and Y is rounded once.  Infinities and NaN in a row give what the formula
+ * gives in that row's Y and change no other row.
+ * Any number of tokens works; the weights of an expert are read again for every 64 tokens, and among those for every 16 rows of it
+ * (32 where tokens > 16 and tokens * topk > 4 * n_experts).
+ * workspace: device memory of at least lh_moe_workspace bytes (16-byte aligned) that no other call uses until this one has run.
+ * Errors: UNSUPPORTED for an unknown dtype; INVALID_ARGUMENT for tokens outside [0, 4194240], hidden or inner < 1, over 2^24
+ * or not multiples of 16, hidden * inner over 2^32, n_experts outside [1, 4096], topk outside [1, 64], scale_norm that is not a
+ * positive finite E4M3 value, x_scale or x_group that do not fit the type, a launch of 2^32 or more work-items, NULL required
+ * pointers, a short workspace, misaligned, non-device or mixed-device pointers.
+ */
+lh_status lh_moe(const void* X, lh_dtype x_dtype, const float* x_scale, int64_t x_group, int64_t tokens,
+                 int64_t hidden, int64_t inner, int64_t n_experts, int64_t topk, const int32_t* ids,
+                 const float* weights, const uint8_t* gate_up_code, const uint8_t* gate_up_fp4,
+                 const float* gate_up_amax, const uint8_t* down_code, const uint8_t* down_fp4,
+                 const float* down_amax, float scale_norm, void* Y, void* workspace, int64_t workspace_bytes,
+                 void* stream);
+
+/* Bytes of workspace that lh_moe needs for these sizes (a host computation; 0 for ones that it refuses). */
+int64_t lh_moe_workspace(lh_dtype x_dtype, int64_t tokens, int64_t hidden, int64_t inner, int64_t n_experts,
+                         int64_t topk);
+
 /* Message of the last error on the calling thread ("" if none); valid until its next call. */
 const char* lh_last_error(void);
 

@@ -28,7 +28,7 @@ EXPORTED = ("lh_accumulate", "lh_accumulate_noalloc", "lh_accumulate_act_aware",
             "lh_accumulate_sweep", "lh_dequantize", "lh_dequantize_ex", "lh_scale_sweep", "lh_scale_sweep_ex", "lh_scale_sweep_diag",
             "lh_scale_sweep_diag_ex", "lh_scale_sweep_mse", "lh_absmax", "lh_rms_norm_quant", "lh_matvec", "lh_cache_write",
             "lh_cache_read", "lh_paged_attention", "lh_paged_attention_workspace", "lh_cache_extend", "lh_cache_extend_workspace",
-           "lh_rotary", "lh_rotary_frequencies", "lh_route", "lh_last_error", "lh_version")
+           "lh_rotary", "lh_rotary_frequencies", "lh_route", "lh_moe", "lh_moe_workspace", "lh_last_error", "lh_version")
 MAX_MULTIPLIERS = 128
 
 
@@ -89,14 +89,16 @@ def lib() -> ctypes.CDLL:
         h.lh_rotary_frequencies.argtypes = [f64, i64, i32, f64, i64, f64, f64, vp, vp]
         h.lh_rotary.argtypes = [vp, i64, i64, vp, i64, i64, i32, i64, i64, i64, vp, vp, i32, i32, f32, vp, i64, vp, i64, vp]
         h.lh_route.argtypes = [vp, i32, i64, i64, i64, i32, f32, vp, vp, vp]
+        h.lh_moe.argtypes = [vp, i32, vp, i64, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, f32, vp, vp, i64, vp]
+        h.lh_moe_workspace.argtypes = [i32, i64, i64, i64, i64, i64]
         for f in ("lh_accumulate", "lh_accumulate_noalloc", "lh_accumulate_act_aware", "lh_accumulate_act_aware_fq",
                   "lh_activation_fake_quant", "lh_scale_sweep", "lh_scale_sweep_ex", "lh_scale_sweep_diag_ex",
                   "lh_dequantize_ex", "lh_accumulate_sweep",
                   "lh_scale_sweep_diag", "lh_scale_sweep_mse", "lh_absmax", "lh_dequantize", "lh_rms_norm_quant",
                   "lh_matvec", "lh_cache_write", "lh_cache_read", "lh_paged_attention", "lh_cache_extend",
-                  "lh_rotary_frequencies", "lh_rotary", "lh_route"):
+                  "lh_rotary_frequencies", "lh_rotary", "lh_route", "lh_moe"):
             getattr(h, f).restype = ctypes.c_int
-        for f in ("lh_paged_attention_workspace", "lh_cache_extend_workspace"):
+        for f in ("lh_paged_attention_workspace", "lh_cache_extend_workspace", "lh_moe_workspace"):
             getattr(h, f).restype = ctypes.c_int64
         h.lh_last_error.argtypes = []
         h.lh_last_error.restype = ctypes.c_char_p
@@ -795,3 +797,63 @@ def lh_route(logits: torch.Tensor, topk: int, *, renormalize: bool = True, scale
     _check(lib().lh_route(logits.data_ptr(), _dtype_code(logits), tokens, experts, topk, renormalize, scale, ids.data_ptr(),
                           weights.data_ptr(), _stream(logits.device)))
     return ids, weights
+
+
+def _rows_type(X: torch.Tensor, x_scale: Optional[torch.Tensor], x_group: int) -> Tuple[int, int]:
+    """(dtype code, x_group) of a product's rows X [rows, cin], whose x_scale is checked."""
+    rows, cin = X.shape
+    if X.dtype == torch.float8_e4m3fn:
+        if x_scale is None:
+            raise ValueError("x_scale is required for E4M3 rows")
+        _need(x_scale, "x_scale", (rows, _scales(cin, x_group)), torch.float32)
+        return LH_DTYPE_E4M3, x_group
+    if x_scale is not None:
+        raise ValueError("x_scale is for E4M3 rows")
+    _scales(cin, x_group)
+    return _dtype_code(X), 0               # x_group says how x_scale is grouped, and there is none
+
+
+def lh_moe_workspace(dtype: torch.dtype, tokens: int, hidden: int, inner: int, n_experts: int, topk: int) -> int:
+    """Bytes of workspace that lh_moe needs for rows of dtype and these sizes."""
+    code = {torch.float32: LH_DTYPE_F32, torch.bfloat16: LH_DTYPE_BF16, torch.float8_e4m3fn: LH_DTYPE_E4M3}[dtype]
+    return int(lib().lh_moe_workspace(code, tokens, hidden, inner, n_experts, topk))
+
+
+def lh_moe(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate_up: Tuple[torch.Tensor, torch.Tensor, torch.Tensor],
+           down: Tuple[torch.Tensor, torch.Tensor, torch.Tensor], Y: Optional[torch.Tensor] = None, *, x_scale: Optional[torch.Tensor] = None,
+           x_group: int = 0, norm: float = 448.0, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y [tokens, hidden]: the expert layer sum_j weights[t, j] * D_e (silu(G_e x) * U_e x), e = ids[t, j], of X [tokens, hidden] (fp32, bf16,
+    or torch.float8_e4m3fn with x_scale and x_group as lh_matvec takes them) and ids, weights [tokens, topk] as lh_route gives them.
+    gate_up = (code [E, 2 * inner, hidden/16], fp4 [E, 2 * inner, hidden/2], amax [E]) and down = (code [E, hidden, inner/16], fp4 [E,
+    hidden, inner/2], amax [E]) are what a scale sweep with normalization `norm` gives.  Y is fp32 for fp32 X, otherwise bf16.
+    workspace (uint8) is allocated on the current stream when not given."""
+    _need(X, "X")
+    if X.dim() != 2 or ids.dim() != 2 or down[0].dim() != 3:
+        raise ValueError("X must be [tokens, hidden], ids [tokens, topk] and down's code [E, hidden, inner/16]")
+    tokens, hidden = X.shape
+    device, u8 = X.device, torch.uint8
+    dtype, x_group = _rows_type(X, x_scale, x_group)
+    topk = ids.shape[1]
+    _need(ids, "ids", (tokens, topk), torch.int32)
+    _need(weights, "weights", (tokens, topk), torch.float32)
+    experts, _, blocks = down[0].shape
+    inner = 16 * blocks
+    for name, (code, fp4, amax), cout, cin in (("gate_up", gate_up, 2 * inner, hidden), ("down", down, hidden, inner)):
+        _need(code, name + " code", (experts, cout, cin // 16), u8)
+        _need(fp4, name + " fp4", (experts, cout, cin // 2), u8)
+        _need(amax, name + " amax", (experts,), torch.float32)
+    y_dtype = torch.float32 if dtype == LH_DTYPE_F32 else torch.bfloat16
+    if Y is None:
+        Y = _empty(tokens, hidden, dtype=y_dtype, device=device)
+    else:
+        _need(Y, "Y", (tokens, hidden), y_dtype)
+    if workspace is not None:
+        _need(workspace, "workspace", dtype=u8)
+        nbytes = workspace.numel()
+    else:
+        nbytes = lib().lh_moe_workspace(dtype, tokens, hidden, inner, experts, topk)
+        workspace = _empty(nbytes, dtype=u8, device=device)
+    _check(lib().lh_moe(X.data_ptr(), dtype, _ptr(x_scale), x_group, tokens, hidden, inner, experts, topk, ids.data_ptr(), weights.data_ptr(),
+                        gate_up[0].data_ptr(), gate_up[1].data_ptr(), gate_up[2].data_ptr(), down[0].data_ptr(), down[1].data_ptr(),
+                        down[2].data_ptr(), norm, Y.data_ptr(), workspace.data_ptr(), nbytes, _stream(device)))
+    return Y

@@ -157,4 +157,22 @@ constexpr int64_t kMaxExperts = 4096;
 hipError_t launch_route(const void* logits, bool bf16, int64_t tokens, int64_t experts, int64_t topk, bool renormalize,
                         float scale, int* ids, float* weights, hipStream_t stream);
 
+// The expert layer (lh_moe): x_type as launch_matvec, gdiv the divisor of the global scales.  moe_workspace is its scratch in bytes.
+struct MoeView {
+  const void* x;
+  int x_type;
+  const float* x_scale;
+  int64_t x_scales, tokens, hidden, inner, experts, topk;
+  const int* ids;
+  const float* weights;
+  const uint8_t *gate_up_code, *gate_up_fp4;
+  const float* gate_up_amax;
+  const uint8_t *down_code, *down_fp4;
+  const float* down_amax;
+  float gdiv;
+  void* y;
+};
+int64_t moe_workspace(const MoeView& v);
+hipError_t launch_moe(const MoeView& v, void* work, hipStream_t stream);
+
 }  // namespace lh

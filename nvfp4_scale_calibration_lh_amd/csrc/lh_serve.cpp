@@ -26,6 +26,29 @@ lh_status check_extend(int64_t batch, int64_t max_pages, int64_t page_size, int6
   return LH_OK;
 }
 
+// tokens * topk choices and their rows' offsets; hidden * inner keeps a matrix's offsets within 32 bits.
+lh_status check_moe(int64_t tokens, int64_t hidden, int64_t inner, int64_t n_experts, int64_t topk) {
+  if (tokens < 0 || tokens > 65535 * 64) return fail(LH_ERR_INVALID_ARGUMENT, "tokens must be in [0, 4194240] (got %lld)", (long long)tokens);
+  if (hidden < 1 || hidden % 16 || hidden > (int64_t(1) << 24)) return fail(LH_ERR_INVALID_ARGUMENT, "hidden must be a positive multiple of 16 up to 2^24 (got %lld)", (long long)hidden);
+  if (inner < 1 || inner % 16 || inner > (int64_t(1) << 24)) return fail(LH_ERR_INVALID_ARGUMENT, "inner must be a positive multiple of 16 up to 2^24 (got %lld)", (long long)inner);
+  if (hidden * inner > int64_t(1) << 32) return fail(LH_ERR_INVALID_ARGUMENT, "hidden * inner must be at most 2^32");
+  if (n_experts < 1 || n_experts > lh::kMaxExperts) return fail(LH_ERR_INVALID_ARGUMENT, "n_experts must be in [1, 4096] (got %lld)", (long long)n_experts);
+  if (topk < 1 || topk > 64) return fail(LH_ERR_INVALID_ARGUMENT, "topk must be in [1, 64] (got %lld)", (long long)topk);
+  return LH_OK;
+}
+
+// Rows of a product: their type (E4M3 with scales, as lh_matvec takes them).
+lh_status check_rows_type(lh_dtype x_dtype, const float* x_scale, int64_t x_group, int64_t rows) {
+  const bool eight = x_dtype == LH_DTYPE_E4M3;
+  if (!eight && !dtype_ok(x_dtype)) return fail(LH_ERR_UNSUPPORTED, "unknown dtype %d", (int)x_dtype);
+  if (x_group != 0 && (x_group != 128 || !eight)) return fail(LH_ERR_INVALID_ARGUMENT, "x_group must be 0, or 128 for E4M3 rows (got %lld)", (long long)x_group);
+  if (eight ? (!x_scale && rows > 0) : x_scale != nullptr)
+    return fail(LH_ERR_INVALID_ARGUMENT, eight ? "x_scale is required for E4M3 rows" : "x_scale must be NULL for rows that are not E4M3");
+  return LH_OK;
+}
+
+int type_of_rows(lh_dtype t) { return t == LH_DTYPE_E4M3 ? 2 : (t == LH_DTYPE_F32 ? 1 : 0); }
+
 }  // namespace
 
 extern "C" {
@@ -144,6 +167,47 @@ lh_status lh_route(const void* logits, lh_dtype dtype, int64_t tokens, int64_t n
   if ((st = guard.enter(dev)) != LH_OK) return st;
   return launched(lh::launch_route(logits, dtype == LH_DTYPE_BF16, tokens, n_experts, topk, renormalize != 0, scale, ids, weights,
                                    reinterpret_cast<hipStream_t>(stream)), "route launch");
+}
+
+int64_t lh_moe_workspace(lh_dtype x_dtype, int64_t tokens, int64_t hidden, int64_t inner, int64_t n_experts, int64_t topk) {
+  if (check_moe(tokens, hidden, inner, n_experts, topk) != LH_OK) return 0;
+  (void)ok();
+  lh::MoeView v{};
+  v.x_type = type_of_rows(x_dtype);
+  v.tokens = tokens;
+  v.hidden = hidden;
+  v.inner = inner;
+  v.experts = n_experts;
+  v.topk = topk;
+  return lh::moe_workspace(v);
+}
+
+lh_status lh_moe(const void* X, lh_dtype x_dtype, const float* x_scale, int64_t x_group, int64_t tokens, int64_t hidden, int64_t inner,
+                 int64_t n_experts, int64_t topk, const int32_t* ids, const float* weights, const uint8_t* gate_up_code,
+                 const uint8_t* gate_up_fp4, const float* gate_up_amax, const uint8_t* down_code, const uint8_t* down_fp4,
+                 const float* down_amax, float scale_norm, void* Y, void* workspace, int64_t workspace_bytes, void* stream) {
+  lh_status st = check_rows_type(x_dtype, x_scale, x_group, tokens);
+  if (st != LH_OK) return st;
+  if ((st = check_moe(tokens, hidden, inner, n_experts, topk)) != LH_OK) return st;
+  if (!e4m3_value(scale_norm)) return fail(LH_ERR_INVALID_ARGUMENT, "scale_norm must be a positive finite E4M3 value such as 448 or 256 (got %g)", (double)scale_norm);
+  if (tokens == 0) return ok();
+  if (!X || !ids || !weights || !gate_up_code || !gate_up_fp4 || !gate_up_amax || !down_code || !down_fp4 || !down_amax || !Y)
+    return fail(LH_ERR_INVALID_ARGUMENT, "X, ids, weights, gate_up_code, gate_up_fp4, gate_up_amax, down_code, down_fp4, down_amax and Y are required");
+  const lh::MoeView v{X, type_of_rows(x_dtype), x_scale, x_group ? (hidden + 127) / 128 : 1, tokens, hidden, inner, n_experts, topk, ids, weights,
+                      gate_up_code, gate_up_fp4, gate_up_amax, down_code, down_fp4, down_amax, 6.0f * scale_norm, Y};
+  const int64_t need = lh::moe_workspace(v);
+  if (!workspace || workspace_bytes < need)
+    return fail(LH_ERR_INVALID_ARGUMENT, "workspace must hold %lld bytes (got %lld)", (long long)need, (long long)(workspace ? workspace_bytes : 0));
+  for (const PtrCheck& p : {PtrCheck{X, "X"}, PtrCheck{Y, "Y"}, PtrCheck{workspace, "workspace"}})
+    if ((st = check_aligned(p.p, p.name)) != LH_OK) return st;
+  if (((reinterpret_cast<uintptr_t>(gate_up_fp4) | reinterpret_cast<uintptr_t>(down_fp4)) & 7) != 0)
+    return fail(LH_ERR_INVALID_ARGUMENT, "gate_up_fp4 and down_fp4 must be 8-byte aligned");
+  int dev = -1;
+  st = check_pointers({{X, "X"}, {x_scale, "x_scale"}, {ids, "ids"}, {weights, "weights"}, {gate_up_code, "gate_up_code"}, {gate_up_fp4, "gate_up_fp4"}, {gate_up_amax, "gate_up_amax"}, {down_code, "down_code"}, {down_fp4, "down_fp4"}, {down_amax, "down_amax"}, {Y, "Y"}, {workspace, "workspace"}}, &dev);
+  if (st != LH_OK) return st;
+  DeviceGuard guard;
+  if ((st = guard.enter(dev)) != LH_OK) return st;
+  return launched(lh::launch_moe(v, workspace, reinterpret_cast<hipStream_t>(stream)), "expert layer launch");
 }
 
 }  // extern "C"

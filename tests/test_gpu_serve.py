@@ -285,3 +285,121 @@ def test_route_masks_and_infinities():
 def test_route_nothing():
     ids, w = lh.lh_route(torch.empty(0, 16, device=DEV), 3)
     assert ids.shape == (0, 3) and w.shape == (0, 3)
+
+
+# ------------------------------------------------------------------------------------------ the expert layer
+def matrices(experts, cout, cin, seed):
+    """NVFP4 weights whose values are near 1 / sqrt(cin): random nibbles, scale codes over a few binades."""
+    r = np.random.default_rng(seed)
+    code = r.integers(0x28, 0x48, (experts, cout, cin // 16)).astype(np.uint8)
+    fp4 = r.integers(0, 256, (experts, cout, cin // 2)).astype(np.uint8)
+    amax = ((0.5 + r.random(experts)) * 700 * cin ** -0.5).astype(np.float32)
+    return code, fp4, amax
+
+
+def on_gpu(m):
+    return tuple(torch.from_numpy(t).to(DEV) for t in m)
+
+
+def layer_rows(rows, cin, x, group, seed):
+    """(tensor, x_scale tensor or None, values in float64)"""
+    g = torch.Generator().manual_seed(seed)
+    v = torch.randn(rows, cin, generator=g)
+    if x != "e4m3":
+        t = v.to(TYPES[x])
+        return t.to(DEV), None, t.double().numpy()
+    width = group or cin
+    q = (v * 100).to(torch.float8_e4m3fn)
+    s = 0.01 * (0.5 + torch.rand(rows, -(-cin // width), generator=g))
+    return q.to(DEV), s.to(DEV), q.double().numpy() * np.repeat(s.double().numpy(), width, 1)[:, :cin]
+
+
+def check_moe(xd, scale, xv, x, group, ids, w, gate_up, down, **kw):
+    """Products are exact and sums fp32: a sum of n terms is off by at most (n + 8) roundings of its terms' magnitudes (every element of
+    fp32 rows is three terms), which the two products pass on; between them exp, the division, three products and the pieces of h."""
+    y = lh.lh_moe(xd, torch.from_numpy(ids).to(DEV), torch.from_numpy(w).to(DEV), on_gpu(gate_up), on_gpu(down), x_scale=scale, x_group=group, **kw)
+    want, terms = serve.moe(xv, ids, w.astype(np.float64), gate_up, down, kw.get("norm", 448.0))
+    hidden, inner = xv.shape[1], down[0].shape[2] * 16
+    pieces = 3 if x == "f32" else 1
+    rel = (pieces * hidden + 8) * U + (3 * inner + 8) * U + 32 * U + (2.0 ** -24 if x == "f32" else 2.0 ** -17) + ids.shape[1] * U
+    bound = rel * terms + 2.0 ** -120
+    bound += HALF["f32" if x == "f32" else "bf16"] * (np.abs(want) + bound)
+    got, none = y.double().cpu().numpy(), np.isnan(want)        # a NaN in a row (8 bits of what is over 464) is one in its outputs
+    np.testing.assert_array_equal(np.isnan(got), none)
+    err, bound, want = np.where(none, 0, np.abs(got - want)), np.where(none, 0, bound), np.where(none, 0, want)
+    assert y.dtype == (torch.float32 if x == "f32" else torch.bfloat16)
+    assert np.all(err <= bound), (float((err / bound).max()), float(err.max()))
+    # and near the plain rounding of the right value in the mean, far under the bound above
+    rms = np.sqrt((err ** 2).mean()) / max(np.sqrt((want ** 2).mean()), 1e-30)
+    assert rms <= (2.0 ** -18 if x == "f32" else 2.0 ** -8), rms
+    return y
+
+
+def choices(tokens, experts, topk, seed):
+    r = np.random.default_rng(seed)
+    ids = np.argsort(r.random((tokens, experts)), 1)[:, :topk].astype(np.int32)
+    w = r.random((tokens, topk)).astype(np.float32)
+    return ids, w / w.sum(1, keepdims=True)
+
+
+# whole and short chunks of 128, less than a chunk, several panels of LDS, shares of k and none, one tile of rows and more
+@pytest.mark.parametrize("tokens,experts,topk,hidden,inner", [(1, 1, 1, 16, 16), (1, 4, 2, 128, 64), (2, 8, 3, 144, 80), (5, 16, 4, 272, 144), (17, 3, 2, 256, 128),
+                                                              (64, 2, 1, 384, 48), (65, 5, 2, 640, 272), (33, 40, 10, 512, 32), (130, 6, 3, 112, 208),
+                                                              (3, 7, 2, 2560, 640), (40, 2, 2, 2064, 1040), (1, 3, 3, 5136, 96), (20, 300, 6, 64, 16)])
+@pytest.mark.parametrize("x,group", [("bf16", 0), ("f32", 0), ("e4m3", 0), ("e4m3", 128)])
+def test_moe(tokens, experts, topk, hidden, inner, x, group):
+    note(f"moe {tokens} tokens top {topk} of {experts}, {hidden} x {inner}, {x} group {group}")
+    gate_up, down = matrices(experts, 2 * inner, hidden, 1), matrices(experts, hidden, inner, 2)
+    xd, scale, xv = layer_rows(tokens, hidden, x, group, 3)
+    ids, w = choices(tokens, experts, topk, 4)
+    check_moe(xd, scale, xv, x, group, ids, w, gate_up, down)
+
+
+def test_moe_choices():
+    """Skipped and repeated choices, tokens without any, every token at one expert, weights of either sign, the other normalization."""
+    gate_up, down = matrices(9, 128, 256, 5), matrices(9, 256, 64, 6)
+    xd, scale, xv = layer_rows(70, 256, "bf16", 0, 7)
+    r = np.random.default_rng(8)
+    ids = r.integers(-2, 11, (70, 6)).astype(np.int32)             # repeats, and some outside
+    ids[3], ids[69], ids[10] = -1, 2 ** 31 - 1, 4
+    w = r.standard_normal((70, 6)).astype(np.float32)
+    note("moe with repeats and choices outside")
+    y = check_moe(xd, scale, xv, "bf16", 0, ids, w, gate_up, down, norm=256.0)
+    assert torch.count_nonzero(y[[3, 69]]) == 0
+    note("moe with every token at one expert")
+    check_moe(xd, scale, xv, "bf16", 0, np.full((70, 2), 8, np.int32), np.full((70, 2), 0.5, np.float32), gate_up, down)
+    note("moe with no choice at all")
+    y = check_moe(xd, scale, xv, "bf16", 0, np.full((70, 2), -1, np.int32), np.ones((70, 2), np.float32), gate_up, down)
+    assert torch.count_nonzero(y) == 0
+
+
+@pytest.mark.parametrize("x", ["bf16", "f32"])
+def test_moe_infinities_stay_in_their_rows(x):
+    note(f"moe infinities {x}")
+    gate_up, down = matrices(4, 96, 160, 9), matrices(4, 160, 48, 10)
+    xd, _, _ = layer_rows(6, 160, x, 0, 11)
+    ids, w = choices(6, 4, 2, 12)
+    args = [torch.from_numpy(t).to(DEV) for t in (ids, w)]
+    clean = lh.lh_moe(xd, *args, on_gpu(gate_up), on_gpu(down))
+    bad = xd.clone()
+    bad[1, 5], bad[4, 159] = float("nan"), float("inf")
+    y = lh.lh_moe(bad, *args, on_gpu(gate_up), on_gpu(down))
+    keep = [0, 2, 3, 5]
+    assert torch.equal(y[keep], clean[keep])
+    assert bool(torch.isnan(y[1]).all()) and not bool(torch.isfinite(y[4]).all())
+
+
+def test_moe_large_activations():
+    """silu far from 0: gates where exp overflows or the weight of the up product is next to nothing."""
+    note("moe large activations")
+    gate_up, down = matrices(2, 64, 64, 13), matrices(2, 64, 32, 14)
+    xd, _, _ = layer_rows(4, 64, "f32", 0, 15)
+    xd = xd * torch.tensor([1e3, 1e-3, 1e6, 30.0], device=DEV)[:, None]
+    ids, w = choices(4, 2, 2, 16)
+    check_moe(xd.contiguous(), None, xd.double().cpu().numpy(), "f32", 0, ids, w, gate_up, down)
+
+
+def test_moe_nothing():
+    y = lh.lh_moe(torch.empty(0, 32, device=DEV), torch.empty(0, 2, dtype=torch.int32, device=DEV), torch.empty(0, 2, device=DEV),
+                  on_gpu(matrices(2, 32, 32, 1)), on_gpu(matrices(2, 32, 16, 1)))
+    assert y.shape == (0, 32)
