@@ -588,6 +588,31 @@ lh_status lh_moe(const void* X, lh_dtype x_dtype, const float* x_scale, int64_t 
 int64_t lh_moe_workspace(lh_dtype x_dtype, int64_t tokens, int64_t hidden, int64_t inner, int64_t n_experts,
                          int64_t topk);
 
+/*
+ * Low-rank adapters of many requests at once, beside a projection that they share (lh_matvec's, of the same rows):
+ *   Y[t] = base[t] + scaling[a] * B_a (A_a x_t),   a = index[t];   Y[t] = base[t] where a is outside [0, n_adapters)
+ * A [n_adapters, rank, cin] and B [n_adapters, cout, rank] of w_dtype (F32 or BF16); ranks [n_adapters] int32 or NULL: adapter a has
+ * ranks[a] (taken as between 0 and rank) rows of A and columns of B, and what is stored past those does not count, whatever it is;
+ * NULL: all have `rank`.  scaling [n_adapters] fp32 or NULL (1).  index [rows] int32.
+ * X [rows, cin], x_scale and x_group as in lh_matvec; base and Y [rows, cout], F32 for F32 rows, BF16 otherwise; Y may be base.
+ * Products of BF16 weights are exact (fp32 elements as in lh_matvec), those of F32 weights fp32 (E4M3 elements are then multiplied by
+ * their scale first); A_a x_t is held to 2^-17 of itself with BF16 weights and Y, otherwise to 2^-24; sums are fp32, in a
+ * fixed order, and Y is rounded once.  Infinities and NaN in a row change no other row.
+ * The weights of an adapter are read again for every 64 rows, and A for every 16 rows of an adapter among those.
+ * workspace: device memory of at least lh_adapter_workspace bytes (16-byte aligned) that no other call uses until this one has run.
+ * Errors: UNSUPPORTED for an unknown dtype; INVALID_ARGUMENT for rows outside [0, 4194240], cin <= 0, over 2^24 or not a multiple of
+ * 16, cout outside [0, 2^24], n_adapters outside [1, 4096], rank outside [8, 256] or not a multiple of 8, x_scale or x_group that do
+ * not fit the type, a launch of 2^32 or more work-items, NULL required pointers, a short workspace, pointers not 16-byte
+ * aligned (X, A, B, base, Y), non-device or mixed-device pointers.
+ */
+lh_status lh_adapter(const void* X, lh_dtype x_dtype, const float* x_scale, int64_t x_group, int64_t rows,
+                     int64_t cin, int64_t cout, int64_t n_adapters, int64_t rank, const void* A, const void* B,
+                     lh_dtype w_dtype, const int32_t* index, const float* scaling, const int32_t* ranks,
+                     const void* base, void* Y, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that lh_adapter needs for these sizes (a host computation; 0 for ones that it refuses). */
+int64_t lh_adapter_workspace(int64_t rows, int64_t cin, int64_t n_adapters, int64_t rank);
+
 /* Message of the last error on the calling thread ("" if none); valid until its next call. */
 const char* lh_last_error(void);
 

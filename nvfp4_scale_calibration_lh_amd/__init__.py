@@ -28,7 +28,8 @@ EXPORTED = ("lh_accumulate", "lh_accumulate_noalloc", "lh_accumulate_act_aware",
             "lh_accumulate_sweep", "lh_dequantize", "lh_dequantize_ex", "lh_scale_sweep", "lh_scale_sweep_ex", "lh_scale_sweep_diag",
             "lh_scale_sweep_diag_ex", "lh_scale_sweep_mse", "lh_absmax", "lh_rms_norm_quant", "lh_matvec", "lh_cache_write",
             "lh_cache_read", "lh_paged_attention", "lh_paged_attention_workspace", "lh_cache_extend", "lh_cache_extend_workspace",
-           "lh_rotary", "lh_rotary_frequencies", "lh_route", "lh_moe", "lh_moe_workspace", "lh_last_error", "lh_version")
+           "lh_rotary", "lh_rotary_frequencies", "lh_route", "lh_moe", "lh_moe_workspace", "lh_adapter",
+           "lh_adapter_workspace", "lh_last_error", "lh_version")
 MAX_MULTIPLIERS = 128
 
 
@@ -91,14 +92,16 @@ def lib() -> ctypes.CDLL:
         h.lh_route.argtypes = [vp, i32, i64, i64, i64, i32, f32, vp, vp, vp]
         h.lh_moe.argtypes = [vp, i32, vp, i64, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, f32, vp, vp, i64, vp]
         h.lh_moe_workspace.argtypes = [i32, i64, i64, i64, i64, i64]
+        h.lh_adapter.argtypes = [vp, i32, vp, i64, i64, i64, i64, i64, i64, vp, vp, i32, vp, vp, vp, vp, vp, vp, i64, vp]
+        h.lh_adapter_workspace.argtypes = [i64, i64, i64, i64]
         for f in ("lh_accumulate", "lh_accumulate_noalloc", "lh_accumulate_act_aware", "lh_accumulate_act_aware_fq",
                   "lh_activation_fake_quant", "lh_scale_sweep", "lh_scale_sweep_ex", "lh_scale_sweep_diag_ex",
                   "lh_dequantize_ex", "lh_accumulate_sweep",
                   "lh_scale_sweep_diag", "lh_scale_sweep_mse", "lh_absmax", "lh_dequantize", "lh_rms_norm_quant",
                   "lh_matvec", "lh_cache_write", "lh_cache_read", "lh_paged_attention", "lh_cache_extend",
-                  "lh_rotary_frequencies", "lh_rotary", "lh_route", "lh_moe"):
+                  "lh_rotary_frequencies", "lh_rotary", "lh_route", "lh_moe", "lh_adapter"):
             getattr(h, f).restype = ctypes.c_int
-        for f in ("lh_paged_attention_workspace", "lh_cache_extend_workspace", "lh_moe_workspace"):
+        for f in ("lh_paged_attention_workspace", "lh_cache_extend_workspace", "lh_moe_workspace", "lh_adapter_workspace"):
             getattr(h, f).restype = ctypes.c_int64
         h.lh_last_error.argtypes = []
         h.lh_last_error.restype = ctypes.c_char_p
@@ -856,4 +859,48 @@ def lh_moe(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate_up: T
     _check(lib().lh_moe(X.data_ptr(), dtype, _ptr(x_scale), x_group, tokens, hidden, inner, experts, topk, ids.data_ptr(), weights.data_ptr(),
                         gate_up[0].data_ptr(), gate_up[1].data_ptr(), gate_up[2].data_ptr(), down[0].data_ptr(), down[1].data_ptr(),
                         down[2].data_ptr(), norm, Y.data_ptr(), workspace.data_ptr(), nbytes, _stream(device)))
+    return Y
+
+
+def lh_adapter_workspace(rows: int, cin: int, n_adapters: int, rank: int) -> int:
+    """Bytes of workspace that lh_adapter needs for these sizes."""
+    return int(lib().lh_adapter_workspace(rows, cin, n_adapters, rank))
+
+
+def lh_adapter(X: torch.Tensor, base: torch.Tensor, A: torch.Tensor, B: torch.Tensor, index: torch.Tensor, Y: Optional[torch.Tensor] = None, *,
+               scaling: Optional[torch.Tensor] = None, ranks: Optional[torch.Tensor] = None, x_scale: Optional[torch.Tensor] = None,
+               x_group: int = 0, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y [rows, cout]: base + scaling[a] * B[a] (A[a] x) for each row x of X [rows, cin] (fp32, bf16, or torch.float8_e4m3fn with x_scale and
+    x_group as lh_matvec takes them) with its adapter a = index[row] (int32; outside [0, n): base alone).  A [n, rank, cin] and
+    B [n, cout, rank] are both fp32 or both bf16, of which adapter a has ranks[a] (int32 [n]; None: rank) rows and columns; scaling
+    [n] fp32 (None: 1).  base and Y are fp32 for fp32 X, otherwise bf16; Y may be base.  workspace (uint8) is allocated on the current stream when not given."""
+    _need(X, "X")
+    if X.dim() != 2 or A.dim() != 3 or B.dim() != 3:
+        raise ValueError("X must be [rows, cin], A [n, rank, cin] and B [n, cout, rank]")
+    rows, cin = X.shape
+    device = X.device
+    dtype, x_group = _rows_type(X, x_scale, x_group)
+    n, cout, rank = B.shape
+    _need(A, "A", (n, rank, cin))
+    _need(B, "B", dtype=A.dtype)
+    _need(index, "index", (rows,), torch.int32)
+    if scaling is not None:
+        _need(scaling, "scaling", (n,), torch.float32)
+    if ranks is not None:
+        _need(ranks, "ranks", (n,), torch.int32)
+    shape, y_dtype = (rows, cout), torch.float32 if dtype == LH_DTYPE_F32 else torch.bfloat16
+    _need(base, "base", shape, y_dtype)
+    if Y is None:
+        Y = _empty(rows, cout, dtype=y_dtype, device=device)
+    else:
+        _need(Y, "Y", shape, y_dtype)
+    if workspace is not None:
+        _need(workspace, "workspace", dtype=torch.uint8)
+        nbytes = workspace.numel()
+    else:
+        nbytes = lib().lh_adapter_workspace(rows, cin, n, rank)
+        workspace = _empty(nbytes, dtype=torch.uint8, device=device)
+    _check(lib().lh_adapter(X.data_ptr(), dtype, _ptr(x_scale), x_group, rows, cin, cout, n, rank, A.data_ptr(), B.data_ptr(), _dtype_code(A),
+                            index.data_ptr(), _ptr(scaling), _ptr(ranks), base.data_ptr(), Y.data_ptr(), workspace.data_ptr(), nbytes,
+                            _stream(device)))
     return Y

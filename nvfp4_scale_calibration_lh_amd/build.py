@@ -15,7 +15,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "liblh.so")
 SOURCES = ["absmax.hip", "accumulate.hip", "sweep.hip", "dequant.hip", "rms_norm.hip", "matvec.hip", "cache.hip",
-           "attention.hip", "extend.hip", "rotary.hip", "route.hip", "moe.hip", "lh_abi.cpp", "lh_decode.cpp", "lh_serve.cpp"]
+           "attention.hip", "extend.hip", "rotary.hip", "route.hip", "moe.hip", "adapter.hip",
+           "lh_abi.cpp", "lh_decode.cpp", "lh_serve.cpp"]
 ARCH = "gfx950"
 # Packed fp32 ALU instructions are kept out of the generated code; MFMA results live in VGPRs
 # (no accumulator-register copies in the sweep loop).

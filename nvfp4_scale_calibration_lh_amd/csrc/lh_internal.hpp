@@ -175,4 +175,22 @@ struct MoeView {
 int64_t moe_workspace(const MoeView& v);
 hipError_t launch_moe(const MoeView& v, void* work, hipStream_t stream);
 
+// Low-rank adapters (lh_adapter): x_type as launch_matvec, w_f32 the type of a and b; scaling and ranks may be NULL, y may be base.
+// adapter_workspace is its scratch in bytes.
+struct AdapterView {
+  const void* x;
+  int x_type;
+  const float* x_scale;
+  int64_t x_scales, rows, cin, cout, adapters, rank;
+  const void *a, *b;
+  bool w_f32;
+  const int* index;
+  const float* scaling;
+  const int* ranks;
+  const void* base;
+  void* y;
+};
+int64_t adapter_workspace(const AdapterView& v);
+hipError_t launch_adapter(const AdapterView& v, void* work, hipStream_t stream);
+
 }  // namespace lh

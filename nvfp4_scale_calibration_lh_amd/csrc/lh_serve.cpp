@@ -37,6 +37,15 @@ lh_status check_moe(int64_t tokens, int64_t hidden, int64_t inner, int64_t n_exp
   return LH_OK;
 }
 
+lh_status check_adapter(int64_t rows, int64_t cin, int64_t cout, int64_t n_adapters, int64_t rank) {
+  if (rows < 0 || rows > 65535 * 64) return fail(LH_ERR_INVALID_ARGUMENT, "rows must be in [0, 4194240] (got %lld)", (long long)rows);
+  if (cin <= 0 || cin % 16 || cin > (int64_t(1) << 24)) return fail(LH_ERR_INVALID_ARGUMENT, "cin must be a positive multiple of 16 up to 2^24 (got %lld)", (long long)cin);
+  if (cout < 0 || cout > (int64_t(1) << 24)) return fail(LH_ERR_INVALID_ARGUMENT, "cout must be in [0, 2^24] (got %lld)", (long long)cout);
+  if (n_adapters < 1 || n_adapters > lh::kMaxExperts) return fail(LH_ERR_INVALID_ARGUMENT, "n_adapters must be in [1, 4096] (got %lld)", (long long)n_adapters);
+  if (rank < 8 || rank % 8 || rank > 256) return fail(LH_ERR_INVALID_ARGUMENT, "rank must be a multiple of 8 in [8, 256] (got %lld)", (long long)rank);
+  return LH_OK;
+}
+
 // Rows of a product: their type (E4M3 with scales, as lh_matvec takes them).
 lh_status check_rows_type(lh_dtype x_dtype, const float* x_scale, int64_t x_group, int64_t rows) {
   const bool eight = x_dtype == LH_DTYPE_E4M3;
@@ -208,6 +217,42 @@ lh_status lh_moe(const void* X, lh_dtype x_dtype, const float* x_scale, int64_t 
   DeviceGuard guard;
   if ((st = guard.enter(dev)) != LH_OK) return st;
   return launched(lh::launch_moe(v, workspace, reinterpret_cast<hipStream_t>(stream)), "expert layer launch");
+}
+
+int64_t lh_adapter_workspace(int64_t rows, int64_t cin, int64_t n_adapters, int64_t rank) {
+  if (check_adapter(rows, cin, 0, n_adapters, rank) != LH_OK) return 0;
+  (void)ok();
+  lh::AdapterView v{};
+  v.rows = rows;
+  v.cin = cin;
+  v.adapters = n_adapters;
+  v.rank = rank;
+  return lh::adapter_workspace(v);
+}
+
+lh_status lh_adapter(const void* X, lh_dtype x_dtype, const float* x_scale, int64_t x_group, int64_t rows, int64_t cin, int64_t cout,
+                     int64_t n_adapters, int64_t rank, const void* A, const void* B, lh_dtype w_dtype, const int32_t* index,
+                     const float* scaling, const int32_t* ranks, const void* base, void* Y, void* workspace, int64_t workspace_bytes,
+                     void* stream) {
+  lh_status st = check_rows_type(x_dtype, x_scale, x_group, rows);
+  if (st != LH_OK) return st;
+  if (!dtype_ok(w_dtype)) return fail(LH_ERR_UNSUPPORTED, "unknown dtype %d of A and B", (int)w_dtype);
+  if ((st = check_adapter(rows, cin, cout, n_adapters, rank)) != LH_OK) return st;
+  if (rows == 0 || cout == 0) return ok();
+  if (!X || !A || !B || !index || !base || !Y) return fail(LH_ERR_INVALID_ARGUMENT, "X, A, B, index, base and Y are required");
+  const lh::AdapterView v{X, type_of_rows(x_dtype), x_scale, x_group ? (cin + 127) / 128 : 1, rows, cin, cout, n_adapters, rank, A, B,
+                          w_dtype == LH_DTYPE_F32, index, scaling, ranks, base, Y};
+  const int64_t need = lh::adapter_workspace(v);
+  if (!workspace || workspace_bytes < need)
+    return fail(LH_ERR_INVALID_ARGUMENT, "workspace must hold %lld bytes (got %lld)", (long long)need, (long long)(workspace ? workspace_bytes : 0));
+  for (const PtrCheck& p : {PtrCheck{X, "X"}, PtrCheck{A, "A"}, PtrCheck{B, "B"}, PtrCheck{base, "base"}, PtrCheck{Y, "Y"}, PtrCheck{workspace, "workspace"}})
+    if ((st = check_aligned(p.p, p.name)) != LH_OK) return st;
+  int dev = -1;
+  st = check_pointers({{X, "X"}, {x_scale, "x_scale"}, {A, "A"}, {B, "B"}, {index, "index"}, {scaling, "scaling"}, {ranks, "ranks"}, {base, "base"}, {Y, "Y"}, {workspace, "workspace"}}, &dev);
+  if (st != LH_OK) return st;
+  DeviceGuard guard;
+  if ((st = guard.enter(dev)) != LH_OK) return st;
+  return launched(lh::launch_adapter(v, workspace, reinterpret_cast<hipStream_t>(stream)), "adapter launch");
 }
 
 }  // extern "C"

@@ -12,6 +12,7 @@
 //
 // Values of weights and rows are exact as in the products of few rows (see nvfp4_weights.hpp); h is held to 2^-17 of itself
 // (its second piece rounds to 8 bits; fp32 rows: to 2^-24 by a third), so that nothing but y rounds to 8 bits.  Sums are fp32, in a fixed order.
+#include "grouping.hpp"
 #include "lh_internal.hpp"
 #include "nvfp4_weights.hpp"
 
@@ -20,7 +21,6 @@
 namespace lh {
 namespace {
 
-constexpr int kTokens = 64;                  // of one pass over the weights: one a lane
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kU = 2;                        // chunks of k a wave takes at a time: whole 128-byte lines of a channel
@@ -44,44 +44,6 @@ struct Args {
   int hidden, inner, experts, topk, x_scales, slots, split;
   float gdiv;
 };
-
-// What the first kernel leaves of a slot for the second: the expert, its number of rows (0: none) and their choices (token * topk + j).
-constexpr int kPlan = 4 + kTokens;
-
-__device__ inline uint64_t lane_of(uint64_t v, int lane) {
-  return (uint64_t)(unsigned)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 | (unsigned)__builtin_amdgcn_readlane((int)v, lane);
-}
-
-// The slot-th of the experts whose bits are set, or -1.
-__device__ inline int find_expert(const uint64_t* bits, int slot) {
-  const int lane = threadIdx.x & 63;
-  const uint64_t word = bits[lane];
-  const int mine = __popcll(word);
-  int upto = mine;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int v = __shfl_up(upto, o, 64);
-    if (lane >= o) upto += v;
-  }
-  const uint64_t there = __ballot(upto > slot);
-  if (there == 0) return -1;
-  const int owner = __ffsll((unsigned long long)there) - 1;
-  uint64_t w = lane_of(word, owner);
-  for (int k = slot - __builtin_amdgcn_readlane(upto - mine, owner); k > 0; --k) w &= w - 1;
-  return 64 * owner + __ffsll((unsigned long long)w) - 1;
-}
-
-// Truncated pieces of 8 bits each, the last one rounded; an infinity or NaN is its first piece.
-template <int P>
-__device__ inline void split(float x, __bf16* out) {
-#pragma unroll
-  for (int p = 0; p + 1 < P; ++p) {
-    const float hi = __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
-    out[p] = __builtin_bit_cast(__bf16, (unsigned short)(__float_as_uint(x) >> 16));
-    x = x == hi ? 0.0f : x - hi;
-  }
-  out[P - 1] = (__bf16)x;
-}
 
 struct Weights {
   v4u nib;

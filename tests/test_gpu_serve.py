@@ -403,3 +403,93 @@ def test_moe_nothing():
     y = lh.lh_moe(torch.empty(0, 32, device=DEV), torch.empty(0, 2, dtype=torch.int32, device=DEV), torch.empty(0, 2, device=DEV),
                   on_gpu(matrices(2, 32, 32, 1)), on_gpu(matrices(2, 32, 16, 1)))
     assert y.shape == (0, 32)
+
+
+# ------------------------------------------------------------------------------------------------- adapters
+def adapter_case(rows, cin, cout, n, rank, x, group, weights, seed, ragged=True):
+    """Arguments on the GPU and in float64; what lies past an adapter's rank is NaN."""
+    g, r = torch.Generator().manual_seed(seed), np.random.default_rng(seed)
+    xd, scale, xv = layer_rows(rows, cin, x, group, seed)
+    base = torch.randn(rows, cout, generator=g).to(torch.float32 if x == "f32" else torch.bfloat16)
+    a = (torch.randn(n, rank, cin, generator=g) * cin ** -0.5).to(TYPES[weights])
+    b = torch.randn(n, cout, rank, generator=g).to(TYPES[weights])
+    index = r.integers(0, n, rows)
+    index[r.random(rows) < 0.2] = r.choice([-1, n, 2 ** 31 - 1, -2 ** 31])
+    ranks = r.integers(0, rank + 1, n) if ragged else None
+    if ragged:
+        for k, m in enumerate(ranks):
+            a[k, m:], b[k, :, m:] = float("nan"), float("nan")
+    scaling = (r.random(n) * 2 - 0.5).astype(np.float32)
+    return xd, scale, xv, base.to(DEV), a.to(DEV), b.to(DEV), index.astype(np.int32), ranks, scaling
+
+
+def check_adapter(case, x, group, weights, **kw):
+    """Sums of n terms are off by at most (n + 8) roundings of their terms' magnitudes (fp32 elements are three terms each, fp32
+    weights round their products, too), u by its pieces and its scaling, and Y once more by its type."""
+    xd, scale, xv, base, a, b, index, ranks, scaling = case
+    args = dict(scaling=torch.from_numpy(scaling).to(DEV), ranks=None if ranks is None else dev(ranks), x_scale=scale, x_group=group)
+    y = lh.lh_adapter(xd, base, a, b, dev(index), **args, **kw)
+    want, terms = serve.adapter(xv, base.double().cpu().numpy(), a.double().cpu().numpy(), b.double().cpu().numpy(), index, scaling, ranks)
+    held = 2.0 ** -24 if x == "f32" or weights == "f32" else 2.0 ** -17
+    rel = (3 * a.shape[2] + 8) * U + (3 * a.shape[1] + 8) * U + 8 * U + held
+    none = np.isnan(want)
+    np.testing.assert_array_equal(np.isnan(y.double().cpu().numpy()), none)
+    want, terms = np.where(none, 0, want), np.where(none, 0, terms)
+    bound = rel * terms
+    bound += HALF["f32" if x == "f32" else "bf16"] * (np.abs(want) + bound)
+    err = np.where(none, 0, np.abs(y.double().cpu().numpy() - want))
+    assert y.dtype == base.dtype and np.all(err <= bound), (float((err / bound).max()), float(err.max()))
+    # in the mean far under that: a bf16 rounding, or a few fp32 ones
+    assert np.sqrt((err ** 2).mean()) <= (2.0 ** -19 if x == "f32" else 2.0 ** -8) * np.sqrt((want ** 2).mean())
+    out = (index < 0) | (index >= len(a))
+    assert torch.equal(y[torch.from_numpy(out).to(DEV)], base[torch.from_numpy(out).to(DEV)])
+    return y
+
+
+@pytest.mark.parametrize("rows,cin,cout,n,rank", [(1, 16, 1, 1, 8), (1, 4096, 512, 3, 16), (5, 144, 30, 2, 8), (17, 256, 257, 1, 24), (64, 528, 100, 7, 64),
+                                                  (65, 640, 1000, 70, 40), (130, 272, 260, 3, 72), (33, 2064, 68, 4, 128), (20, 1040, 52, 2, 136),
+                                                  (9, 384, 2049, 5, 256), (40, 12288, 130, 40, 16)])
+@pytest.mark.parametrize("x,group", [("bf16", 0), ("f32", 0), ("e4m3", 0), ("e4m3", 128)])
+@pytest.mark.parametrize("weights", ["bf16", "f32"])
+def test_adapter(rows, cin, cout, n, rank, x, group, weights):
+    note(f"adapter {rows} rows {cin} to {cout}, {n} of rank {rank} {weights}, {x} group {group}")
+    case = adapter_case(rows, cin, cout, n, rank, x, group, weights, rows + rank)
+    y = check_adapter(case, x, group, weights)
+    xd, scale, _, base, a, b, index, ranks, scaling = case
+    again = base.clone()
+    lh.lh_adapter(xd, again, a, b, dev(index), again, scaling=torch.from_numpy(scaling).to(DEV), ranks=dev(ranks), x_scale=scale, x_group=group)
+    assert torch.equal(again.view(torch.uint8), y.view(torch.uint8))          # in place, the same bits
+
+
+def test_adapter_full_ranks_and_no_scaling():
+    note("adapter without ranks, one request for all rows")
+    case = adapter_case(70, 256, 192, 2, 32, "bf16", 0, "bf16", 4, ragged=False)
+    case[6][:] = 1
+    check_adapter(case, "bf16", 0, "bf16")
+    xd, _, _, base, a, b, index, _, scaling = case
+    y = lh.lh_adapter(xd, base, a, b, dev(index))
+    one = lh.lh_adapter(xd, base, a, b, dev(index), scaling=torch.ones(2, device=DEV), ranks=dev([32, 32]))
+    assert torch.equal(y, one)
+    note("adapter with no row that has one")
+    y = lh.lh_adapter(xd, base, a, b, dev(np.full(70, -1)))
+    assert torch.equal(y, base)
+
+
+def test_adapter_infinities_stay_in_their_rows():
+    note("adapter infinities")
+    xd, _, _, base, a, b, index, _, _ = adapter_case(6, 144, 64, 2, 16, "bf16", 0, "bf16", 5, ragged=False)
+    index[:] = [0, 0, 1, 1, 0, -1]
+    clean = lh.lh_adapter(xd, base, a, b, dev(index))
+    bad = xd.clone()
+    bad[0, 3], bad[2, 143], bad[5, 0] = float("nan"), float("inf"), float("nan")
+    y = lh.lh_adapter(bad, base, a, b, dev(index))
+    assert torch.equal(y[[1, 3, 4, 5]], clean[[1, 3, 4, 5]])
+    assert bool(torch.isnan(y[0]).all()) and not bool(torch.isfinite(y[2]).all())
+
+
+def test_adapter_nothing():
+    a, b = torch.zeros(2, 8, 32, device=DEV), torch.zeros(2, 40, 8, device=DEV)
+    y = lh.lh_adapter(torch.empty(0, 32, device=DEV), torch.empty(0, 40, device=DEV), a, b, dev([]))
+    assert y.shape == (0, 40)
+    y = lh.lh_adapter(torch.ones(3, 32, device=DEV), torch.empty(3, 0, device=DEV), a, torch.zeros(2, 0, 8, device=DEV), dev([0, 1, 0]))
+    assert y.shape == (3, 0)
