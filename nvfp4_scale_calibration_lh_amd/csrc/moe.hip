@@ -2,16 +2,19 @@
 //   y[t] = sum_j w[t, j] D_e (silu(G_e x[t]) * U_e x[t]),  e = ids[t, j],  silu(g) = g / (1 + exp(-g))
 //
 // Bound by reading the weights of every expert that is hit once (0.5625 bytes each).  Three kernels:
-//   gate and up  a workgroup takes the n-th expert that the (up to 64) tokens hit, which it finds from the ids by itself, and some
-//                of its channels; a wave has 8 gate rows and the 8 up rows that belong to them as one 16-row operand, so that
-//                silu(g) * u needs no other wave.  h = w * silu(g) * u goes to the workspace as two (fp32: three) bf16 pieces.
+//   gate and up  the channels of all experts that (up to 64) tokens hit, in tiles, are shared out evenly over as many workgroups as
+//                are resident; each finds the experts of its share and their rows from the ids by itself.  A wave has 8 gate rows
+//                and the 8 up rows that belong to them as one 16-row operand, so that silu(g) * u needs no other wave.
+//                h = w * silu(g) * u goes to the workspace in fp32.
 //   down         the same walk over D_e with h for x, one fp32 row for each chosen expert of a token
 //   sum          adds a token's rows in the order of its choices
-// The rows (x or h) are staged in LDS and shared by the workgroup's waves; the weights stream through registers, each
-// wave its own channels, or KS waves a share of k each where that is needed to fill the chip.
+// The rows (x or h) are staged in LDS, as much of k as fits, and shared by the workgroup's waves; the weights stream through registers, each
+// wave its own channels, or `split` waves a share of k each where that is needed to fill the chip.
 //
-// Values of weights and rows are exact as in the products of few rows (see nvfp4_weights.hpp); h is held to 2^-17 of itself
-// (its second piece rounds to 8 bits; fp32 rows: to 2^-24 by a third), so that nothing but y rounds to 8 bits.  Sums are fp32, in a fixed order.
+// A weight's E2M1 value times its block's E4M3 scale has at most 6 significant bits in [2^-10, 2688], exact in fp16.  Rows are fp16
+// with a factor for each 128 elements: E4M3 values exactly, with the scale they came with; bf16 and fp32 times the power of two that
+// takes the largest of the 128 to [2^14, 2^15), fp32 in two pieces: bf16 exactly from 2^-31 of that largest element on and to within
+// 2^-39 of it below, fp32 to 2^-23 of itself and 2^-39 of the largest.  Products are exact, sums fp32, in a fixed order.
 #include "grouping.hpp"
 #include "lh_internal.hpp"
 #include "nvfp4_weights.hpp"
@@ -23,10 +26,9 @@ namespace {
 
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kU = 2;                        // chunks of k a wave takes at a time: whole 128-byte lines of a channel
-constexpr int kD = 3;                        // steps whose weights are held or on their way
-constexpr int kBudget = 52 * 1024;           // LDS of the rows, so that three workgroups fit a compute unit
-constexpr int kComputeUnits = 256;
+constexpr int kU = 4;                        // chunks of k a wave takes at a time, at most
+constexpr int kBudget = 66 * 1024;           // LDS of the rows, so that two workgroups fit a compute unit
+constexpr int kResident = 2 * 256;           // workgroups
 
 struct Args {
   const void* x;
@@ -36,304 +38,328 @@ struct Args {
   const uint8_t* code;
   const uint8_t* fp4;
   const float* amax;
+  int* hits;                                 // experts hit by each 64 tokens
   int* plan;
-  __bf16* h;
+  float* h;
   float* part;
   void* y;
   int64_t tokens;
-  int hidden, inner, experts, topk, x_scales, slots, split;
+  int hidden, inner, experts, topk, x_scales, slots;
+  int split, each;                           // waves that share k; chunks of a step
   float gdiv;
 };
 
+typedef uint16_t u16_a1 __attribute__((aligned(1)));
+
+// 32 nibbles of one channel and the scales of their two blocks.
 struct Weights {
   v4u nib;
-  v2u code;
+  unsigned code;
 };
 
-// X: type of x.  DOWN: the second product, whose rows are h.  P: bf16 (E4M3: fp16) pieces of a row's element.  HP: pieces of h.
-// CT: 16-row tiles of rows taken at a time; an expert with more rows has its weights read again.
-template <int X, bool DOWN, int P, int HP, int CT>
-__global__ __launch_bounds__(kThreads) void k_experts(const Args a) {
-  constexpr bool EIGHT = X == kXE4m3 && !DOWN;
-  constexpr int WX = EIGHT ? kXE4m3 : kXBf16;
-  using frag = typename Frag<WX>::type;
+__device__ inline unsigned row_max(unsigned v) {     // over 16 neighbouring lanes
+#define LH_STEP(n) v = max(v, (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + n, 0xf, 0xf, false))
+  LH_STEP(8);
+  LH_STEP(4);
+  LH_STEP(2);
+  LH_STEP(1);
+#undef LH_STEP
+  return v;
+}
+
+// n / d for n < 2^21, by the reciprocal of d (a quotient is at least 0.5 / d away from the next whole number).
+__device__ inline int quotient(int n, float reciprocal) { return (int)(((float)n + 0.5f) * reciprocal); }
+
+// 1 / (1 + exp(-g)) * g; the power of two from the exact product's two halves.
+__device__ inline float silu(float g) {
+  constexpr float kHigh = -1.4426950216293335f, kLow = -1.9259629911e-8f;       // -log2(e)
+  const float t = g * kHigh, rest = fmaf(g, kHigh, -t) + g * kLow;
+  const float e = __builtin_amdgcn_exp2f(t) * (fabsf(t) < 1e30f ? 1.0f + rest * 0.6931471824645996f : 1.0f);     // exp(-g)
+  return g / (1.0f + e);
+}
+
+// X: type of the rows, in P pieces.  DOWN: the second product, whose rows are h.  MT: 16-row tiles taken at a time at most.  SMALL: k is
+// less than a chunk.
+//
+// Instructions are fetched from cold caches at each launch (0.6 us a KB was seen), which a call for one token feels: so the code is short, its
+// loops are not unrolled further than the registers ask for, and there are no 64-bit divisions.
+template <int X, int P, bool DOWN, int MT, bool SMALL>
+__global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
+  constexpr int kRows = DOWN ? 16 : 8;       // channels of a tile
   __shared__ uint64_t bits[64];
-  __shared__ int rows[kTokens];
+  __shared__ int rows[kTokens], source[kTokens];                     // an expert's rows: choices, and rows of x
   __shared__ float share[kTokens];
   __shared__ int found;
-  extern __shared__ char lds[];
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  float* red = (float*)(lds + kBudget);
+  short* chosen = (short*)(lds + kBudget + kWaves * 1024);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, quarter = lane >> 4;
-  const int ks = wave % a.split, together = kWaves / a.split;      // tiles of the workgroup
-  const int tiles = DOWN ? a.hidden / 16 : a.inner / 8, groups = (tiles + together - 1) / together;
-  const int slot = blockIdx.x / (unsigned)groups, group = blockIdx.x % (unsigned)groups;
-  const int tile = min(group * together + wave / a.split, tiles - 1);
-  const bool own = group * together + wave / a.split < tiles && ks == 0;
-  int* plan = a.plan + ((int64_t)blockIdx.y * a.slots + slot) * kPlan;
-  int expert, n;
+  const int shift = __builtin_ctz(a.split), ks = wave & (a.split - 1), mine = wave >> shift, together = kWaves >> shift;    // tiles of the workgroup
+  const int tiles = (DOWN ? a.hidden : a.inner) / kRows, groups = (tiles + together - 1) >> (3 - shift);
+  const int64_t token0 = (int64_t)blockIdx.y * kTokens;
+  const int tokens = (int)min((int64_t)kTokens, a.tokens - token0);
+  int hits;
   if constexpr (DOWN) {
-    expert = __builtin_amdgcn_readfirstlane(plan[0]);
-    n = __builtin_amdgcn_readfirstlane(plan[1]);
-    if (n == 0) return;
+    hits = a.hits[blockIdx.y];
   } else {
-    const int64_t first = (int64_t)blockIdx.y * kTokens;
-    const int count = (int)min((int64_t)kTokens, a.tokens - first) * a.topk;
-    const int* ids = a.ids + first * a.topk;
+    const int* ids = a.ids + token0 * a.topk;
     if (threadIdx.x < 64) bits[threadIdx.x] = 0;
     __syncthreads();
-    for (int c = threadIdx.x; c < count; c += kThreads) {
+#pragma clang loop unroll(disable)
+    for (int c = threadIdx.x; c < tokens * a.topk; c += kThreads) {
       const int id = ids[c];
-      if (id >= 0 && id < a.experts) atomicOr((unsigned long long*)&bits[id >> 6], 1ull << (id & 63));
+      const bool in = id >= 0 && id < a.experts;
+      if (in) atomicOr((unsigned long long*)&bits[id >> 6], 1ull << (id & 63));
+      chosen[c] = in ? (short)id : (short)-1;
     }
     __syncthreads();
-    expert = find_expert(bits, slot);
-    if (expert < 0) {
-      if (group == 0 && threadIdx.x == 0) plan[1] = 0;
-      return;
-    }
+    hits = __popcll(bits[lane]);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) hits += __shfl_xor(hits, o, 64);
+    hits = __builtin_amdgcn_readfirstlane(hits);
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.hits[blockIdx.y] = hits;
   }
+  // the tiles of all experts, shared out evenly
+  const unsigned all = (unsigned)hits * groups, per = all / gridDim.x, over = all - per * gridDim.x;
+  unsigned at = per * blockIdx.x + min(blockIdx.x, over);
+  const unsigned end = at + per + (blockIdx.x < over);
+
   const int k_all = DOWN ? a.inner : a.hidden, full = k_all / kChunk, chunks = (k_all + kChunk - 1) / kChunk;
   const unsigned row_bytes = (unsigned)k_all / 2, row_codes = (unsigned)k_all / 16;
-  const int64_t channel0 = (int64_t)expert * (DOWN ? a.hidden : 2 * a.inner) + (DOWN ? 16 : 8) * tile;
+  // the last chunk, if short, is the last 128 elements, and those that the one before it has are 0 in the rows
+  auto start_of = [&](int c) { return SMALL ? 0 : (c < full ? c * kChunk : k_all - kChunk); };
+  const int turn = a.each * a.split, steps = (chunks + turn - 1) / turn;       // of every wave; past the last chunk it multiplies nothing
   const unsigned channel = DOWN ? i : (i < 8 ? i : a.inner + i - 8);
-  const uint8_t* nib = a.fp4 + channel0 * row_bytes;
-  const uint8_t* code = a.code + channel0 * row_codes;
-  const unsigned w_at = channel * row_bytes + quarter * 16, c_at = channel * row_codes;
-  const int steps = (full + kU - 1) / kU;
-  const int mine = ks < steps ? (steps - ks + a.split - 1) / a.split : 0;      // steps of this wave
-  Weights w[kD][kU];
-  auto load_w = [&](Weights (&w)[kU], int m) __attribute__((always_inline)) {
-    const int g = min(m, mine - 1) * a.split + ks;
+  const unsigned w_at = channel * row_bytes + quarter * 16, c_at = channel * row_codes + quarter * 2;
+
+  while (at < end) {                          // the share's part of one expert
+    const int slot = at / (unsigned)groups, first = at - slot * groups, count = min(groups - first, (int)(end - at));
+    at += count;
+    int* plan = a.plan + ((int64_t)blockIdx.y * a.slots + slot) * kPlan;
+    const int expert = DOWN ? __builtin_amdgcn_readfirstlane(plan[0]) : find_expert(bits, slot);
+    const int64_t channel0 = (int64_t)expert * (DOWN ? a.hidden : 2 * a.inner);
+    // a step's weights of a wave: of tile `mine` of a group, its chunks of k
+    auto load_w = [&](Weights (&w)[kU], int group, int step) __attribute__((always_inline)) {
+      const int64_t c0 = channel0 + min((first + group) * together + mine, tiles - 1) * kRows;
+      const uint8_t *n0 = a.fp4 + c0 * row_bytes, *q0 = a.code + c0 * row_codes;
+      const int c = (step * a.split + ks) * a.each;
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int c = min(g * kU + u, full - 1);
-      w[u].nib = *(const v4u_a8*)(nib + (size_t)c * (kChunk / 2) + w_at);
-      w[u].code = *(const v2u_a1*)(code + (size_t)c * (kChunk / 16) + c_at);
-    }
-  };
-  const bool all_held = mine <= kD;           // then nothing is loaded in the loop
-  if (mine > 0) {
-#pragma unroll
-    for (int d = 0; d < kD - 1; ++d) load_w(w[d], d);
-    if (all_held) load_w(w[kD - 1], kD - 1);
-  }
-  if constexpr (DOWN) {
-    if (threadIdx.x < kTokens) rows[threadIdx.x] = plan[4 + threadIdx.x];
-  } else {
-    if (wave == 0) {                          // a token's first choice of the expert stands for all of them
-      const int64_t t = (int64_t)blockIdx.y * kTokens + lane;
-      int at = -1;
-      float sum = 0.0f;
-      if (t < a.tokens)
-        for (int j = 0; j < a.topk; ++j)
-          if (a.ids[t * a.topk + j] == expert) {
-            at = at < 0 ? j : at;
-            sum += a.weights[t * a.topk + j];
+      for (int u = 0; u < kU; ++u) {
+        if (u >= a.each || c + u >= chunks) break;
+        const int k = start_of(c + u);
+        if constexpr (SMALL) {
+          const int left = k_all - quarter * 32;                     // 16 elements at a time
+          w[u].nib = v4u{0, 0, 0, 0};
+          w[u].code = 0;
+          if (left >= 16) {
+            const v2u v = *(const v2u*)(n0 + w_at);
+            w[u].nib[0] = v[0], w[u].nib[1] = v[1];
+            w[u].code = q0[c_at];
           }
-      const uint64_t hit = __ballot(at >= 0);
-      const int rank = __popcll(hit & ((1ull << lane) - 1));
-      if (at >= 0) {
-        rows[rank] = (int)(t * a.topk) + at;
+          if (left >= 32) {
+            const v2u v = *(const v2u*)(n0 + w_at + 8);
+            w[u].nib[2] = v[0], w[u].nib[3] = v[1];
+            w[u].code |= (unsigned)q0[c_at + 1] << 8;
+          }
+        } else {
+          w[u].nib = *(const v4u_a8*)(n0 + k / 2 + w_at);
+          w[u].code = *(const u16_a1*)(q0 + k / 16 + c_at);
+        }
+      }
+    };
+    Weights next[kU];
+    load_w(next, 0, 0);
+    __syncthreads();                          // the rows before have been used
+    int n;
+    if constexpr (DOWN) {
+      n = __builtin_amdgcn_readfirstlane(plan[1]);
+      if (threadIdx.x < kTokens) rows[threadIdx.x] = source[threadIdx.x] = plan[4 + threadIdx.x];
+    } else if (wave < 2) {                    // a token's first choice of the expert stands for all of them
+      int pick = -1, repeats = 0;
+      if (lane < tokens)
+#pragma clang loop unroll_count(2)
+        for (int j = a.topk - 1; j >= 0; --j) {
+          const bool same = chosen[lane * a.topk + j] == expert;
+          repeats += same;
+          pick = same ? j : pick;
+        }
+      const uint64_t hit = __ballot(pick >= 0);
+      const int rank = __popcll(hit & ((1ull << lane) - 1)), number = (int)(token0 + lane) * a.topk + pick;
+      if (wave == 0) {
+        if (pick >= 0) rows[rank] = number, source[rank] = (int)token0 + lane;
+        if (lane == 0) found = __popcll(hit);
+        if (first == 0) {                     // for the second product
+          if (lane == 0) plan[0] = expert, plan[1] = __popcll(hit);
+          if (pick >= 0) plan[4 + rank] = number;
+        }
+      } else if (pick >= 0) {
+        float sum = a.weights[number];
+#pragma clang loop unroll(disable)
+        for (int j = pick + 1; repeats > 1; ++j)
+          if (chosen[lane * a.topk + j] == expert) sum += a.weights[number - pick + j], --repeats;
         share[rank] = sum;
       }
-      if (group == 0) {
-        if (lane == 0) plan[0] = expert, plan[1] = __popcll(hit);
-        if (at >= 0) plan[4 + rank] = (int)(t * a.topk) + at;
-      }
-      if (lane == 0) found = __popcll(hit);
     }
-  }
-  __syncthreads();
-  if constexpr (!DOWN) n = found;
+    __syncthreads();
+    if constexpr (!DOWN) n = __builtin_amdgcn_readfirstlane(found);
+    const float g = a.amax[expert] / a.gdiv;
 
-  for (int r0 = 0; r0 < n; r0 += 16 * CT) {
-    const int live = min(16 * CT, n - r0);
-    // chunks of the rows that LDS holds at a time
-    const int fit = kBudget / (live * P * (kChunk * 2) + live * P * 16 / kU + (EIGHT ? live * 4 : 0)) / kU * kU;
-    const int panel = min(max(fit, kU), (chunks + kU - 1) / kU * kU);
-    const unsigned stride = panel * (kChunk * 2) + 16;               // bytes of a row's piece
-    float* scales = (float*)(lds + live * P * stride);               // [chunk][row]
-    int begin = -panel;                                              // of the panel, in chunks
-    auto next_panel = [&]() __attribute__((always_inline)) {
-      begin += panel;
-      __syncthreads();
-      const int held = min(panel, chunks - begin), units = held * (kChunk / 8), total = live * units;
-      for (int at0 = threadIdx.x; at0 < total; at0 += 4 * kThreads) {
-        v4u got[4][DOWN ? P : (X == kXF32 ? 2 : 1)];
+#pragma clang loop unroll(disable)
+    for (int r0 = 0; r0 < n; r0 += 16 * MT) {
+      const int live = min(16 * MT, n - r0);
+      // chunks of the rows that LDS holds at a time
+      const int fit = (kBudget - live * P * 16) / (live * turn * (P * kChunk * 2 + 4));
+      const int panel = min(max(fit, 1), steps) * turn, panels = (chunks + panel - 1) / panel;
+      const unsigned stride = panel * (kChunk * 2) + 16;             // bytes of a row's piece; 16 rows begin in different banks
+      float* scales = (float*)(lds + live * P * stride);             // [chunk][row]
+      int begin = -1;                                                // of what is held, in chunks
+      auto hold = [&](int from) __attribute__((always_inline)) {
+        begin = from;
+        __syncthreads();
+        const int units = min(panel, chunks - begin) * (kChunk / 8), total = live * units;
+        const float reciprocal = 1.0f / (float)units;
+#pragma clang loop unroll(disable)
+        for (int at0 = threadIdx.x; at0 < total; at0 += 2 * kThreads) {
+          v4u got[2][X == kXF32 ? 2 : 1];
+          float scale[2];
+          int r[2], u[2];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int at = min(at0 + b * kThreads, total - 1), r = at / units, k = begin * kChunk + (at - r * units) * 8;
-          const int k_in = min(k, k_all - 8);                        // rows are multiples of 16
-          if constexpr (DOWN) {
-#pragma unroll
-            for (int p = 0; p < P; ++p) got[b][p] = *(const v4u*)(a.h + ((int64_t)rows[r0 + r] * P + p) * a.inner + k_in);
-          } else {
-            const int64_t from = (int64_t)(rows[r0 + r] / a.topk) * a.hidden + k_in;
-            if constexpr (X == kXBf16) got[b][0] = *(const v4u*)((const __bf16*)a.x + from);
-            if constexpr (X == kXF32) got[b][0] = *(const v4u*)((const float*)a.x + from), got[b][1] = *(const v4u*)((const float*)a.x + from + 4);
-            if constexpr (X == kXE4m3) {
+          for (int b = 0; b < 2; ++b) {
+            const int unit = min(at0 + b * kThreads, total - 16 + (int)(threadIdx.x & 15));    // 16 lanes have a chunk of a row
+            r[b] = quotient(unit, reciprocal), u[b] = unit - r[b] * units;
+            const int c = begin + u[b] / 16, k = min(start_of(c) + u[b] % 16 * 8, k_all - 8);
+            const int64_t row = source[r0 + r[b]], from = row * k_all + k;
+            if constexpr (X == kXF32) {
+              const float* p = (DOWN ? (const float*)a.h : (const float*)a.x) + from;
+              got[b][0] = *(const v4u*)p, got[b][1] = *(const v4u*)(p + 4);
+            } else if constexpr (X == kXBf16) {
+              got[b][0] = *(const v4u*)((const __bf16*)a.x + from);
+            } else {
               const v2u v = *(const v2u*)((const uint8_t*)a.x + from);
               got[b][0] = v4u{v[0], v[1], 0, 0};
+              scale[b] = a.x_scale[row * a.x_scales + (a.x_scales > 1 ? c : 0)];
             }
           }
-        }
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int at = at0 + b * kThreads, r = at / units, u = at - r * units;
-          if (at >= total) continue;
-          const bool in = begin * kChunk + u * 8 < k_all;
-          v4u out[P];
-          if constexpr (DOWN || X == kXBf16) {
+          for (int b = 0; b < 2; ++b) {
+            const int c = begin + u[b] / 16, k = start_of(c) + u[b] % 16 * 8;
+            const bool in = k >= c * kChunk && k < k_all;            // otherwise it counts in another chunk
+            h8 out[P];
+            if constexpr (X == kXE4m3) {
+              each<4>([&](auto pp) {
+                constexpr int Q = decltype(pp)::value;
+                const h2 v = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)got[b][0][Q / 2], 1.0f, Q % 2 == 1);
+                out[0][2 * Q] = v[0];
+                out[0][2 * Q + 1] = v[1];
+              });
+            } else {
+              float v[8];
 #pragma unroll
-            for (int p = 0; p < P; ++p) out[p] = got[b][p];
-          } else if constexpr (X == kXE4m3) {
-            h8 f;
-            each<4>([&](auto pp) {
-              constexpr int Q = decltype(pp)::value;
-              const h2 v = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)got[b][0][Q / 2], 1.0f, Q % 2 == 1);
-              f[2 * Q] = v[0];
-              f[2 * Q + 1] = v[1];
-            });
-            out[0] = __builtin_bit_cast(v4u, f);
-          } else {
-            __bf16 f[3][8];
+              for (int e = 0; e < 8; ++e)
+                v[e] = X == kXF32 ? __uint_as_float(got[b][e / 4][e % 4]) : __uint_as_float(e % 2 ? got[b][0][e / 2] & 0xFFFF0000u : got[b][0][e / 2] << 16);
+              unsigned most = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              __bf16 three[3];
-              split<3>(__uint_as_float(got[b][e / 4][e % 4]), three);
-              f[0][e] = three[0], f[1][e] = three[1], f[2][e] = three[2];
+              for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+              const int top = min(max((int)(row_max(in ? most : 0) >> 23), 1), 254);   // beside an infinity, what is finite stays so
+              scale[b] = __builtin_ldexpf(1.0f, top - 141);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float y = __builtin_ldexpf(v[e], 141 - top);
+                out[0][e] = (_Float16)y;
+                if constexpr (P == 2) out[1][e] = y == (float)out[0][e] ? (_Float16)0.0f : (_Float16)(y - (float)out[0][e]);
+              }
             }
-            __builtin_memcpy(out, f, sizeof f);
+            if (at0 + b * kThreads >= total) continue;
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+              *(v4u*)(lds + (unsigned)(p * live + r[b]) * stride + u[b] * 16) = in ? __builtin_bit_cast(v4u, out[p]) : v4u{0, 0, 0, 0};
+            if (u[b] % 16 == 0) scales[u[b] / 16 * live + r[b]] = scale[b];
           }
-#pragma unroll
-          for (int p = 0; p < P; ++p) *(v4u*)(lds + (unsigned)(p * live + r) * stride + u * 16) = in ? out[p] : v4u{0, 0, 0, 0};
         }
-      }
-      if constexpr (EIGHT)
-        for (int at = threadIdx.x; at < held * live; at += kThreads) {
-          const int c = at / live, r = at - c * live;
-          scales[at] = a.x_scale[(int64_t)(rows[r0 + r] / a.topk) * a.x_scales + (a.x_scales > 1 ? begin + c : 0)];
-        }
-      __syncthreads();
-    };
-    v4f acc[CT];
-    unsigned x_at[CT];
-    int row_of[CT];
+        __syncthreads();
+      };
+      v4f acc[MT];
 #pragma unroll
-    for (int c = 0; c < CT; ++c) {
-      acc[c] = v4f{0, 0, 0, 0};
-      row_of[c] = min(16 * c + i, live - 1);
-      x_at[c] = row_of[c] * stride + quarter * 16;
-    }
-    // chunk c of k (of the panel's) with these weights
-    auto multiply = [&](const Weights& w, int c) __attribute__((always_inline)) {
-      v4f part[CT];
+      for (int t = 0; t < MT; ++t) acc[t] = v4f{0, 0, 0, 0};
+      auto multiply = [&](const Weights& w, int c) __attribute__((always_inline)) {
+        const h2 scale = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w.code, 1.0f, false);
+        h8 f[4];
+        each<4>([&](auto st) __attribute__((always_inline)) {
+          constexpr int S = decltype(st)::value;
+          const h2 s = {scale[S / 2], scale[S / 2]};
+          each<4>([&](auto pp) {
+            constexpr int Q = decltype(pp)::value;
+            const h2 v = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w.nib[S], 1.0f, Q) * s;
+            f[S][2 * Q] = v[0];
+            f[S][2 * Q + 1] = v[1];
+          });
+        });
 #pragma unroll
-      for (int t = 0; t < CT; ++t) part[t] = v4f{0, 0, 0, 0};
-      auto& sum = *(EIGHT ? &part : &acc);
-      const v4u words = exchange<kXBf16>(w.nib);
-      const v2u codes = lane_codes<kXBf16>(w.code, quarter);
-      const char* from = lds + (unsigned)(c - begin) * (kChunk * 2);
-      each<4>([&](auto st) __attribute__((always_inline)) {
-        constexpr int S = decltype(st)::value;
-        const auto fw = weights<WX, 2 * (S % 2)>(words[S], codes[S / 2]);
-#pragma unroll
-        for (int t = 0; t < CT; ++t)
+        for (int t = 0; t < MT; ++t) {
+          if (MT > 1 && t > 0 && 16 * t >= live) break;
+          const int row = min(16 * t + i, live - 1);
+          const char* from = lds + (unsigned)(c - begin) * (kChunk * 2) + (row * stride + quarter * 64);
+          v4f sum = {0, 0, 0, 0};
 #pragma unroll
           for (int p = 0; p < P; ++p)
-            sum[t] = mfma(fw, __builtin_bit_cast(frag, *(const v4u*)(from + x_at[t] + p * live * stride + S * 64)), sum[t]);
-      });
-      if constexpr (EIGHT) {
 #pragma unroll
-        for (int t = 0; t < CT; ++t) acc[t] += scales[(c - begin) * live + row_of[t]] * part[t];
-      }
-    };
-    auto one = [&](int m, const Weights (&w)[kU]) __attribute__((always_inline)) {
-      const int c = (m * a.split + ks) * kU;
-      while (c >= begin + panel) next_panel();
-#pragma unroll
-      for (int u = 0; u < kU; ++u)
-        if (c + u < full) multiply(w[u], c + u);
-    };
-    next_panel();
-    if (r0 > 0 && mine > 0) {                  // the weights once more
-#pragma unroll
-      for (int d = 0; d < kD - 1; ++d) load_w(w[d], d);
-      if (all_held) load_w(w[kD - 1], kD - 1);
-    }
-    if (all_held) {
-      each<kD>([&](auto dd) __attribute__((always_inline)) {
-        constexpr int d = decltype(dd)::value;
-        if (d < mine) one(d, w[d]);
-      });
-    } else {
-      for (int m = 0; m < mine; m += kD)
-        each<kD>([&](auto dd) __attribute__((always_inline)) {
-          constexpr int d = decltype(dd)::value;
-          if (m + d < mine) {
-            load_w(w[(d + kD - 1) % kD], m + d + kD - 1);
-            one(m + d, w[d]);
-          }
-        });
-    }
-    while (begin + panel < chunks) next_panel();
-    if (full < chunks && ks == 0) {            // the last, short chunk: 16 elements at a time
-      const int left = k_all - full * kChunk, own_k = left - quarter * 32;
-      const uint8_t* pn = nib + (size_t)full * (kChunk / 2) + w_at;
-      const uint8_t* pq = code + (size_t)full * (kChunk / 16) + c_at;
-      Weights t{};
-      if (own_k >= 16) {
-        const v2u v = *(const v2u*)pn;
-        t.nib[0] = v[0], t.nib[1] = v[1];
-      }
-      if (own_k >= 32) {
-        const v2u v = *(const v2u*)(pn + 8);
-        t.nib[2] = v[0], t.nib[3] = v[1];
-      }
-#pragma unroll
-      for (int b = 0; b < 7; ++b)
-        if (16 * b < left) t.code[b / 4] |= (unsigned)pq[b] << (8 * (b % 4));
-      multiply(t, full);
-    }
-    if (a.split > 1) {                         // the shares of k, in their order
-      __syncthreads();
-      float* red = (float*)lds;
-#pragma unroll
-      for (int t = 0; t < CT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) red[((wave * CT + t) * 4 + r) * 64 + lane] = acc[t][r];
-      __syncthreads();
-      if (ks == 0)
-        for (int s = 1; s < a.split; ++s)
-#pragma unroll
-          for (int t = 0; t < CT; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[t][r] += red[(((wave + s) * CT + t) * 4 + r) * 64 + lane];
-    }
-    const float g = a.amax[expert] / a.gdiv;
-#pragma unroll
-    for (int t = 0; t < CT; ++t) {
-      const int row = 16 * t + i;
-      if constexpr (DOWN) {
-        if (own && row < live) *(v4f*)(a.part + (int64_t)rows[r0 + row] * a.hidden + 16 * tile + 4 * quarter) = acc[t] * g;
-      } else {                                 // a lane of the lower half has gate rows, 32 lanes on are their up rows
-        __bf16 out[HP][4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float gate = acc[t][r] * g, up = __shfl_xor(gate, 32, 64);
-          __bf16 pieces[HP];
-          split<HP>(gate / (1.0f + expf(-gate)) * up * share[min(r0 + row, kTokens - 1)], pieces);
-#pragma unroll
-          for (int p = 0; p < HP; ++p) out[p][r] = pieces[p];
+            for (int s = 0; s < 4; ++s) sum = mfma(f[s], __builtin_bit_cast(h8, *(const v4u*)(from + p * live * stride + s * 16)), sum);
+          acc[t] += scales[(c - begin) * live + row] * sum;
         }
-        if (own && row < live && quarter < 2) {
+      };
+      if (r0 > 0) load_w(next, 0, 0);         // once more
+      int group = 0, step = 0;
+#pragma clang loop unroll(disable)
+      for (int left = count * steps; left > 0; --left) {
+        const int now = step, here = panels == 1 ? 0 : now * turn / panel * panel;
+        if (here != begin) hold(here);        // the same step of all waves
+        Weights w[kU];
 #pragma unroll
-          for (int p = 0; p < HP; ++p) {
-            v2u v;
-            __builtin_memcpy(&v, out[p], sizeof v);
-            *(v2u*)(a.h + ((int64_t)rows[r0 + row] * HP + p) * a.inner + 8 * tile + 4 * quarter) = v;
+        for (int u = 0; u < kU; ++u) w[u] = next[u];
+        const bool last = ++step == steps;
+        if (last) step = 0;
+        if (left > 1) load_w(next, group + last, step);
+        const int c = (now * a.split + ks) * a.each;
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          if (u >= a.each || c + u >= chunks) break;
+          multiply(w[u], c + u);
+        }
+        if (!last) continue;
+        const int tile = (first + group) * together + mine;
+        const bool own = tile < tiles && ks == 0;
+        ++group;
+#pragma clang loop unroll(disable)
+        for (int t = 0; 16 * t < live; ++t) {
+          v4f v = acc[0];
+#pragma unroll
+          for (int m = 0; m + 1 < MT; ++m) acc[m] = acc[m + 1];
+          acc[MT - 1] = v4f{0, 0, 0, 0};
+          if (a.split > 1) {                  // the shares of k, in their order
+            *(v4f*)(red + (wave * 64 + lane) * 4) = v;
+            __syncthreads();
+            if (ks == 0)
+#pragma clang loop unroll(disable)
+              for (int s = 1; s < a.split; ++s) v += *(const v4f*)(red + ((wave + s) * 64 + lane) * 4);
+            __syncthreads();
+          }
+          const int row = 16 * t + i;
+          v *= g;
+          if constexpr (DOWN) {
+            if (own && row < live) *(v4f*)(a.part + (int64_t)rows[r0 + row] * a.hidden + 16 * tile + 4 * quarter) = v;
+          } else {                            // a lane of the lower half has gate rows, 32 lanes on are their up rows
+            const float weight = share[min(r0 + row, kTokens - 1)];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float up = __shfl_xor(v[r], 32, 64);
+              v[r] = silu(v[r]) * up * weight;
+            }
+            if (own && row < live && quarter < 2) *(v4f*)(a.h + (int64_t)rows[r0 + row] * a.inner + 8 * tile + 4 * quarter) = v;
           }
         }
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[t] = v4f{0, 0, 0, 0};
       }
     }
   }
@@ -380,55 +406,58 @@ __global__ __launch_bounds__(256) void k_experts_sum(const Args a) {
 }
 
 struct Layout {
-  int64_t slots, chunks, plan, h, part, all;  // bytes; chunks of tokens
+  int64_t slots, chunks, hits, plan, h, part, all;                   // chunks of tokens; bytes
 };
 Layout layout(const MoeView& v) {
   Layout l{};
   auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
   l.slots = std::min(v.experts, std::min<int64_t>(v.tokens, kTokens) * v.topk);
   l.chunks = (v.tokens + kTokens - 1) / kTokens;
+  l.hits = up(l.chunks * 4);
   l.plan = up(l.slots * l.chunks * kPlan * 4);
-  l.h = up(v.tokens * v.topk * v.inner * (v.x_type == kXF32 ? 3 : 2) * 2);
+  l.h = up(v.tokens * v.topk * v.inner * 4);
   l.part = v.tokens * v.topk * v.hidden * 4;
-  l.all = l.plan + l.h + l.part;
+  l.all = l.hits + l.plan + l.h + l.part;
   return l;
 }
 
-template <int X, int CT>
+template <int X, int P, bool DOWN, int MT>
 hipError_t go(const MoeView& v, Args a, const Layout& l, hipStream_t stream) {
-  constexpr int P = Frag<X>::pieces, HP = X == kXF32 ? 3 : 2;
-  // waves that share k, so that some 2000 waves have work
-  auto split = [&](int64_t tiles, int64_t k) {
-    int s = 1;
-    while (s < kWaves && l.slots * tiles * s < 8 * kComputeUnits && s * kChunk * kU < k) s *= 2;
-    return s;
-  };
-  auto grid = [&](int64_t tiles) { return (tiles + kWaves / a.split - 1) / (kWaves / a.split) * l.slots; };
-  constexpr size_t kLds = kBudget + 1024;
+  const int64_t k = DOWN ? v.inner : v.hidden, tiles = DOWN ? v.hidden / 16 : v.inner / 8, chunks = (k + kChunk - 1) / kChunk;
+  // waves that share k, so that some 4000 waves have work; their chunks of a step have to fit LDS for all rows
+  const int64_t rows = std::min<int64_t>(16 * MT, v.tokens);
+  auto fits = [&](int64_t turn) { return rows * (P * (turn * kChunk * 2 + 16) + 4 * turn) <= kBudget; };
+  a.split = 1;
+  while (a.split < kWaves && 2 * a.split <= chunks && l.slots * tiles * a.split < kResident * kWaves && fits(2 * a.split)) a.split *= 2;
+  const int64_t steps = (chunks + kU * a.split - 1) / (kU * a.split);
+  a.each = (int)((chunks + steps * a.split - 1) / (steps * a.split));
+  while (!fits(a.each * a.split)) --a.each;
+  const int64_t groups = (tiles + kWaves / a.split - 1) / (kWaves / a.split);
+  if (l.slots * groups >= int64_t(1) << 31) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)std::min<int64_t>(kResident, l.slots * groups), (unsigned)l.chunks);
+  const size_t lds = kBudget + kWaves * 1024 + (DOWN ? 0 : kTokens * v.topk * 2);
+  return k < kChunk ? launch_kernel(k_experts<X, P, DOWN, MT, true>, grid, dim3(kThreads), lds, stream, a)
+                    : launch_kernel(k_experts<X, P, DOWN, MT, false>, grid, dim3(kThreads), lds, stream, a);
+}
+
+template <bool MANY>
+hipError_t go_all(const MoeView& v, Args a, const Layout& l, hipStream_t stream) {
+  constexpr int kOne = MANY ? 4 : 1, kTwo = MANY ? 2 : 1;            // 16-row tiles for which a step's chunks fit LDS in one or two pieces
+  const int64_t blocks = (v.hidden / 4 + 255) / 256 * v.tokens;
+  if (blocks >= (int64_t(1) << 24)) return hipErrorInvalidConfiguration;
   a.code = v.gate_up_code;
   a.fp4 = v.gate_up_fp4;
   a.amax = v.gate_up_amax;
-  a.split = split(v.inner / 8, v.hidden);
-  int64_t n = grid(v.inner / 8);
-  if (n >= (int64_t(1) << 32) / kThreads) return hipErrorInvalidConfiguration;
-  hipError_t e = launch_kernel(k_experts<X, false, P, HP, CT>, dim3((unsigned)n, (unsigned)l.chunks), dim3(kThreads), kLds, stream, a);
+  hipError_t e = v.x_type == kXBf16 ? go<kXBf16, 1, false, kOne>(v, a, l, stream)
+                 : v.x_type == kXF32 ? go<kXF32, 2, false, kTwo>(v, a, l, stream) : go<kXE4m3, 1, false, kOne>(v, a, l, stream);
   if (e != hipSuccess) return e;
   a.code = v.down_code;
   a.fp4 = v.down_fp4;
   a.amax = v.down_amax;
-  a.split = split(v.hidden / 16, v.inner);
-  n = grid(v.hidden / 16);
-  if (n >= (int64_t(1) << 32) / kThreads) return hipErrorInvalidConfiguration;
-  e = launch_kernel(k_experts<X == kXF32 ? kXF32 : kXBf16, true, HP, HP, CT>, dim3((unsigned)n, (unsigned)l.chunks), dim3(kThreads), kLds, stream, a);
+  e = v.x_type == kXF32 ? go<kXF32, 2, true, kTwo>(v, a, l, stream) : go<kXF32, 1, true, kOne>(v, a, l, stream);
   if (e != hipSuccess) return e;
-  const int64_t blocks = (v.hidden / 4 + 255) / 256 * v.tokens;
-  if (blocks >= (int64_t(1) << 24)) return hipErrorInvalidConfiguration;
-  return launch_kernel(k_experts_sum<X != kXF32>, dim3((unsigned)blocks), dim3(256), 0, stream, a);
-}
-
-template <int X>
-hipError_t go_x(const MoeView& v, const Args& a, const Layout& l, hipStream_t stream) {
-  return v.tokens <= 16 || v.tokens * v.topk <= 4 * v.experts ? go<X, 1>(v, a, l, stream) : go<X, 2>(v, a, l, stream);
+  return v.x_type == kXF32 ? launch_kernel(k_experts_sum<false>, dim3((unsigned)blocks), dim3(256), 0, stream, a)
+                           : launch_kernel(k_experts_sum<true>, dim3((unsigned)blocks), dim3(256), 0, stream, a);
 }
 
 }  // namespace
@@ -442,9 +471,10 @@ hipError_t launch_moe(const MoeView& v, void* work, hipStream_t stream) {
   a.x_scale = v.x_scale;
   a.ids = v.ids;
   a.weights = v.weights;
-  a.plan = (int*)work;
-  a.h = (__bf16*)((char*)work + l.plan);
-  a.part = (float*)((char*)work + l.plan + l.h);
+  a.hits = (int*)work;
+  a.plan = (int*)((char*)work + l.hits);
+  a.h = (float*)((char*)work + l.hits + l.plan);
+  a.part = (float*)((char*)work + l.hits + l.plan + l.h);
   a.y = v.y;
   a.tokens = v.tokens;
   a.hidden = (int)v.hidden;
@@ -454,8 +484,7 @@ hipError_t launch_moe(const MoeView& v, void* work, hipStream_t stream) {
   a.x_scales = (int)v.x_scales;
   a.slots = (int)l.slots;
   a.gdiv = v.gdiv;
-  if (v.x_type == kXBf16) return go_x<kXBf16>(v, a, l, stream);
-  return v.x_type == kXF32 ? go_x<kXF32>(v, a, l, stream) : go_x<kXE4m3>(v, a, l, stream);
+  return v.tokens <= 16 ? go_all<false>(v, a, l, stream) : go_all<true>(v, a, l, stream);
 }
 
 }  // namespace lh

@@ -316,13 +316,14 @@ def layer_rows(rows, cin, x, group, seed):
 
 def check_moe(xd, scale, xv, x, group, ids, w, gate_up, down, **kw):
     """Products are exact and sums fp32: a sum of n terms is off by at most (n + 8) roundings of its terms' magnitudes (every element of
-    fp32 rows is three terms), which the two products pass on; between them exp, the division, three products and the pieces of h."""
+    fp32 rows is three terms), which the two products pass on; between them exp, the division and three products.  h is one fp16 number
+    with a factor (2^-12 of itself: y's own rounding is 2^-8), for fp32 rows two (2^-24, and 2^-40 of the largest of 128, as are those rows)."""
     y = lh.lh_moe(xd, torch.from_numpy(ids).to(DEV), torch.from_numpy(w).to(DEV), on_gpu(gate_up), on_gpu(down), x_scale=scale, x_group=group, **kw)
     want, terms = serve.moe(xv, ids, w.astype(np.float64), gate_up, down, kw.get("norm", 448.0))
     hidden, inner = xv.shape[1], down[0].shape[2] * 16
     pieces = 3 if x == "f32" else 1
-    rel = (pieces * hidden + 8) * U + (3 * inner + 8) * U + 32 * U + (2.0 ** -24 if x == "f32" else 2.0 ** -17) + ids.shape[1] * U
-    bound = rel * terms + 2.0 ** -120
+    rel = (pieces * hidden + 8) * U + (3 * inner + 8) * U + 32 * U + (2.0 ** -23 if x == "f32" else 2.0 ** -12) + ids.shape[1] * U
+    bound = rel * terms + 2.0 ** -38 * terms.max(1, keepdims=True) + 2.0 ** -120
     bound += HALF["f32" if x == "f32" else "bf16"] * (np.abs(want) + bound)
     got, none = y.double().cpu().numpy(), np.isnan(want)        # a NaN in a row (8 bits of what is over 464) is one in its outputs
     np.testing.assert_array_equal(np.isnan(got), none)
