@@ -27,7 +27,7 @@ namespace {
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kU = 4;                        // chunks of k a wave takes at a time, at most
-constexpr int kBudget = 66 * 1024;           // LDS of the rows, so that two workgroups fit a compute unit
+constexpr int kBudget = 64 * 1024;           // LDS of the rows, so that two workgroups fit a compute unit
 constexpr int kResident = 2 * 256;           // workgroups
 
 struct Args {
@@ -45,16 +45,16 @@ struct Args {
   void* y;
   int64_t tokens;
   int hidden, inner, experts, topk, x_scales, slots;
-  int split, each;                           // waves that share k; chunks of a step
+  int split, each, rows;                     // waves that share k; chunks of a step; rows taken at a time
   float gdiv;
 };
 
-typedef uint16_t u16_a1 __attribute__((aligned(1)));
-
-// 32 nibbles of one channel and the scales of their two blocks.
+// A step's weights of a lane: 32 nibbles of each chunk, and the 8 scales of its channel for the chunk that is its quarter of the wave.
+// (Scales loaded chunk by chunk, 8 bytes a channel, made the reading of the weights take 69 us where this takes 43: 135 experts
+// of 1280x2560, 249 MB, loads alone.)
 struct Weights {
-  v4u nib;
-  unsigned code;
+  v4u nib[kU];
+  v2u code;
 };
 
 __device__ inline unsigned row_max(unsigned v) {     // over 16 neighbouring lanes
@@ -91,6 +91,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
   __shared__ float share[kTokens];
   __shared__ int found;
   extern __shared__ __attribute__((aligned(16))) char lds[];
+  __shared__ __attribute__((aligned(16))) uint8_t codes[kWaves][16][8 * kU];
   float* red = (float*)(lds + kBudget);
   short* chosen = (short*)(lds + kBudget + kWaves * 1024);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -131,7 +132,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
   auto start_of = [&](int c) { return SMALL ? 0 : (c < full ? c * kChunk : k_all - kChunk); };
   const int turn = a.each * a.split, steps = (chunks + turn - 1) / turn;       // of every wave; past the last chunk it multiplies nothing
   const unsigned channel = DOWN ? i : (i < 8 ? i : a.inner + i - 8);
-  const unsigned w_at = channel * row_bytes + quarter * 16, c_at = channel * row_codes + quarter * 2;
+  const unsigned w_at = channel * row_bytes + quarter * 16, c_at = channel * row_codes;
 
   while (at < end) {                          // the share's part of one expert
     const int slot = at / (unsigned)groups, first = at - slot * groups, count = min(groups - first, (int)(end - at));
@@ -140,35 +141,35 @@ __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
     const int expert = DOWN ? __builtin_amdgcn_readfirstlane(plan[0]) : find_expert(bits, slot);
     const int64_t channel0 = (int64_t)expert * (DOWN ? a.hidden : 2 * a.inner);
     // a step's weights of a wave: of tile `mine` of a group, its chunks of k
-    auto load_w = [&](Weights (&w)[kU], int group, int step) __attribute__((always_inline)) {
+    auto load_w = [&](Weights& w, int group, int step) __attribute__((always_inline)) {
       const int64_t c0 = channel0 + min((first + group) * together + mine, tiles - 1) * kRows;
       const uint8_t *n0 = a.fp4 + c0 * row_bytes, *q0 = a.code + c0 * row_codes;
       const int c = (step * a.split + ks) * a.each;
+      if constexpr (SMALL) {                  // 16 elements at a time
+        const int left = k_all - quarter * 32;
+        w.nib[0] = v4u{0, 0, 0, 0};
+        w.code = v2u{0, 0};
+        if (left >= 16) {
+          const v2u v = *(const v2u*)(n0 + w_at);
+          w.nib[0][0] = v[0], w.nib[0][1] = v[1];
+        }
+        if (left >= 32) {
+          const v2u v = *(const v2u*)(n0 + w_at + 8);
+          w.nib[0][2] = v[0], w.nib[0][3] = v[1];
+        }
+#pragma unroll
+        for (int b = 0; b < 7; ++b)
+          if (16 * b < k_all) w.code[b / 4] |= (unsigned)q0[c_at + b] << (8 * (b % 4));
+        return;
+      }
+      if (quarter < a.each && c + quarter < chunks) w.code = *(const v2u_a1*)(q0 + (start_of(c + quarter) / 16 + c_at));
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         if (u >= a.each || c + u >= chunks) break;
-        const int k = start_of(c + u);
-        if constexpr (SMALL) {
-          const int left = k_all - quarter * 32;                     // 16 elements at a time
-          w[u].nib = v4u{0, 0, 0, 0};
-          w[u].code = 0;
-          if (left >= 16) {
-            const v2u v = *(const v2u*)(n0 + w_at);
-            w[u].nib[0] = v[0], w[u].nib[1] = v[1];
-            w[u].code = q0[c_at];
-          }
-          if (left >= 32) {
-            const v2u v = *(const v2u*)(n0 + w_at + 8);
-            w[u].nib[2] = v[0], w[u].nib[3] = v[1];
-            w[u].code |= (unsigned)q0[c_at + 1] << 8;
-          }
-        } else {
-          w[u].nib = *(const v4u_a8*)(n0 + k / 2 + w_at);
-          w[u].code = *(const u16_a1*)(q0 + k / 16 + c_at);
-        }
+        w.nib[u] = *(const v4u_a8*)(n0 + start_of(c + u) / 2 + w_at);
       }
     };
-    Weights next[kU];
+    Weights next;
     load_w(next, 0, 0);
     __syncthreads();                          // the rows before have been used
     int n;
@@ -206,8 +207,8 @@ __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
     const float g = a.amax[expert] / a.gdiv;
 
 #pragma clang loop unroll(disable)
-    for (int r0 = 0; r0 < n; r0 += 16 * MT) {
-      const int live = min(16 * MT, n - r0);
+    for (int r0 = 0; r0 < n; r0 += a.rows) {
+      const int live = min(a.rows, n - r0);
       // chunks of the rows that LDS holds at a time
       const int fit = (kBudget - live * P * 16) / (live * turn * (P * kChunk * 2 + 4));
       const int panel = min(max(fit, 1), steps) * turn, panels = (chunks + panel - 1) / panel;
@@ -282,15 +283,15 @@ __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
       v4f acc[MT];
 #pragma unroll
       for (int t = 0; t < MT; ++t) acc[t] = v4f{0, 0, 0, 0};
-      auto multiply = [&](const Weights& w, int c) __attribute__((always_inline)) {
-        const h2 scale = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w.code, 1.0f, false);
+      auto multiply = [&](const v4u& nib, int u, int c) __attribute__((always_inline)) {
+        const h2 scale = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)*(const uint16_t*)&codes[wave][i][8 * u + 2 * quarter], 1.0f, false);
         h8 f[4];
         each<4>([&](auto st) __attribute__((always_inline)) {
           constexpr int S = decltype(st)::value;
           const h2 s = {scale[S / 2], scale[S / 2]};
           each<4>([&](auto pp) {
             constexpr int Q = decltype(pp)::value;
-            const h2 v = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w.nib[S], 1.0f, Q) * s;
+            const h2 v = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(nib[S], 1.0f, Q) * s;
             f[S][2 * Q] = v[0];
             f[S][2 * Q + 1] = v[1];
           });
@@ -314,9 +315,13 @@ __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
       for (int left = count * steps; left > 0; --left) {
         const int now = step, here = panels == 1 ? 0 : now * turn / panel * panel;
         if (here != begin) hold(here);        // the same step of all waves
-        Weights w[kU];
+        *(v2u*)&codes[wave][i][8 * quarter] = next.code;
+        v4u nib[kU];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) w[u] = next[u];
+        for (int u = 0; u < kU; ++u) {
+          nib[u] = next.nib[u];
+          asm volatile("" : "+v"(nib[u]));    // waits for them here, before the next loads are issued, not behind those
+        }
         const bool last = ++step == steps;
         if (last) step = 0;
         if (left > 1) load_w(next, group + last, step);
@@ -324,7 +329,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           if (u >= a.each || c + u >= chunks) break;
-          multiply(w[u], c + u);
+          multiply(nib[u], u, c + u);
         }
         if (!last) continue;
         const int tile = (first + group) * together + mine;
@@ -424,14 +429,16 @@ Layout layout(const MoeView& v) {
 template <int X, int P, bool DOWN, int MT>
 hipError_t go(const MoeView& v, Args a, const Layout& l, hipStream_t stream) {
   const int64_t k = DOWN ? v.inner : v.hidden, tiles = DOWN ? v.hidden / 16 : v.inner / 8, chunks = (k + kChunk - 1) / kChunk;
-  // waves that share k, so that some 4000 waves have work; their chunks of a step have to fit LDS for all rows
+  // waves that share k, so that some 4000 waves have work
+  auto fits = [&](int64_t turn) { return kBudget / (P * (turn * kChunk * 2 + 16) + 4 * turn); };       // rows whose chunks of a step LDS holds
   const int64_t rows = std::min<int64_t>(16 * MT, v.tokens);
-  auto fits = [&](int64_t turn) { return rows * (P * (turn * kChunk * 2 + 16) + 4 * turn) <= kBudget; };
   a.split = 1;
-  while (a.split < kWaves && 2 * a.split <= chunks && l.slots * tiles * a.split < kResident * kWaves && fits(2 * a.split)) a.split *= 2;
+  while (a.split < kWaves && 2 * a.split <= chunks && l.slots * tiles * a.split < kResident * kWaves && fits(2 * a.split) >= std::min<int64_t>(rows, 16)) a.split *= 2;
   const int64_t steps = (chunks + kU * a.split - 1) / (kU * a.split);
   a.each = (int)((chunks + steps * a.split - 1) / (steps * a.split));
-  while (!fits(a.each * a.split)) --a.each;
+  while (fits(a.each * a.split) < std::min<int64_t>(rows, 16)) --a.each;
+  a.rows = (int)std::min<int64_t>(16 * MT, fits(a.each * a.split) / 16 * 16);
+  if (a.rows < 16) a.rows = (int)rows;       // fewer than 16 tokens
   const int64_t groups = (tiles + kWaves / a.split - 1) / (kWaves / a.split);
   if (l.slots * groups >= int64_t(1) << 31) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)std::min<int64_t>(kResident, l.slots * groups), (unsigned)l.chunks);
