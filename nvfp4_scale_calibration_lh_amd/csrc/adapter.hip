@@ -21,6 +21,7 @@ constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kMaxParts = 8;                 // workgroups that share k
 constexpr int kRanks = 64;                   // of one workgroup of the first kernel
+constexpr int kGroups = 768;                 // workgroups of the second kernel: three a compute unit are resident
 constexpr int kCopy = 2048;                  // channels that a workgroup copies of a row without adapter
 
 struct Args {
@@ -32,6 +33,7 @@ struct Args {
   const int* ranks;
   const void* base;
   void* y;
+  int* hits;                                 // adapters that each 64 rows ask for
   int* plan;
   float* u;
   int64_t rows;
@@ -103,58 +105,67 @@ __global__ __launch_bounds__(kThreads) void k_adapter_in(const Args a) {
   __syncthreads();
   if (wave == 0 && wanted >= 0 && wanted < a.adapters) atomicOr((unsigned long long*)&bits[wanted >> 6], 1ull << (wanted & 63));
   __syncthreads();
-  const int adapter = find_expert(bits, slot);
-  if (adapter < 0) {
-    if (leads && threadIdx.x == 0) plan[1] = 0;
-    return;
+  if (leads && slot == 0 && wave == 0) {
+    int hits = __popcll(bits[lane]);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) hits += __shfl_xor(hits, o, 64);
+    if (lane == 0) a.hits[blockIdx.y] = hits;
   }
+  const int adapter = find_expert(bits, slot);
+  if (adapter < 0) return;
+  const int ranks = rank_of(a, adapter);
+  const int chunks = (a.cin + kChunk - 1) / kChunk;
+  constexpr int kUnits = WF32 ? 8 : 4, kEach = WF32 ? 4 : 8;         // loads of a chunk, elements of one
+  v4u w[RT][kUnits];
+  auto load_w = [&](int c) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < RT; ++j) {           // rows past the adapter's rank repeat its last: the second kernel leaves them out
+      const int64_t at = ((int64_t)adapter * a.rank + min(first + 16 * j + i, max(ranks - 1, 0))) * a.cin;
+#pragma unroll
+      for (int s = 0; s < kUnits; ++s) {
+        const int k = min(c * kChunk + (4 * s + quarter) * kEach, a.cin - kEach);
+        w[j][s] = WF32 ? *(const v4u*)((const float*)a.a + at + k) : *(const v4u*)((const __bf16*)a.a + at + k);
+      }
+    }
+  };
+  const int own = part * kWaves + wave;
+  if (own < chunks) load_w(own);
   if (wave == 0) {
     const uint64_t hit = __ballot(wanted == adapter);
     const int at = __popcll(hit & ((1ull << lane) - 1));
     if (wanted == adapter) rows[at] = (int)t;
     if (leads) {
-      if (lane == 0) plan[0] = adapter, plan[1] = __popcll(hit);
+      if (lane == 0) plan[0] = adapter, plan[1] = __popcll(hit), plan[2] = ranks;
       if (wanted == adapter) plan[4 + at] = (int)t;
     }
     if (lane == 0) found = __popcll(hit);
   }
-  const int ranks = rank_of(a, adapter);
   __syncthreads();
   const int n = found;
   if (first >= ranks) return;
   const int tiles = min(RT, (ranks - first + 15) / 16);
-  int64_t w_at[RT];
-#pragma unroll
-  for (int j = 0; j < RT; ++j)               // rows past the adapter's rank repeat its last: the second kernel leaves them out
-    w_at[j] = ((int64_t)adapter * a.rank + min(first + 16 * j + i, ranks - 1)) * a.cin;
-  const int chunks = (a.cin + kChunk - 1) / kChunk;
   for (int r0 = 0; r0 < n; r0 += 16) {
     const int row = rows[min(r0 + i, n - 1)];
     const int64_t x_at = (int64_t)row * a.cin;
     v4f acc[RT];
 #pragma unroll
     for (int j = 0; j < RT; ++j) acc[j] = v4f{0, 0, 0, 0};
-    for (int c = part * kWaves + wave; c < chunks; c += a.parts * kWaves) {
+    for (int c = own; c < chunks; c += a.parts * kWaves) {
+      if (c > own || r0 > 0) load_w(c);
       float scale = 1.0f;
       if constexpr (X == kXE4m3) scale = a.x_scale[(int64_t)row * a.x_scales + (a.x_scales > 1 ? c : 0)];
       if constexpr (WF32) {
         v4f x[8];
 #pragma unroll
-        for (int s = 0; s < 8; ++s) {
-          const int k = c * kChunk + 16 * s + 4 * quarter;
-          x[s] = four<X>(a.x, x_at + min(k, a.cin - 4), scale);
-        }
+        for (int s = 0; s < 8; ++s) x[s] = four<X>(a.x, x_at + min(c * kChunk + 16 * s + 4 * quarter, a.cin - 4), scale);
 #pragma unroll
         for (int j = 0; j < RT; ++j) {
           if (j >= tiles) break;
-          v4f w[8];
-#pragma unroll
-          for (int s = 0; s < 8; ++s) w[s] = *(const v4f*)((const float*)a.a + w_at[j] + min(c * kChunk + 16 * s + 4 * quarter, a.cin - 4));
 #pragma unroll
           for (int s = 0; s < 8; ++s) {
-            if (c * kChunk + 16 * s >= a.cin) break;               // rows are multiples of 16
+            if (c * kChunk + 16 * s >= a.cin) break;                 // rows are multiples of 16
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[j] = mfma_f32(w[s][e], x[s][e], acc[j]);
+            for (int e = 0; e < 4; ++e) acc[j] = mfma_f32(__uint_as_float(w[j][s][e]), x[s][e], acc[j]);
           }
         }
       } else {
@@ -170,13 +181,10 @@ __global__ __launch_bounds__(kThreads) void k_adapter_in(const Args a) {
 #pragma unroll
         for (int j = 0; j < RT; ++j) {
           if (j >= tiles) break;
-          v4u w[4];
-#pragma unroll
-          for (int s = 0; s < 4; ++s) w[s] = *(const v4u*)((const __bf16*)a.a + w_at[j] + min(c * kChunk + 32 * s + 8 * quarter, a.cin - 8));
           v4f sum = SCALED ? v4f{0, 0, 0, 0} : acc[j];
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
-            const v4u held = c * kChunk + 32 * s + 8 * quarter < a.cin ? w[s] : v4u{0, 0, 0, 0};
+            const v4u held = c * kChunk + 32 * s + 8 * quarter < a.cin ? w[j][s] : v4u{0, 0, 0, 0};
 #pragma unroll
             for (int p = 0; p < P; ++p) sum = mfma(__builtin_bit_cast(b8, held), x[s][p], sum);
           }
@@ -197,123 +205,171 @@ __global__ __launch_bounds__(kThreads) void k_adapter_in(const Args a) {
   }
 }
 
-// RK: steps of 32 ranks; NT: 16-channel tiles of a wave; P: bf16 pieces of u.
+// RK: steps of 32 ranks; NT: 16-channel tiles a wave takes at a time; P: bf16 pieces of u.  A workgroup makes its adapter's u once and takes
+// several steps of channels, the weights and the base of the next on their way.
 template <bool YF32, bool WF32, int RK, int NT>
 __global__ __launch_bounds__(kThreads) void k_adapter_out(const Args a) {
   constexpr int P = WF32 ? 1 : (YF32 ? 3 : 2);
   constexpr int kWide = 32 * RK + 8;         // a row of u in LDS, so that 16 rows lie in different banks
+  constexpr int kRows = RK <= 2 ? 64 : (RK == 4 ? 32 : 16);          // rows whose u is held
   using T = std::conditional_t<YF32, float, __bf16>;
   using U = std::conditional_t<WF32, float, __bf16>;
+  using four_t = T __attribute__((ext_vector_type(4)));
   __shared__ int rows[kTokens];
-  __shared__ __attribute__((aligned(16))) U us[P][16][kWide];
+  __shared__ __attribute__((aligned(16))) U us[P][kRows][kWide];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, quarter = lane >> 4;
   const T* base = (const T*)a.base;
   T* y = (T*)a.y;
-  if (blockIdx.x >= (unsigned)a.slots * a.groups) {                  // rows without an adapter
-    const int64_t c0 = (int64_t)(blockIdx.x - a.slots * a.groups) * kCopy, c1 = min(c0 + kCopy, (int64_t)a.cout);
-    const int64_t first = (int64_t)blockIdx.y * kTokens;
+  // a workgroup serves up to 64 chunks of 64 rows
+  const int chunk0 = (int)blockIdx.y * 64, chunks = (int)min((int64_t)64, (a.rows + kTokens - 1) / kTokens - chunk0);
+  if (blockIdx.x >= (unsigned)a.groups) {                            // rows without an adapter
+    const int place = blockIdx.x - a.groups, parts = (a.cout + kCopy - 1) / kCopy;
+    const int64_t first = ((int64_t)chunk0 + place / parts) * kTokens;
+    const int c0 = place % parts * kCopy, c1 = min(c0 + kCopy, a.cout);
     const int id = first + lane < a.rows ? a.index[first + lane] : 0;
     for (uint64_t left = __ballot(id < 0 || id >= a.adapters); left; left &= left - 1) {
       const int64_t at = (first + __ffsll((unsigned long long)left) - 1) * a.cout;
-      for (int64_t c = c0 + threadIdx.x; c < c1; c += kThreads) y[at + c] = base[at + c];
+      for (int c = c0 + threadIdx.x; c < c1; c += kThreads) y[at + c] = base[at + c];
     }
     return;
   }
-  const int slot = blockIdx.x / (unsigned)a.groups, group = blockIdx.x % (unsigned)a.groups;
-  const int* plan = a.plan + ((int64_t)blockIdx.y * a.slots + slot) * kPlan;
-  const int adapter = __builtin_amdgcn_readfirstlane(plan[0]), n = __builtin_amdgcn_readfirstlane(plan[1]);
-  if (n == 0) return;
-  const int ranks = rank_of(a, adapter);
-  const int c0 = (group * kWaves + wave) * 16 * NT;
-  // a wave's weights; what is past the adapter's rank counts as 0
-  constexpr int kUnits = WF32 ? 2 * RK : RK, kEach = WF32 ? 4 : 8;
-  v4u w[NT][kUnits];
+  // the steps of all adapters of these chunks, shared out evenly
+  constexpr int kStep = 16 * NT * kWaves;    // channels of a step
+  int upto = lane < chunks ? a.hits[chunk0 + lane] : 0;
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int64_t at = ((int64_t)adapter * a.cout + min(c0 + 16 * j + i, a.cout - 1)) * a.rank;
-#pragma unroll
-    for (int s = 0; s < kUnits; ++s) {
-      const int k = (s * 4 + quarter) * kEach;
-      w[j][s] = WF32 ? *(const v4u*)((const float*)a.b + at + min(k, a.rank - kEach)) : *(const v4u*)((const __bf16*)a.b + at + min(k, a.rank - kEach));
-    }
+  for (int o = 1; o < 64; o <<= 1) {
+    const int v = __shfl_up(upto, o, 64);
+    if (lane >= o) upto += v;
   }
-  if (threadIdx.x < kTokens) rows[threadIdx.x] = plan[4 + threadIdx.x];
-  const float scaling = a.scaling ? a.scaling[adapter] : 1.0f;
+  const unsigned steps = (a.cout + kStep - 1) / kStep, all = __builtin_amdgcn_readlane(upto, 63) * steps, per = all / a.groups, over = all - per * a.groups;
+  unsigned place = per * blockIdx.x + min(blockIdx.x, over);
+  const unsigned end = place + per + (blockIdx.x < over);
+  const bool whole = a.cout % 4 == 0;        // four neighbouring channels are one load
+  constexpr int kUnits = WF32 ? 2 * RK : RK, kEach = WF32 ? 4 : 8;
+  while (place < end) {                       // the share's part of one adapter
+    const int hit = place / steps, s0 = place - hit * steps, s1 = min(steps, s0 + (end - place));
+    place += s1 - s0;
+    const int chunk = __ffsll((unsigned long long)__ballot(upto > hit)) - 1, slot = hit - (chunk > 0 ? __builtin_amdgcn_readlane(upto, chunk - 1) : 0);
+    const int* plan = a.plan + ((int64_t)(chunk0 + chunk) * a.slots + slot) * kPlan;
+    const int adapter = __builtin_amdgcn_readfirstlane(plan[0]), n = __builtin_amdgcn_readfirstlane(plan[1]), ranks = __builtin_amdgcn_readfirstlane(plan[2]);
+    v4u next[NT][kUnits];
+    auto load_w = [&](int step) __attribute__((always_inline)) {
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
+      for (int j = 0; j < NT; ++j) {
+        const int64_t at = ((int64_t)adapter * a.cout + min(step * kStep + (wave * NT + j) * 16 + i, a.cout - 1)) * a.rank;
 #pragma unroll
-    for (int s = 0; s < kUnits; ++s) {
-      const int left = ranks - (s * 4 + quarter) * kEach;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (WF32)
-          w[j][s][e] = e < left ? w[j][s][e] : 0u;
-        else
-          w[j][s][e] = 2 * e + 1 < left ? w[j][s][e] : (2 * e < left ? w[j][s][e] & 0xFFFFu : 0u);
+        for (int s = 0; s < kUnits; ++s) {
+          if (s > 0 && s * 4 * kEach >= ranks) break;
+          const int k = min((s * 4 + quarter) * kEach, a.rank - kEach);
+          next[j][s] = WF32 ? *(const v4u*)((const float*)a.b + at + k) : *(const v4u*)((const __bf16*)a.b + at + k);
+        }
       }
-    }
-  for (int r0 = 0; r0 < n; r0 += 16) {
-    const int live = min(16, n - r0);
-    __syncthreads();
-    for (int at = threadIdx.x; at < 16 * 32 * RK; at += kThreads) {
-      const int r = at / (32 * RK), k = at % (32 * RK);
-      float v = 0.0f;
-      if (r < live && k < ranks) {
-        const float* from = a.u + (int64_t)rows[r0 + r] * a.wide + k;
-        float got[kMaxParts];
+    };
+    load_w(s0);
+    __syncthreads();                            // the rows before have been used
+    if (threadIdx.x < kTokens) rows[threadIdx.x] = plan[4 + threadIdx.x];
+    const float scaling = a.scaling ? a.scaling[adapter] : 1.0f;
+    for (int r0 = 0; r0 < n; r0 += kRows) {
+      const int live = min(kRows, n - r0);
+      __syncthreads();
+      for (int at = threadIdx.x; at < live * 32 * RK; at += kThreads) {
+        const int r = at / (32 * RK), k = at % (32 * RK);
+        float v = 0.0f;
+        if (k < ranks) {
+          const float* from = a.u + (int64_t)rows[r0 + r] * a.wide + k;
+          float got[kMaxParts];
 #pragma unroll
-        for (int p = 0; p < kMaxParts; ++p) got[p] = from[(int64_t)min(p, a.parts - 1) * a.rows * a.wide];
+          for (int p = 0; p < kMaxParts; ++p) got[p] = from[(int64_t)min(p, a.parts - 1) * a.rows * a.wide];
 #pragma unroll
-        for (int p = 0; p < kMaxParts; ++p) v += p < a.parts ? got[p] : 0.0f;
-        v *= scaling;
+          for (int p = 0; p < kMaxParts; ++p) v += p < a.parts ? got[p] : 0.0f;
+          v *= scaling;
+        }
+        if constexpr (WF32) {
+          us[0][r][k] = v;
+        } else {
+          __bf16 pieces[P];
+          split<P>(v, pieces);
+#pragma unroll
+          for (int p = 0; p < P; ++p) us[p][r][k] = pieces[p];
+        }
       }
-      if constexpr (WF32) {
-        us[0][r][k] = v;
-      } else {
-        __bf16 pieces[P];
-        split<P>(v, pieces);
+      __syncthreads();
+      if (r0 > 0) load_w(s0);
+      four_t soon[NT];                          // base of the first 16 rows, with the weights
+      auto load_base = [&](four_t (&to)[NT], int t, int step) __attribute__((always_inline)) {
+        const int64_t row = rows[r0 + min(t + i, live - 1)];
 #pragma unroll
-        for (int p = 0; p < P; ++p) us[p][r][k] = pieces[p];
-      }
-    }
-    __syncthreads();
+        for (int j = 0; j < NT; ++j) to[j] = *(const four_t*)(base + row * a.cout + min(step * kStep + (wave * NT + j) * 16 + 4 * quarter, a.cout - 4));
+      };
+      if (whole) load_base(soon, 0, s0);
+      for (int step = s0; step < s1; ++step) {
+        const int c0 = step * kStep + wave * NT * 16;
+        four_t old[NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      v4f acc = {0, 0, 0, 0};
+        for (int j = 0; j < NT; ++j) {
+          old[j] = soon[j];
+          asm volatile("" : "+v"(old[j]));
+        }
+        v4u w[NT][kUnits];                      // what is past the adapter's rank counts as 0
 #pragma unroll
-      for (int s = 0; s < kUnits; ++s)
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-          const v4u u = *(const v4u*)&us[p][i][(s * 4 + quarter) * kEach];
-          if constexpr (WF32) {
+          for (int s = 0; s < kUnits; ++s) {
+            const int left = ranks - (s * 4 + quarter) * kEach;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc = mfma_f32(__uint_as_float(w[j][s][e]), __uint_as_float(u[e]), acc);
-          } else {
-            acc = mfma(__builtin_bit_cast(b8, w[j][s]), __builtin_bit_cast(b8, u), acc);
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (WF32)
+                w[j][s][e] = e < left ? next[j][s][e] : 0u;
+              else
+                w[j][s][e] = 2 * e + 1 < left ? next[j][s][e] : (2 * e < left ? next[j][s][e] & 0xFFFFu : 0u);
+            }
+            asm volatile("" : "+v"(w[j][s]));
+          }
+        if (step + 1 < s1) {
+          load_w(step + 1);
+          if (whole) load_base(soon, 0, step + 1);
+        }
+        for (int t = 0; t < live; t += 16) {
+          if (t > 0 && whole) load_base(old, t, step);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            v4f acc = {0, 0, 0, 0};
+#pragma unroll
+            for (int s = 0; s < kUnits; ++s)
+#pragma unroll
+              for (int p = 0; p < P; ++p) {
+                const v4u u = *(const v4u*)&us[p][min(t + i, live - 1)][(s * 4 + quarter) * kEach];
+                if constexpr (WF32) {
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) acc = mfma_f32(__uint_as_float(w[j][s][e]), __uint_as_float(u[e]), acc);
+                } else {
+                  acc = mfma(__builtin_bit_cast(b8, w[j][s]), __builtin_bit_cast(b8, u), acc);
+                }
+              }
+            if (t + i >= live) continue;
+            const int c = c0 + 16 * j + 4 * quarter;
+            const int64_t at = (int64_t)rows[r0 + t + i] * a.cout + c;
+            if (whole) {
+              if (c >= a.cout) continue;
+              four_t v;
+#pragma unroll
+              for (int r = 0; r < 4; ++r) v[r] = (T)((float)old[j][r] + acc[r]);
+              *(four_t*)(y + at) = v;
+            } else {
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (c + r < a.cout) y[at + r] = (T)((float)base[at + r] + acc[r]);
+            }
           }
         }
-      if (i >= live) continue;
-      const int c = c0 + 16 * j + 4 * quarter;
-      const int64_t at = (int64_t)rows[r0 + i] * a.cout + c;
-      if (a.cout % 4 == 0) {
-        if (c >= a.cout) continue;
-        T v[4];
-        __builtin_memcpy(v, __builtin_assume_aligned(base + at, 4 * sizeof(T)), sizeof v);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = (T)((float)v[r] + acc[r]);
-        __builtin_memcpy(__builtin_assume_aligned(y + at, 4 * sizeof(T)), v, sizeof v);
-      } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (c + r < a.cout) y[at + r] = (T)((float)base[at + r] + acc[r]);
       }
     }
   }
 }
 
 struct Layout {
-  int64_t slots, chunks, parts, wide, plan, all;                       // chunks of rows; bytes
+  int64_t slots, chunks, parts, wide, hits, plan, all;                 // chunks of rows; bytes
 };
 Layout layout(const AdapterView& v) {
   Layout l{};
@@ -322,7 +378,8 @@ Layout layout(const AdapterView& v) {
   l.parts = std::clamp<int64_t>(((v.cin + kChunk - 1) / kChunk + kWaves - 1) / kWaves, 1, kMaxParts);
   l.wide = (v.rank + 31) / 32 * 32;
   l.plan = (l.slots * l.chunks * kPlan * 4 + 255) / 256 * 256;
-  l.all = l.plan + l.parts * v.rows * l.wide * 4;
+  l.hits = (l.chunks * 4 + 255) / 256 * 256;
+  l.all = l.hits + l.plan + l.parts * v.rows * l.wide * 4;
   return l;
 }
 
@@ -336,17 +393,19 @@ hipError_t go_in(const Args& a, const Layout& l, hipStream_t stream) {
 
 template <bool YF32, bool WF32, int RK, int NT>
 hipError_t go_out(Args a, const Layout& l, hipStream_t stream) {
-  a.groups = (a.cout + 16 * NT * kWaves - 1) / (16 * NT * kWaves);
-  const int64_t n = l.slots * a.groups + (a.in_place ? 0 : (a.cout + kCopy - 1) / kCopy);
+  const int64_t steps = (a.cout + 16 * NT * kWaves - 1) / (16 * NT * kWaves), chunks = std::min<int64_t>(l.chunks, 64);
+  if (l.slots * chunks * steps >= int64_t(1) << 31) return hipErrorInvalidConfiguration;
+  a.groups = (int)std::min<int64_t>(l.slots * chunks * steps, kGroups);
+  const int64_t n = a.groups + (a.in_place ? 0 : (a.cout + kCopy - 1) / kCopy * chunks);
   if (n >= int64_t(1) << 24) return hipErrorInvalidConfiguration;
-  return launch_kernel(k_adapter_out<YF32, WF32, RK, NT>, dim3((unsigned)n, (unsigned)l.chunks), dim3(kThreads), 0, stream, a);
+  return launch_kernel(k_adapter_out<YF32, WF32, RK, NT>, dim3((unsigned)n, (unsigned)((l.chunks + 63) / 64)), dim3(kThreads), 0, stream, a);
 }
 
 template <bool YF32, bool WF32>
 hipError_t go_rank(const Args& a, const Layout& l, hipStream_t stream) {
-  if (a.rank <= 32) return go_out<YF32, WF32, 1, 4>(a, l, stream);
-  if (a.rank <= 64) return go_out<YF32, WF32, 2, 4>(a, l, stream);
-  if (a.rank <= 128) return go_out<YF32, WF32, 4, 2>(a, l, stream);
+  if (a.rank <= 32) return go_out<YF32, WF32, 1, 2>(a, l, stream);
+  if (a.rank <= 64) return go_out<YF32, WF32, 2, 2>(a, l, stream);
+  if (a.rank <= 128) return go_out<YF32, WF32, 4, 1>(a, l, stream);
   return go_out<YF32, WF32, 8, 1>(a, l, stream);
 }
 
@@ -366,8 +425,9 @@ hipError_t launch_adapter(const AdapterView& v, void* work, hipStream_t stream) 
   a.ranks = v.ranks;
   a.base = v.base;
   a.y = v.y;
-  a.plan = (int*)work;
-  a.u = (float*)((char*)work + l.plan);
+  a.hits = (int*)work;
+  a.plan = (int*)((char*)work + l.hits);
+  a.u = (float*)((char*)work + l.hits + l.plan);
   a.rows = v.rows;
   a.cin = (int)v.cin;
   a.cout = (int)v.cout;

@@ -20,7 +20,8 @@ namespace lh {
 namespace {
 
 constexpr int kMaxThreads = 1024;
-constexpr int kRun = 2048;                   // rows of one workgroup of the second kernel
+constexpr int kRun = 1024;                   // rows of one workgroup of the second kernel
+constexpr int kWindow = 512;                 // sequences whose first rows it holds
 
 struct Args {
   int* table;
@@ -164,9 +165,8 @@ __device__ inline int given_back(const Args& a, const Plan& p, int i) {
   return a.table[b * a.width + p.kept[b] + (i - p.freed[b])];
 }
 
-// Row r, whose sequence is among lo .. hi (the batch's size: behind the last sequence).
-__device__ inline void one_row(const Args& a, const Plan& p, int r, int lo, int hi, int count) {
-  const int b = last_upto(p.start, r, lo, hi);
+// Row r of sequence b (the batch's size: behind the last sequence).
+__device__ inline void one_row(const Args& a, const Plan& p, int r, int b, int count) {
   int64_t slot = -1;
   int position = -1, sequence = -1;
   if (b < a.batch) {
@@ -200,7 +200,7 @@ __global__ __launch_bounds__(kMaxThreads) void k_extend(const Args a) {
   sums(a, p, shared);
   __syncthreads();
   const int count = p.head[0];
-  for (int r = threadIdx.x; r < a.rows; r += blockDim.x) one_row(a, p, r, 0, a.batch, count);
+  for (int r = threadIdx.x; r < a.rows; r += blockDim.x) one_row(a, p, r, last_upto(p.start, r, 0, a.batch), count);
   const int back = min(p.head[2], a.capacity - count);
   for (int i = threadIdx.x; i < back; i += blockDim.x) a.stack[count + i] = given_back(a, p, i);
 }
@@ -210,14 +210,44 @@ __global__ __launch_bounds__(kMaxThreads) void k_extend_sums(const Args a) {
   sums(a, Plan(a.work, a.batch + 1), shared);
 }
 
+// The last of v[0 .. n) that is at most x (v[0] is), for the whole workgroup of 256: 256 places at a time.
+__device__ inline int last_upto_together(const int* v, int x, int n, int* shared) {
+  int lo = 0, span = n;                      // in [lo, lo + span)
+  while (span > 1) {
+    const int step = (span + 255) / 256;
+    const int64_t at = lo + (int64_t)threadIdx.x * step;
+    const uint64_t upto = __ballot(at < lo + (int64_t)span && v[min(at, (int64_t)n - 1)] <= x);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = __popcll(upto);
+    __syncthreads();
+    const int before = shared[0] + shared[1] + shared[2] + shared[3] - 1;
+    span = min(step, lo + span - (lo + before * step));
+    lo += before * step;
+  }
+  return lo;
+}
+
+// A workgroup finds its first row's sequence, takes the starts of the sequences from there on into LDS, and looks its
+// rows up among them (in memory, where a run of rows spans more sequences than that).
 __global__ __launch_bounds__(256) void k_extend_rows(const Args a) {
+  __shared__ int shared[4];
+  __shared__ int starts[kWindow];
   const Plan p(a.work, a.batch + 1);
   const int count = p.head[0], back = min(p.head[2], a.capacity - count);
   const int64_t r0 = (int64_t)blockIdx.x * kRun;
   if (r0 < a.rows) {
     const int r1 = (int)min(r0 + kRun, (int64_t)a.rows);
-    const int lo = last_upto(p.start, (int)r0, 0, a.batch), hi = last_upto(p.start, r1 - 1, lo, a.batch);
-    for (int r = (int)r0 + threadIdx.x; r < r1; r += 256) one_row(a, p, r, lo, hi, count);
+    const int lo = last_upto_together(p.start, (int)r0, a.batch + 1, shared), held = min(kWindow, a.batch + 1 - lo);
+    for (int k = threadIdx.x; k < held; k += 256) starts[k] = p.start[lo + k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kRun / 256; ++k) {
+      const int r = (int)r0 + threadIdx.x + 256 * k;
+      if (r >= r1) break;
+      int b = lo + last_upto(starts, r, 0, held - 1);
+      if (b == lo + held - 1 && b < a.batch) b = last_upto(p.start, r, b, a.batch);
+      one_row(a, p, r, b, count);
+    }
   }
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < back; i += (int64_t)gridDim.x * 256)
     a.stack[count + i] = given_back(a, p, (int)i);

@@ -494,3 +494,10 @@ def test_adapter_nothing():
     assert y.shape == (0, 40)
     y = lh.lh_adapter(torch.ones(3, 32, device=DEV), torch.empty(3, 0, device=DEV), a, torch.zeros(2, 0, 8, device=DEV), dev([0, 1, 0]))
     assert y.shape == (3, 0)
+
+
+def test_adapter_many_rows():
+    """More than 64 times 64 rows, whose adapters are shared out over workgroups 4096 rows at a time."""
+    note("adapter 4300 rows")
+    case = adapter_case(4300, 64, 100, 5, 8, "bf16", 0, "bf16", 6)
+    check_adapter(case, "bf16", 0, "bf16")
