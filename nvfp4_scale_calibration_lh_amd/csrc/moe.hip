@@ -5,9 +5,9 @@
 //   gate and up  the channels of all experts that (up to 64) tokens hit, in tiles, are shared out evenly over as many workgroups as
 //                are resident; each finds the experts of its share and their rows from the ids by itself.  A wave has 8 gate rows
 //                and the 8 up rows that belong to them as one 16-row operand, so that silu(g) * u needs no other wave.
-//                h = w * silu(g) * u goes to the workspace in fp32.
+//                h = silu(g) * u goes to the workspace in fp32.
 //   down         the same walk over D_e with h for x, one fp32 row for each chosen expert of a token
-//   sum          adds a token's rows in the order of its choices
+//   sum          adds a token's rows times their weights, in the order of its choices
 // The rows (x or h) are staged in LDS, as much of k as fits, and shared by the workgroup's waves; the weights stream through registers, each
 // wave its own channels, or `split` waves a share of k each where that is needed to fill the chip.
 //
@@ -26,8 +26,7 @@ namespace {
 
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kU = 4;                        // chunks of k a wave takes at a time, at most
-constexpr int kBudget = 64 * 1024;           // LDS of the rows, so that two workgroups fit a compute unit
+constexpr int kLds = 80 * 1024;              // of a workgroup, so that two fit a compute unit
 constexpr int kResident = 2 * 256;           // workgroups
 
 struct Args {
@@ -45,16 +44,18 @@ struct Args {
   void* y;
   int64_t tokens;
   int hidden, inner, experts, topk, x_scales, slots;
-  int split, each, rows;                     // waves that share k; chunks of a step; rows taken at a time
+  int split, each, rows;                     // waves that share k; chunks of a step of theirs; rows taken at a time
+  int budget;                                // LDS of the rows
   float gdiv;
 };
 
-// A step's weights of a lane: 32 nibbles of each chunk, and the 8 scales of its channel for the chunk that is its quarter of the wave.
-// (Scales loaded chunk by chunk, 8 bytes a channel, made the reading of the weights take 69 us where this takes 43: 135 experts
+// A step's weights of a lane: 32 nibbles of each chunk, and the 8 scales of its channel for the chunk of each four that is its quarter of
+// the wave.  (Scales loaded chunk by chunk, 8 bytes a channel, made the reading of the weights take 69 us where this takes 43: 135 experts
 // of 1280x2560, 249 MB, loads alone.)
+template <int U>
 struct Weights {
-  v4u nib[kU];
-  v2u code;
+  v4u nib[U];
+  v2u code[(U + 3) / 4];
 };
 
 __device__ inline unsigned row_max(unsigned v) {     // over 16 neighbouring lanes
@@ -78,22 +79,23 @@ __device__ inline float silu(float g) {
   return g / (1.0f + e);
 }
 
-// X: type of the rows, in P pieces.  DOWN: the second product, whose rows are h.  MT: 16-row tiles taken at a time at most.  SMALL: k is
-// less than a chunk.
+// X: type of the rows, in P pieces.  DOWN: the second product, whose rows are h.  MT: 16-row tiles taken at a time at most.  U: chunks of k
+// a wave holds or has on their way; a chunk's registers are loaded again as soon as it has been multiplied.  U = 1: k is less than a chunk.
 //
 // Instructions are fetched from cold caches at each launch (0.6 us a KB was seen), which a call for one token feels: so the code is short, its
 // loops are not unrolled further than the registers ask for, and there are no 64-bit divisions.
-template <int X, int P, bool DOWN, int MT, bool SMALL>
+template <int X, int P, bool DOWN, int MT, int U>
 __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
   constexpr int kRows = DOWN ? 16 : 8;       // channels of a tile
+  constexpr bool SMALL = U == 1;
+  constexpr int kSets = (U + 3) / 4;
   __shared__ uint64_t bits[64];
   __shared__ int rows[kTokens], source[kTokens];                     // an expert's rows: choices, and rows of x
-  __shared__ float share[kTokens];
   __shared__ int found;
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  __shared__ __attribute__((aligned(16))) uint8_t codes[kWaves][16][8 * kU];
-  float* red = (float*)(lds + kBudget);
-  short* chosen = (short*)(lds + kBudget + kWaves * 1024);
+  __shared__ __attribute__((aligned(16))) uint8_t codes[kWaves][kSets][16][32];
+  short* chosen = (short*)(lds + a.budget);
+  float* red = (float*)(lds + a.budget + (DOWN ? 0 : kTokens * 2 * a.topk));
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, quarter = lane >> 4;
   const int shift = __builtin_ctz(a.split), ks = wave & (a.split - 1), mine = wave >> shift, together = kWaves >> shift;    // tiles of the workgroup
@@ -126,10 +128,11 @@ __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
   unsigned at = per * blockIdx.x + min(blockIdx.x, over);
   const unsigned end = at + per + (blockIdx.x < over);
 
-  const int k_all = DOWN ? a.inner : a.hidden, full = k_all / kChunk, chunks = (k_all + kChunk - 1) / kChunk;
+  const int k_all = DOWN ? a.inner : a.hidden, chunks = (k_all + kChunk - 1) / kChunk;
   const unsigned row_bytes = (unsigned)k_all / 2, row_codes = (unsigned)k_all / 16;
   // the last chunk, if short, is the last 128 elements, and those that the one before it has are 0 in the rows
-  auto start_of = [&](int c) { return SMALL ? 0 : (c < full ? c * kChunk : k_all - kChunk); };
+  const int last_start = k_all - kChunk;
+  auto start_of = [&](int c) { return SMALL ? 0 : min(c * kChunk, last_start); };
   const int turn = a.each * a.split, steps = (chunks + turn - 1) / turn;       // of every wave; past the last chunk it multiplies nothing
   const unsigned channel = DOWN ? i : (i < 8 ? i : a.inner + i - 8);
   const unsigned w_at = channel * row_bytes + quarter * 16, c_at = channel * row_codes;
@@ -140,66 +143,68 @@ __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
     int* plan = a.plan + ((int64_t)blockIdx.y * a.slots + slot) * kPlan;
     const int expert = DOWN ? __builtin_amdgcn_readfirstlane(plan[0]) : find_expert(bits, slot);
     const int64_t channel0 = (int64_t)expert * (DOWN ? a.hidden : 2 * a.inner);
-    // a step's weights of a wave: of tile `mine` of a group, its chunks of k
-    auto load_w = [&](Weights& w, int group, int step) __attribute__((always_inline)) {
+    // where a step's weights of a wave are, tile `mine` of a group and its chunks of k; past the last step all lanes load one place
+    // again, so that the loads in flight are the same number on every path
+    struct Place {
+      const uint8_t *nib, *code;
+      int chunk;
+      unsigned mask;
+    };
+    auto place_of = [&](int group, int step, bool any) __attribute__((always_inline)) {
       const int64_t c0 = channel0 + min((first + group) * together + mine, tiles - 1) * kRows;
-      const uint8_t *n0 = a.fp4 + c0 * row_bytes, *q0 = a.code + c0 * row_codes;
-      const int c = (step * a.split + ks) * a.each;
+      return Place{a.fp4 + c0 * row_bytes, a.code + c0 * row_codes, (step * a.split + ks) * a.each, any ? ~0u : 0u};
+    };
+    Weights<U> w;
+    auto load_nib = [&](const Place& p, int u) __attribute__((always_inline)) {
       if constexpr (SMALL) {                  // 16 elements at a time
         const int left = k_all - quarter * 32;
         w.nib[0] = v4u{0, 0, 0, 0};
-        w.code = v2u{0, 0};
         if (left >= 16) {
-          const v2u v = *(const v2u*)(n0 + w_at);
+          const v2u v = *(const v2u*)(p.nib + w_at);
           w.nib[0][0] = v[0], w.nib[0][1] = v[1];
         }
         if (left >= 32) {
-          const v2u v = *(const v2u*)(n0 + w_at + 8);
+          const v2u v = *(const v2u*)(p.nib + w_at + 8);
           w.nib[0][2] = v[0], w.nib[0][3] = v[1];
         }
-#pragma unroll
-        for (int b = 0; b < 7; ++b)
-          if (16 * b < k_all) w.code[b / 4] |= (unsigned)q0[c_at + b] << (8 * (b % 4));
-        return;
-      }
-      if (quarter < a.each && c + quarter < chunks) w.code = *(const v2u_a1*)(q0 + (start_of(c + quarter) / 16 + c_at));
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        if (u >= a.each || c + u >= chunks) break;
-        w.nib[u] = *(const v4u_a8*)(n0 + start_of(c + u) / 2 + w_at);
+      } else {
+        w.nib[u] = *(const v4u_a8*)(p.nib + (unsigned)start_of(p.chunk + u) / 2 + (w_at & (u < a.each ? p.mask : 0u)));
       }
     };
-    Weights next;
-    load_w(next, 0, 0);
+    auto load_code = [&](const Place& p, int s) __attribute__((always_inline)) {
+      if constexpr (SMALL) {
+        w.code[0] = v2u{0, 0};
+#pragma unroll
+        for (int b = 0; b < 7; ++b)
+          if (16 * b < k_all) w.code[0][b / 4] |= (unsigned)p.code[c_at + b] << (8 * (b % 4));
+      } else {
+        w.code[s] = *(const v2u_a1*)(p.code + (((unsigned)start_of(p.chunk + 4 * s + quarter) / 16 + c_at) & p.mask));
+      }
+    };
+    auto load_all = [&]() __attribute__((always_inline)) {
+      const Place p = place_of(0, 0, true);
+#pragma unroll
+      for (int s = 0; s < kSets; ++s) load_code(p, s);
+#pragma unroll
+      for (int u = 0; u < U; ++u) load_nib(p, u);
+    };
     __syncthreads();                          // the rows before have been used
     int n;
     if constexpr (DOWN) {
       n = __builtin_amdgcn_readfirstlane(plan[1]);
       if (threadIdx.x < kTokens) rows[threadIdx.x] = source[threadIdx.x] = plan[4 + threadIdx.x];
-    } else if (wave < 2) {                    // a token's first choice of the expert stands for all of them
-      int pick = -1, repeats = 0;
+    } else if (wave == 0) {                   // a token's first choice of the expert stands for all of them
+      int pick = -1;
       if (lane < tokens)
 #pragma clang loop unroll_count(2)
-        for (int j = a.topk - 1; j >= 0; --j) {
-          const bool same = chosen[lane * a.topk + j] == expert;
-          repeats += same;
-          pick = same ? j : pick;
-        }
+        for (int j = a.topk - 1; j >= 0; --j) pick = chosen[lane * a.topk + j] == expert ? j : pick;
       const uint64_t hit = __ballot(pick >= 0);
       const int rank = __popcll(hit & ((1ull << lane) - 1)), number = (int)(token0 + lane) * a.topk + pick;
-      if (wave == 0) {
-        if (pick >= 0) rows[rank] = number, source[rank] = (int)token0 + lane;
-        if (lane == 0) found = __popcll(hit);
-        if (first == 0) {                     // for the second product
-          if (lane == 0) plan[0] = expert, plan[1] = __popcll(hit);
-          if (pick >= 0) plan[4 + rank] = number;
-        }
-      } else if (pick >= 0) {
-        float sum = a.weights[number];
-#pragma clang loop unroll(disable)
-        for (int j = pick + 1; repeats > 1; ++j)
-          if (chosen[lane * a.topk + j] == expert) sum += a.weights[number - pick + j], --repeats;
-        share[rank] = sum;
+      if (pick >= 0) rows[rank] = number, source[rank] = (int)token0 + lane;
+      if (lane == 0) found = __popcll(hit);
+      if (first == 0) {                       // for the second product
+        if (lane == 0) plan[0] = expert, plan[1] = __popcll(hit);
+        if (pick >= 0) plan[4 + rank] = number;
       }
     }
     __syncthreads();
@@ -210,18 +215,20 @@ __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
     for (int r0 = 0; r0 < n; r0 += a.rows) {
       const int live = min(a.rows, n - r0);
       // chunks of the rows that LDS holds at a time
-      const int fit = (kBudget - live * P * 16) / (live * turn * (P * kChunk * 2 + 4));
+      const int fit = (a.budget - live * P * 16) / (live * turn * (P * kChunk * 2 + 4));
       const int panel = min(max(fit, 1), steps) * turn, panels = (chunks + panel - 1) / panel;
       const unsigned stride = panel * (kChunk * 2) + 16;             // bytes of a row's piece; 16 rows begin in different banks
       float* scales = (float*)(lds + live * P * stride);             // [chunk][row]
       int begin = -1;                                                // of what is held, in chunks
+      bool fresh = true;                                             // no weights are on their way
       auto hold = [&](int from) __attribute__((always_inline)) {
         begin = from;
         __syncthreads();
         const int units = min(panel, chunks - begin) * (kChunk / 8), total = live * units;
         const float reciprocal = 1.0f / (float)units;
 #pragma clang loop unroll(disable)
-        for (int at0 = threadIdx.x; at0 < total; at0 += 2 * kThreads) {
+        for (int done = 0; done < total; done += 2 * kThreads) {
+          const int at0 = done + threadIdx.x;
           v4u got[2][X == kXF32 ? 2 : 1];
           float scale[2];
           int r[2], u[2];
@@ -242,6 +249,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
               scale[b] = a.x_scale[row * a.x_scales + (a.x_scales > 1 ? c : 0)];
             }
           }
+          if (fresh) load_all(), fresh = false;      // behind the first rows, which are needed first
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             const int c = begin + u[b] / 16, k = start_of(c) + u[b] % 16 * 8;
@@ -284,7 +292,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
 #pragma unroll
       for (int t = 0; t < MT; ++t) acc[t] = v4f{0, 0, 0, 0};
       auto multiply = [&](const v4u& nib, int u, int c) __attribute__((always_inline)) {
-        const h2 scale = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)*(const uint16_t*)&codes[wave][i][8 * u + 2 * quarter], 1.0f, false);
+        const h2 scale = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)*(const uint16_t*)&codes[wave][u / 4][i][8 * (u % 4) + 2 * quarter], 1.0f, false);
         h8 f[4];
         each<4>([&](auto st) __attribute__((always_inline)) {
           constexpr int S = decltype(st)::value;
@@ -309,27 +317,24 @@ __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
           acc[t] += scales[(c - begin) * live + row] * sum;
         }
       };
-      if (r0 > 0) load_w(next, 0, 0);         // once more
       int group = 0, step = 0;
 #pragma clang loop unroll(disable)
       for (int left = count * steps; left > 0; --left) {
         const int now = step, here = panels == 1 ? 0 : now * turn / panel * panel;
         if (here != begin) hold(here);        // the same step of all waves
-        *(v2u*)&codes[wave][i][8 * quarter] = next.code;
-        v4u nib[kU];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          nib[u] = next.nib[u];
-          asm volatile("" : "+v"(nib[u]));    // waits for them here, before the next loads are issued, not behind those
-        }
         const bool last = ++step == steps;
         if (last) step = 0;
-        if (left > 1) load_w(next, group + last, step);
+        const Place p = place_of(group + (last && left > 1), step, left > 1);
+#pragma unroll
+        for (int s = 0; s < kSets; ++s) {
+          *(v2u*)&codes[wave][s][i][8 * quarter] = w.code[s];
+          load_code(p, s);
+        }
         const int c = (now * a.split + ks) * a.each;
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          if (u >= a.each || c + u >= chunks) break;
-          multiply(nib[u], u, c + u);
+        for (int u = 0; u < U; ++u) {
+          if (u < a.each && c + u < chunks) multiply(w.nib[u], u, c + u);
+          load_nib(p, u);
         }
         if (!last) continue;
         const int tile = (first + group) * together + mine;
@@ -354,11 +359,10 @@ __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
           if constexpr (DOWN) {
             if (own && row < live) *(v4f*)(a.part + (int64_t)rows[r0 + row] * a.hidden + 16 * tile + 4 * quarter) = v;
           } else {                            // a lane of the lower half has gate rows, 32 lanes on are their up rows
-            const float weight = share[min(r0 + row, kTokens - 1)];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const float up = __shfl_xor(v[r], 32, 64);
-              v[r] = silu(v[r]) * up * weight;
+              v[r] = silu(v[r]) * up;
             }
             if (own && row < live && quarter < 2) *(v4f*)(a.h + (int64_t)rows[r0 + row] * a.inner + 8 * tile + 4 * quarter) = v;
           }
@@ -379,26 +383,34 @@ __global__ __launch_bounds__(256) void k_experts_sum(const Args a) {
   const int lane = threadIdx.x & 63;
   const int* ids = a.ids + t * a.topk;
   const int id = lane < a.topk ? ids[lane] : -1;
+  const float given = lane < a.topk ? a.weights[t * a.topk + lane] : 0.0f;
+  float weight = 0.0f;                        // the sum of those of its expert
   bool first = id >= 0 && id < a.experts;
-  for (int j = 0; j + 1 < a.topk; ++j)
-    if (j < lane && __builtin_amdgcn_readlane(id, j) == id) first = false;
+#pragma clang loop unroll(disable)
+  for (int j = 0; j < a.topk; ++j) {
+    const bool same = __builtin_amdgcn_readlane(id, j) == id;
+    weight += same ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(given), j)) : 0.0f;
+    first = first && !(same && j < lane);
+  }
   const uint64_t mask = __ballot(first);
   if (c >= a.hidden) return;
   v4f y = {0, 0, 0, 0};
   const float* from = a.part + t * a.topk * a.hidden + c;
   for (uint64_t m = mask; m;) {
     v4f v[4];
+    float w[4];
     bool have[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {              // independent loads
       have[k] = m != 0;
       const int j = have[k] ? __ffsll((unsigned long long)m) - 1 : __ffsll((unsigned long long)mask) - 1;
       v[k] = *(const v4f*)(from + (int64_t)j * a.hidden);
+      w[k] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(weight), j));
       m &= m - 1;
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (have[k]) y += v[k];
+      if (have[k]) y += w[k] * v[k];
   }
   if constexpr (BF16) {
     __bf16 out[4] = {(__bf16)y[0], (__bf16)y[1], (__bf16)y[2], (__bf16)y[3]};
@@ -426,42 +438,50 @@ Layout layout(const MoeView& v) {
   return l;
 }
 
-template <int X, int P, bool DOWN, int MT>
+template <int X, int P, bool DOWN, int MT, int U>
 hipError_t go(const MoeView& v, Args a, const Layout& l, hipStream_t stream) {
   const int64_t k = DOWN ? v.inner : v.hidden, tiles = DOWN ? v.hidden / 16 : v.inner / 8, chunks = (k + kChunk - 1) / kChunk;
+  const int64_t lds = kLds - 1536 - kWaves * 512 * ((U + 3) / 4) - (DOWN ? 0 : kTokens * 2 * v.topk), most = std::min<int64_t>(v.tokens, 16);
+  // rows whose chunks of a step LDS holds
+  auto fits = [&](int64_t turn, bool shared) { return (lds - (shared ? kWaves * 1024 : 0)) / (P * (turn * kChunk * 2 + 16) + 4 * turn); };
   // waves that share k, so that some 4000 waves have work
-  auto fits = [&](int64_t turn) { return kBudget / (P * (turn * kChunk * 2 + 16) + 4 * turn); };       // rows whose chunks of a step LDS holds
-  const int64_t rows = std::min<int64_t>(16 * MT, v.tokens);
   a.split = 1;
-  while (a.split < kWaves && 2 * a.split <= chunks && l.slots * tiles * a.split < kResident * kWaves && fits(2 * a.split) >= std::min<int64_t>(rows, 16)) a.split *= 2;
-  const int64_t steps = (chunks + kU * a.split - 1) / (kU * a.split);
+  while (a.split < kWaves && 2 * a.split <= chunks && l.slots * tiles * a.split < kResident * kWaves && fits(2 * a.split, true) >= most) a.split *= 2;
+  const bool shared = a.split > 1;
+  const int64_t steps = (chunks + U * a.split - 1) / (U * a.split);
   a.each = (int)((chunks + steps * a.split - 1) / (steps * a.split));
-  while (fits(a.each * a.split) < std::min<int64_t>(rows, 16)) --a.each;
-  a.rows = (int)std::min<int64_t>(16 * MT, fits(a.each * a.split) / 16 * 16);
-  if (a.rows < 16) a.rows = (int)rows;       // fewer than 16 tokens
+  while (fits(a.each * a.split, shared) < most) --a.each;
+  a.rows = (int)std::min<int64_t>(16 * MT, fits(a.each * a.split, shared) / 16 * 16);
+  if (a.rows < 16) a.rows = (int)most;        // fewer than 16 tokens
+  a.budget = (int)((lds - (shared ? kWaves * 1024 : 0)) / 16 * 16);
   const int64_t groups = (tiles + kWaves / a.split - 1) / (kWaves / a.split);
   if (l.slots * groups >= int64_t(1) << 31) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)std::min<int64_t>(kResident, l.slots * groups), (unsigned)l.chunks);
-  const size_t lds = kBudget + kWaves * 1024 + (DOWN ? 0 : kTokens * v.topk * 2);
-  return k < kChunk ? launch_kernel(k_experts<X, P, DOWN, MT, true>, grid, dim3(kThreads), lds, stream, a)
-                    : launch_kernel(k_experts<X, P, DOWN, MT, false>, grid, dim3(kThreads), lds, stream, a);
+  return launch_kernel(k_experts<X, P, DOWN, MT, U>, grid, dim3(kThreads), (size_t)(a.budget + (DOWN ? 0 : kTokens * 2 * v.topk) + (shared ? kWaves * 1024 : 0)), stream, a);
 }
 
-template <bool MANY>
+// Up to 16 tokens one row tile, more two or, where experts have many rows each, four.
+template <int X, int P, bool DOWN>
+hipError_t go_rows(const MoeView& v, const Args& a, const Layout& l, hipStream_t stream) {
+  constexpr int kMost = P == 1 ? 4 : 2;       // row tiles whose 4 chunks LDS holds
+  if ((DOWN ? v.inner : v.hidden) < kChunk) return v.tokens <= 16 ? go<X, P, DOWN, 1, 1>(v, a, l, stream) : go<X, P, DOWN, kMost, 1>(v, a, l, stream);
+  if (v.tokens <= 16) return go<X, P, DOWN, 1, 4>(v, a, l, stream);
+  return v.tokens * v.topk <= 4 * v.experts ? go<X, P, DOWN, P == 1 ? 2 : 1, 4>(v, a, l, stream) : go<X, P, DOWN, kMost, 4>(v, a, l, stream);
+}
+
 hipError_t go_all(const MoeView& v, Args a, const Layout& l, hipStream_t stream) {
-  constexpr int kOne = MANY ? 4 : 1, kTwo = MANY ? 2 : 1;            // 16-row tiles for which a step's chunks fit LDS in one or two pieces
   const int64_t blocks = (v.hidden / 4 + 255) / 256 * v.tokens;
   if (blocks >= (int64_t(1) << 24)) return hipErrorInvalidConfiguration;
   a.code = v.gate_up_code;
   a.fp4 = v.gate_up_fp4;
   a.amax = v.gate_up_amax;
-  hipError_t e = v.x_type == kXBf16 ? go<kXBf16, 1, false, kOne>(v, a, l, stream)
-                 : v.x_type == kXF32 ? go<kXF32, 2, false, kTwo>(v, a, l, stream) : go<kXE4m3, 1, false, kOne>(v, a, l, stream);
+  hipError_t e = v.x_type == kXBf16 ? go_rows<kXBf16, 1, false>(v, a, l, stream)
+                 : v.x_type == kXF32 ? go_rows<kXF32, 2, false>(v, a, l, stream) : go_rows<kXE4m3, 1, false>(v, a, l, stream);
   if (e != hipSuccess) return e;
   a.code = v.down_code;
   a.fp4 = v.down_fp4;
   a.amax = v.down_amax;
-  e = v.x_type == kXF32 ? go<kXF32, 2, true, kTwo>(v, a, l, stream) : go<kXF32, 1, true, kOne>(v, a, l, stream);
+  e = v.x_type == kXF32 ? go_rows<kXF32, 2, true>(v, a, l, stream) : go_rows<kXF32, 1, true>(v, a, l, stream);
   if (e != hipSuccess) return e;
   return v.x_type == kXF32 ? launch_kernel(k_experts_sum<false>, dim3((unsigned)blocks), dim3(256), 0, stream, a)
                            : launch_kernel(k_experts_sum<true>, dim3((unsigned)blocks), dim3(256), 0, stream, a);
@@ -491,7 +511,7 @@ hipError_t launch_moe(const MoeView& v, void* work, hipStream_t stream) {
   a.x_scales = (int)v.x_scales;
   a.slots = (int)l.slots;
   a.gdiv = v.gdiv;
-  return v.tokens <= 16 ? go_all<false>(v, a, l, stream) : go_all<true>(v, a, l, stream);
+  return go_all(v, a, l, stream);
 }
 
 }  // namespace lh
