@@ -29,6 +29,8 @@ constexpr int kThreads = 64 * kWaves;
 constexpr int kLds = 80 * 1024;              // of a workgroup, so that two fit a compute unit
 constexpr int kResident = 2 * 256;           // workgroups
 
+constexpr int kXHalf = 3;                    // rows as k_rows leaves them
+
 struct Args {
   const void* x;
   const float* x_scale;
@@ -40,12 +42,15 @@ struct Args {
   int* hits;                                 // experts hit by each 64 tokens
   int* plan;
   float* h;
+  _Float16* half;                            // rows made ready for products, and their factors (see k_rows)
+  float* factor;
   float* part;
   void* y;
   int64_t tokens;
   int hidden, inner, experts, topk, x_scales, slots;
   int split, each, rows;                     // waves that share k; chunks of a step of theirs; rows taken at a time
   int budget;                                // LDS of the rows
+  int64_t all_rows;                          // that were made ready
   float gdiv;
 };
 
@@ -68,6 +73,65 @@ __device__ inline unsigned row_max(unsigned v) {     // over 16 neighbouring lan
   return v;
 }
 
+// Eight elements of a row, as loaded, in fp16 pieces, and their factor, which 16 neighbouring lanes with the 128 elements of a chunk share
+// (E4M3 elements have one already).
+template <int X, int P>
+__device__ inline void make_ready(const v4u* got, bool in, h8* out, float& factor) {
+  if constexpr (X == kXE4m3) {
+    each<4>([&](auto pp) {
+      constexpr int Q = decltype(pp)::value;
+      const h2 v = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)got[0][Q / 2], 1.0f, Q % 2 == 1);
+      out[0][2 * Q] = v[0];
+      out[0][2 * Q + 1] = v[1];
+    });
+  } else {
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      v[e] = X == kXF32 ? __uint_as_float(got[e / 4][e % 4]) : __uint_as_float(e % 2 ? got[0][e / 2] & 0xFFFF0000u : got[0][e / 2] << 16);
+    unsigned most = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+    const int top = min(max((int)(row_max(in ? most : 0) >> 23), 1), 254);       // beside an infinity, what is finite stays so
+    factor = __builtin_ldexpf(1.0f, top - 141);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float y = __builtin_ldexpf(v[e], 141 - top);
+      out[0][e] = (_Float16)y;
+      if constexpr (P == 2) out[1][e] = y == (float)out[0][e] ? (_Float16)0.0f : (_Float16)(y - (float)out[0][e]);
+    }
+  }
+}
+
+// Rows of k elements made ready for the products once, where each would otherwise be made ready by many workgroups many times:
+// half [piece][row][chunk][128], factor [row][chunk].  Chunks as in k_experts: the last one, if short, is the last 128 elements
+// with 0 for those that the chunk before it has (k >= 128).
+template <int X, int P>
+__global__ __launch_bounds__(256) void k_rows(const void* x, const float* x_scale, int x_scales, _Float16* half, float* factor, int64_t rows, int k_all) {
+  const int chunks = (k_all + kChunk - 1) / kChunk;
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 16, row = at / chunks;
+  if (row >= rows) return;                    // 16 lanes together
+  const int c = (int)(at - row * chunks), k = min(c * kChunk, k_all - kChunk) + (threadIdx.x & 15) * 8;
+  const int64_t from = row * k_all + k;
+  v4u got[2];
+  float f;
+  if constexpr (X == kXF32) {
+    got[0] = *(const v4u*)((const float*)x + from), got[1] = *(const v4u*)((const float*)x + from + 4);
+  } else if constexpr (X == kXBf16) {
+    got[0] = *(const v4u*)((const __bf16*)x + from);
+  } else {
+    const v2u v = *(const v2u*)((const uint8_t*)x + from);
+    got[0] = v4u{v[0], v[1], 0, 0};
+    f = x_scale[row * x_scales + (x_scales > 1 ? c : 0)];
+  }
+  const bool in = k >= c * kChunk;
+  h8 out[P];
+  make_ready<X, P>(got, in, out, f);
+#pragma unroll
+  for (int p = 0; p < P; ++p) *(v4u*)(half + (p * rows * chunks + at) * kChunk + (threadIdx.x & 15) * 8) = in ? __builtin_bit_cast(v4u, out[p]) : v4u{0, 0, 0, 0};
+  if ((threadIdx.x & 15) == 0) factor[at] = f;
+}
+
 // n / d for n < 2^21, by the reciprocal of d (a quotient is at least 0.5 / d away from the next whole number).
 __device__ inline int quotient(int n, float reciprocal) { return (int)(((float)n + 0.5f) * reciprocal); }
 
@@ -87,7 +151,8 @@ __device__ inline float silu(float g) {
 template <int X, int P, bool DOWN, int MT, int U>
 __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
   constexpr int kRows = DOWN ? 16 : 8;       // channels of a tile
-  constexpr bool SMALL = U == 1;
+  constexpr bool SMALL = U == 1, READY = X == kXHalf;
+  constexpr int kBatch = READY ? 4 : 2;      // 16-byte units of rows that a thread loads together
   constexpr int kSets = (U + 3) / 4;
   __shared__ uint64_t bits[64];
   __shared__ int rows[kTokens], source[kTokens];                     // an expert's rows: choices, and rows of x
@@ -218,32 +283,41 @@ __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
       const int fit = (a.budget - live * P * 16) / (live * turn * (P * kChunk * 2 + 4));
       const int panel = min(max(fit, 1), steps) * turn, panels = (chunks + panel - 1) / panel;
       const unsigned stride = panel * (kChunk * 2) + 16;             // bytes of a row's piece; 16 rows begin in different banks
-      float* scales = (float*)(lds + live * P * stride);             // [chunk][row]
+      float* scales = (float*)(lds + live * P * stride);             // [row][chunk]
       int begin = -1;                                                // of what is held, in chunks
       bool fresh = true;                                             // no weights are on their way
       auto hold = [&](int from) __attribute__((always_inline)) {
         begin = from;
         __syncthreads();
-        const int units = min(panel, chunks - begin) * (kChunk / 8), total = live * units;
+        constexpr int kSame = READY ? P : 1;                         // rows made ready: their pieces like rows of their own
+        const int units = min(panel, chunks - begin) * (kChunk / 8), total = kSame * live * units;
         const float reciprocal = 1.0f / (float)units;
 #pragma clang loop unroll(disable)
-        for (int done = 0; done < total; done += 2 * kThreads) {
+        for (int done = 0; done < total; done += kBatch * kThreads) {
           const int at0 = done + threadIdx.x;
-          v4u got[2][X == kXF32 ? 2 : 1];
-          float scale[2];
-          int r[2], u[2];
+          v4u got[kBatch][X == kXF32 ? 2 : 1];
+          float scale[kBatch];
+          int r[kBatch], u[kBatch];
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
+          for (int b = 0; b < kBatch; ++b) {
             const int unit = min(at0 + b * kThreads, total - 16 + (int)(threadIdx.x & 15));    // 16 lanes have a chunk of a row
             r[b] = quotient(unit, reciprocal), u[b] = unit - r[b] * units;
-            const int c = begin + u[b] / 16, k = min(start_of(c) + u[b] % 16 * 8, k_all - 8);
+            const int c = begin + u[b] / 16;
+            if constexpr (READY) {
+              const int p = P > 1 && r[b] >= live;
+              const int64_t chunk = ((int64_t)source[r0 + r[b] - p * live] + (p ? a.all_rows : 0)) * chunks + c;
+              got[b][0] = *(const v4u*)(a.half + chunk * kChunk + u[b] % 16 * 8);
+              if (u[b] % 16 == 0 && !p) scale[b] = a.factor[chunk];
+              continue;
+            }
+            const int k = min(start_of(c) + u[b] % 16 * 8, k_all - 8);
             const int64_t row = source[r0 + r[b]], from = row * k_all + k;
             if constexpr (X == kXF32) {
               const float* p = (DOWN ? (const float*)a.h : (const float*)a.x) + from;
               got[b][0] = *(const v4u*)p, got[b][1] = *(const v4u*)(p + 4);
             } else if constexpr (X == kXBf16) {
               got[b][0] = *(const v4u*)((const __bf16*)a.x + from);
-            } else {
+            } else if constexpr (X == kXE4m3) {
               const v2u v = *(const v2u*)((const uint8_t*)a.x + from);
               got[b][0] = v4u{v[0], v[1], 0, 0};
               scale[b] = a.x_scale[row * a.x_scales + (a.x_scales > 1 ? c : 0)];
@@ -251,39 +325,22 @@ __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
           }
           if (fresh) load_all(), fresh = false;      // behind the first rows, which are needed first
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const int c = begin + u[b] / 16, k = start_of(c) + u[b] % 16 * 8;
-            const bool in = k >= c * kChunk && k < k_all;            // otherwise it counts in another chunk
-            h8 out[P];
-            if constexpr (X == kXE4m3) {
-              each<4>([&](auto pp) {
-                constexpr int Q = decltype(pp)::value;
-                const h2 v = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)got[b][0][Q / 2], 1.0f, Q % 2 == 1);
-                out[0][2 * Q] = v[0];
-                out[0][2 * Q + 1] = v[1];
-              });
+          for (int b = 0; b < kBatch; ++b) {
+            if constexpr (READY) {
+              if (at0 + b * kThreads >= total) continue;
+              *(v4u*)(lds + (unsigned)r[b] * stride + u[b] * 16) = got[b][0];
+              if (u[b] % 16 == 0 && r[b] < live) scales[r[b] * panel + u[b] / 16] = scale[b];
             } else {
-              float v[8];
+              const int c = begin + u[b] / 16, k = start_of(c) + u[b] % 16 * 8;
+              const bool in = k >= c * kChunk && k < k_all;          // otherwise it counts in another chunk
+              h8 out[P];
+              make_ready<X, P>(got[b], in, out, scale[b]);
+              if (at0 + b * kThreads >= total) continue;
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                v[e] = X == kXF32 ? __uint_as_float(got[b][e / 4][e % 4]) : __uint_as_float(e % 2 ? got[b][0][e / 2] & 0xFFFF0000u : got[b][0][e / 2] << 16);
-              unsigned most = 0;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(v[e]) & 0x7FFFFFFFu);
-              const int top = min(max((int)(row_max(in ? most : 0) >> 23), 1), 254);   // beside an infinity, what is finite stays so
-              scale[b] = __builtin_ldexpf(1.0f, top - 141);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float y = __builtin_ldexpf(v[e], 141 - top);
-                out[0][e] = (_Float16)y;
-                if constexpr (P == 2) out[1][e] = y == (float)out[0][e] ? (_Float16)0.0f : (_Float16)(y - (float)out[0][e]);
-              }
+              for (int p = 0; p < P; ++p)
+                *(v4u*)(lds + (unsigned)(p * live + r[b]) * stride + u[b] * 16) = in ? __builtin_bit_cast(v4u, out[p]) : v4u{0, 0, 0, 0};
+              if (u[b] % 16 == 0) scales[r[b] * panel + u[b] / 16] = scale[b];
             }
-            if (at0 + b * kThreads >= total) continue;
-#pragma unroll
-            for (int p = 0; p < P; ++p)
-              *(v4u*)(lds + (unsigned)(p * live + r[b]) * stride + u[b] * 16) = in ? __builtin_bit_cast(v4u, out[p]) : v4u{0, 0, 0, 0};
-            if (u[b] % 16 == 0) scales[u[b] / 16 * live + r[b]] = scale[b];
           }
         }
         __syncthreads();
@@ -291,7 +348,16 @@ __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
       v4f acc[MT];
 #pragma unroll
       for (int t = 0; t < MT; ++t) acc[t] = v4f{0, 0, 0, 0};
-      auto multiply = [&](const v4u& nib, int u, int c) __attribute__((always_inline)) {
+      // the rows of this lane, as places in LDS
+      int x_at[MT], s_at[MT];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const int row = min(16 * t + i, live - 1);
+        x_at[t] = row * stride + quarter * 64, s_at[t] = row * panel;
+      }
+      // chunk u of a step that begins `c` chunks into what is held
+      auto multiply = [&](const v4u& nib, auto uu, int c) __attribute__((always_inline)) {
+        constexpr int u = decltype(uu)::value;
         const h2 scale = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)*(const uint16_t*)&codes[wave][u / 4][i][8 * (u % 4) + 2 * quarter], 1.0f, false);
         h8 f[4];
         each<4>([&](auto st) __attribute__((always_inline)) {
@@ -307,14 +373,13 @@ __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
           if (MT > 1 && t > 0 && 16 * t >= live) break;
-          const int row = min(16 * t + i, live - 1);
-          const char* from = lds + (unsigned)(c - begin) * (kChunk * 2) + (row * stride + quarter * 64);
+          const char* from = lds + (x_at[t] + c * (kChunk * 2)) + u * (kChunk * 2);
           v4f sum = {0, 0, 0, 0};
 #pragma unroll
           for (int p = 0; p < P; ++p)
 #pragma unroll
             for (int s = 0; s < 4; ++s) sum = mfma(f[s], __builtin_bit_cast(h8, *(const v4u*)(from + p * live * stride + s * 16)), sum);
-          acc[t] += scales[(c - begin) * live + row] * sum;
+          acc[t] += *(scales + (s_at[t] + c) + u) * sum;
         }
       };
       int group = 0, step = 0;
@@ -331,11 +396,11 @@ __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
           load_code(p, s);
         }
         const int c = (now * a.split + ks) * a.each;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (u < a.each && c + u < chunks) multiply(w.nib[u], u, c + u);
+        each<U>([&](auto uu) __attribute__((always_inline)) {
+          constexpr int u = decltype(uu)::value;
+          if (u < a.each && c + u < chunks) multiply(w.nib[u], uu, c - begin);
           load_nib(p, u);
-        }
+        });
         if (!last) continue;
         const int tile = (first + group) * together + mine;
         const bool own = tile < tiles && ks == 0;
@@ -423,7 +488,8 @@ __global__ __launch_bounds__(256) void k_experts_sum(const Args a) {
 }
 
 struct Layout {
-  int64_t slots, chunks, hits, plan, h, part, all;                   // chunks of tokens; bytes
+  int64_t slots, chunks, hits, plan, h, half, factor, part, all;     // chunks of tokens; bytes
+  bool many;                                  // rows are made ready first
 };
 Layout layout(const MoeView& v) {
   Layout l{};
@@ -434,7 +500,13 @@ Layout layout(const MoeView& v) {
   l.plan = up(l.slots * l.chunks * kPlan * 4);
   l.h = up(v.tokens * v.topk * v.inner * 4);
   l.part = v.tokens * v.topk * v.hidden * 4;
-  l.all = l.hits + l.plan + l.h + l.part;
+  l.many = v.tokens > 16 && v.tokens * v.topk > 4 * v.experts && v.hidden >= kChunk && v.inner >= kChunk;
+  if (l.many) {
+    const int64_t x = v.tokens * ((v.hidden + kChunk - 1) / kChunk), h = v.tokens * v.topk * ((v.inner + kChunk - 1) / kChunk);
+    l.half = up(std::max(x, h) * kChunk * 2 * (v.x_type == kXF32 ? 2 : 1));
+    l.factor = up(std::max(x, h) * 4);
+  }
+  l.all = l.hits + l.plan + l.h + l.half + l.factor + l.part;
   return l;
 }
 
@@ -452,6 +524,7 @@ hipError_t go(const MoeView& v, Args a, const Layout& l, hipStream_t stream) {
   a.each = (int)((chunks + steps * a.split - 1) / (steps * a.split));
   while (fits(a.each * a.split, shared) < most) --a.each;
   a.rows = (int)std::min<int64_t>(16 * MT, fits(a.each * a.split, shared) / 16 * 16);
+  if (X == kXHalf) a.all_rows = DOWN ? v.tokens * v.topk : v.tokens;
   if (a.rows < 16) a.rows = (int)most;        // fewer than 16 tokens
   a.budget = (int)((lds - (shared ? kWaves * 1024 : 0)) / 16 * 16);
   const int64_t groups = (tiles + kWaves / a.split - 1) / (kWaves / a.split);
@@ -460,13 +533,18 @@ hipError_t go(const MoeView& v, Args a, const Layout& l, hipStream_t stream) {
   return launch_kernel(k_experts<X, P, DOWN, MT, U>, grid, dim3(kThreads), (size_t)(a.budget + (DOWN ? 0 : kTokens * 2 * v.topk) + (shared ? kWaves * 1024 : 0)), stream, a);
 }
 
-// Up to 16 tokens one row tile, more two or, where experts have many rows each, four.
 template <int X, int P, bool DOWN>
 hipError_t go_rows(const MoeView& v, const Args& a, const Layout& l, hipStream_t stream) {
-  constexpr int kMost = P == 1 ? 4 : 2;       // row tiles whose 4 chunks LDS holds
-  if ((DOWN ? v.inner : v.hidden) < kChunk) return v.tokens <= 16 ? go<X, P, DOWN, 1, 1>(v, a, l, stream) : go<X, P, DOWN, kMost, 1>(v, a, l, stream);
-  if (v.tokens <= 16) return go<X, P, DOWN, 1, 4>(v, a, l, stream);
-  return v.tokens * v.topk <= 4 * v.experts ? go<X, P, DOWN, P == 1 ? 2 : 1, 4>(v, a, l, stream) : go<X, P, DOWN, kMost, 4>(v, a, l, stream);
+  if (l.many) {                               // experts have many rows each
+    const int64_t rows = DOWN ? v.tokens * v.topk : v.tokens, k = DOWN ? v.inner : v.hidden, blocks = (rows * ((k + kChunk - 1) / kChunk) + 15) / 16;
+    if (blocks >= int64_t(1) << 24) return hipErrorInvalidConfiguration;
+    k_rows<X, P><<<dim3((unsigned)blocks), dim3(256), 0, stream>>>(DOWN ? a.h : a.x, a.x_scale, a.x_scales, a.half, a.factor, rows, (int)k);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    return go<kXHalf, P, DOWN, P == 1 ? 4 : 2, 4>(v, a, l, stream);
+  }
+  if ((DOWN ? v.inner : v.hidden) < kChunk) return v.tokens <= 16 ? go<X, P, DOWN, 1, 1>(v, a, l, stream) : go<X, P, DOWN, 2, 1>(v, a, l, stream);
+  return v.tokens <= 16 ? go<X, P, DOWN, 1, 4>(v, a, l, stream) : go<X, P, DOWN, 2, 4>(v, a, l, stream);
 }
 
 hipError_t go_all(const MoeView& v, Args a, const Layout& l, hipStream_t stream) {
@@ -501,7 +579,9 @@ hipError_t launch_moe(const MoeView& v, void* work, hipStream_t stream) {
   a.hits = (int*)work;
   a.plan = (int*)((char*)work + l.hits);
   a.h = (float*)((char*)work + l.hits + l.plan);
-  a.part = (float*)((char*)work + l.hits + l.plan + l.h);
+  a.half = (_Float16*)((char*)work + l.hits + l.plan + l.h);
+  a.factor = (float*)((char*)work + l.hits + l.plan + l.h + l.half);
+  a.part = (float*)((char*)work + l.hits + l.plan + l.h + l.half + l.factor);
   a.y = v.y;
   a.tokens = v.tokens;
   a.hidden = (int)v.hidden;
