@@ -253,6 +253,9 @@ __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
 #pragma unroll
       for (int u = 0; u < U; ++u) load_nib(p, u);
     };
+    // few rows come soon enough behind the first weights; many are asked for first (32 tokens 113 us with the weights first)
+    bool fresh = MT > 1;                      // no weights are on their way
+    if constexpr (MT == 1) load_all();
     __syncthreads();                          // the rows before have been used
     int n;
     if constexpr (DOWN) {
@@ -285,7 +288,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
       const unsigned stride = panel * (kChunk * 2) + 16;             // bytes of a row's piece; 16 rows begin in different banks
       float* scales = (float*)(lds + live * P * stride);             // [row][chunk]
       int begin = -1;                                                // of what is held, in chunks
-      bool fresh = true;                                             // no weights are on their way
+      fresh = fresh || r0 > 0;
       auto hold = [&](int from) __attribute__((always_inline)) {
         begin = from;
         __syncthreads();
@@ -516,9 +519,12 @@ hipError_t go(const MoeView& v, Args a, const Layout& l, hipStream_t stream) {
   const int64_t lds = kLds - 1536 - kWaves * 512 * ((U + 3) / 4) - (DOWN ? 0 : kTokens * 2 * v.topk), most = std::min<int64_t>(v.tokens, 16);
   // rows whose chunks of a step LDS holds
   auto fits = [&](int64_t turn, bool shared) { return (lds - (shared ? kWaves * 1024 : 0)) / (P * (turn * kChunk * 2 + 16) + 4 * turn); };
-  // waves that share k, so that some 4000 waves have work
+  // Waves that share k: until some 1500 have work, or all that are resident where each would still take 6000 elements of k.  One token of
+  // ten experts of 1280x2560 and 2560x640 22.1 us, 23.3 with 2048 or 3000 waves, 24.9 with 4096; eight of 4096x12288 with 61 tokens 236 with
+  // all resident, 246 without.
+  auto more = [&](int64_t waves) { return waves < 1536 || (waves < kResident * kWaves && chunks / a.split >= 48); };
   a.split = 1;
-  while (a.split < kWaves && 2 * a.split <= chunks && l.slots * tiles * a.split < kResident * kWaves && fits(2 * a.split, true) >= most) a.split *= 2;
+  while (a.split < kWaves && 2 * a.split <= chunks && more(l.slots * tiles * a.split) && fits(2 * a.split, true) >= most) a.split *= 2;
   const bool shared = a.split > 1;
   const int64_t steps = (chunks + U * a.split - 1) / (U * a.split);
   a.each = (int)((chunks + steps * a.split - 1) / (steps * a.split));
