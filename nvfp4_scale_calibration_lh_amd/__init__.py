@@ -703,19 +703,15 @@ def lh_cache_extend(block_table: torch.Tensor, lengths: torch.Tensor, new_tokens
         slots = _empty(max_tokens, dtype=torch.int64, device=device)
     else:
         _need(slots, "slots", (max_tokens,), torch.int64)
-    given = (positions, sequence, offsets, new_lengths, new_count)
     sizes = (max_tokens, max_tokens, batch + 1, batch, 1)
-    if any(t is None for t in given):       # one allocation for all that are wanted
-        made = _empty(sum(n for n, t in zip(sizes, given) if t is None), dtype=i32, device=device)
-        made = iter(made.split_with_sizes([n for n, t in zip(sizes, given) if t is None]))
-    out = []
-    for name, n, t in zip(("positions", "sequence", "offsets", "new_lengths", "new_count"), sizes, given):
-        if t is None:
-            t = next(made)
-        else:
-            _need(t, name, (n,), i32)
-        out.append(t)
-    positions, sequence, offsets, new_lengths, new_count = out
+    if positions is None and sequence is None and offsets is None and new_lengths is None and new_count is None:     # one allocation for all
+        positions, sequence, offsets, new_lengths, new_count = _empty(2 * (max_tokens + batch + 1), dtype=i32, device=device).split_with_sizes(sizes)
+    else:
+        given = (positions, sequence, offsets, new_lengths, new_count)
+        for name, n, t in zip(("positions", "sequence", "offsets", "new_lengths", "new_count"), sizes, given):
+            if t is not None:
+                _need(t, name, (n,), i32)
+        positions, sequence, offsets, new_lengths, new_count = (_empty(n, dtype=i32, device=device) if t is None else t for n, t in zip(sizes, given))
     nbytes = 0
     if workspace is not None:
         _need(workspace, "workspace", dtype=torch.uint8)

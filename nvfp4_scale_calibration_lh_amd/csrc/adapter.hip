@@ -21,7 +21,7 @@ constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kMaxParts = 8;                 // workgroups that share k
 constexpr int kRanks = 64;                   // of one workgroup of the first kernel
-constexpr int kGroups = 768;                 // workgroups of the second kernel: three a compute unit are resident
+constexpr int kGroups = 896;                 // workgroups of the second kernel (768 37.1 us, 1024 36.7, 1280 37.9, 512 41.8 against 36.0)
 constexpr int kCopy = 2048;                  // channels that a workgroup copies of a row without adapter
 
 struct Args {
@@ -205,9 +205,9 @@ __global__ __launch_bounds__(kThreads) void k_adapter_in(const Args a) {
   }
 }
 
-// RK: steps of 32 ranks; NT: 16-channel tiles a wave takes at a time; P: bf16 pieces of u.  A workgroup makes its adapter's u once and takes
-// several steps of channels, the weights and the base of the next on their way.
-template <bool YF32, bool WF32, int RK, int NT>
+// RK: steps of 32 ranks; P: bf16 pieces of u.  A workgroup makes its adapter's u once and takes several steps of channels, 16 a wave, the
+// weights and the base of the next on their way (32 channels a wave measured 37.8 us instead of 36 for 96 rows over 64 adapters).
+template <bool YF32, bool WF32, int RK>
 __global__ __launch_bounds__(kThreads) void k_adapter_out(const Args a) {
   constexpr int P = WF32 ? 1 : (YF32 ? 3 : 2);
   constexpr int kWide = 32 * RK + 8;         // a row of u in LDS, so that 16 rows lie in different banks
@@ -235,7 +235,7 @@ __global__ __launch_bounds__(kThreads) void k_adapter_out(const Args a) {
     return;
   }
   // the steps of all adapters of these chunks, shared out evenly
-  constexpr int kStep = 16 * NT * kWaves;    // channels of a step
+  constexpr int kStep = 16 * kWaves;    // channels of a step
   int upto = lane < chunks ? a.hits[chunk0 + lane] : 0;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
@@ -253,17 +253,14 @@ __global__ __launch_bounds__(kThreads) void k_adapter_out(const Args a) {
     const int chunk = __ffsll((unsigned long long)__ballot(upto > hit)) - 1, slot = hit - (chunk > 0 ? __builtin_amdgcn_readlane(upto, chunk - 1) : 0);
     const int* plan = a.plan + ((int64_t)(chunk0 + chunk) * a.slots + slot) * kPlan;
     const int adapter = __builtin_amdgcn_readfirstlane(plan[0]), n = __builtin_amdgcn_readfirstlane(plan[1]), ranks = __builtin_amdgcn_readfirstlane(plan[2]);
-    v4u next[NT][kUnits];
+    v4u next[kUnits];
     auto load_w = [&](int step) __attribute__((always_inline)) {
+      const int64_t at = ((int64_t)adapter * a.cout + min(step * kStep + wave * 16 + i, a.cout - 1)) * a.rank;
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int64_t at = ((int64_t)adapter * a.cout + min(step * kStep + (wave * NT + j) * 16 + i, a.cout - 1)) * a.rank;
-#pragma unroll
-        for (int s = 0; s < kUnits; ++s) {
-          if (s > 0 && s * 4 * kEach >= ranks) break;
-          const int k = min((s * 4 + quarter) * kEach, a.rank - kEach);
-          next[j][s] = WF32 ? *(const v4u*)((const float*)a.b + at + k) : *(const v4u*)((const __bf16*)a.b + at + k);
-        }
+      for (int s = 0; s < kUnits; ++s) {
+        if (s > 0 && s * 4 * kEach >= ranks) break;
+        const int k = min((s * 4 + quarter) * kEach, a.rank - kEach);
+        next[s] = WF32 ? *(const v4u*)((const float*)a.b + at + k) : *(const v4u*)((const __bf16*)a.b + at + k);
       }
     };
     load_w(s0);
@@ -296,71 +293,59 @@ __global__ __launch_bounds__(kThreads) void k_adapter_out(const Args a) {
       }
       __syncthreads();
       if (r0 > 0) load_w(s0);
-      four_t soon[NT];                          // base of the first 16 rows, with the weights
-      auto load_base = [&](four_t (&to)[NT], int t, int step) __attribute__((always_inline)) {
+      four_t soon;                              // base of the first 16 rows, with the weights
+      auto load_base = [&](four_t& to, int t, int step) __attribute__((always_inline)) {
         const int64_t row = rows[r0 + min(t + i, live - 1)];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) to[j] = *(const four_t*)(base + row * a.cout + min(step * kStep + (wave * NT + j) * 16 + 4 * quarter, a.cout - 4));
+        to = *(const four_t*)(base + row * a.cout + min(step * kStep + wave * 16 + 4 * quarter, a.cout - 4));
       };
       if (whole) load_base(soon, 0, s0);
       for (int step = s0; step < s1; ++step) {
-        const int c0 = step * kStep + wave * NT * 16;
-        four_t old[NT];
+        const int c = step * kStep + wave * 16 + 4 * quarter;
+        four_t old = soon;
+        asm volatile("" : "+v"(old));           // waits for these loads here, before the next are issued, not behind those
+        v4u w[kUnits];                          // what is past the adapter's rank counts as 0
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          old[j] = soon[j];
-          asm volatile("" : "+v"(old[j]));
-        }
-        v4u w[NT][kUnits];                      // what is past the adapter's rank counts as 0
+        for (int s = 0; s < kUnits; ++s) {
+          const int left = ranks - (s * 4 + quarter) * kEach;
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int s = 0; s < kUnits; ++s) {
-            const int left = ranks - (s * 4 + quarter) * kEach;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if constexpr (WF32)
-                w[j][s][e] = e < left ? next[j][s][e] : 0u;
-              else
-                w[j][s][e] = 2 * e + 1 < left ? next[j][s][e] : (2 * e < left ? next[j][s][e] & 0xFFFFu : 0u);
-            }
-            asm volatile("" : "+v"(w[j][s]));
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (WF32)
+              w[s][e] = e < left ? next[s][e] : 0u;
+            else
+              w[s][e] = 2 * e + 1 < left ? next[s][e] : (2 * e < left ? next[s][e] & 0xFFFFu : 0u);
           }
+          asm volatile("" : "+v"(w[s]));
+        }
         if (step + 1 < s1) {
           load_w(step + 1);
           if (whole) load_base(soon, 0, step + 1);
         }
         for (int t = 0; t < live; t += 16) {
           if (t > 0 && whole) load_base(old, t, step);
+          v4f acc = {0, 0, 0, 0};
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            v4f acc = {0, 0, 0, 0};
+          for (int s = 0; s < kUnits; ++s)
 #pragma unroll
-            for (int s = 0; s < kUnits; ++s)
+            for (int p = 0; p < P; ++p) {
+              const v4u u = *(const v4u*)&us[p][min(t + i, live - 1)][(s * 4 + quarter) * kEach];
+              if constexpr (WF32) {
 #pragma unroll
-              for (int p = 0; p < P; ++p) {
-                const v4u u = *(const v4u*)&us[p][min(t + i, live - 1)][(s * 4 + quarter) * kEach];
-                if constexpr (WF32) {
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) acc = mfma_f32(__uint_as_float(w[j][s][e]), __uint_as_float(u[e]), acc);
-                } else {
-                  acc = mfma(__builtin_bit_cast(b8, w[j][s]), __builtin_bit_cast(b8, u), acc);
-                }
+                for (int e = 0; e < 4; ++e) acc = mfma_f32(__uint_as_float(w[s][e]), __uint_as_float(u[e]), acc);
+              } else {
+                acc = mfma(__builtin_bit_cast(b8, w[s]), __builtin_bit_cast(b8, u), acc);
               }
-            if (t + i >= live) continue;
-            const int c = c0 + 16 * j + 4 * quarter;
-            const int64_t at = (int64_t)rows[r0 + t + i] * a.cout + c;
-            if (whole) {
-              if (c >= a.cout) continue;
-              four_t v;
-#pragma unroll
-              for (int r = 0; r < 4; ++r) v[r] = (T)((float)old[j][r] + acc[r]);
-              *(four_t*)(y + at) = v;
-            } else {
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-                if (c + r < a.cout) y[at + r] = (T)((float)base[at + r] + acc[r]);
             }
+          if (t + i >= live || c >= a.cout) continue;
+          const int64_t at = (int64_t)rows[r0 + t + i] * a.cout + c;
+          if (whole) {
+            four_t v;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = (T)((float)old[r] + acc[r]);
+            *(four_t*)(y + at) = v;
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (c + r < a.cout) y[at + r] = (T)((float)base[at + r] + acc[r]);
           }
         }
       }
@@ -391,22 +376,22 @@ hipError_t go_in(const Args& a, const Layout& l, hipStream_t stream) {
   return launch_kernel(k_adapter_in<X, WF32, 4>, grid, dim3(kThreads), 0, stream, a);
 }
 
-template <bool YF32, bool WF32, int RK, int NT>
+template <bool YF32, bool WF32, int RK>
 hipError_t go_out(Args a, const Layout& l, hipStream_t stream) {
-  const int64_t steps = (a.cout + 16 * NT * kWaves - 1) / (16 * NT * kWaves), chunks = std::min<int64_t>(l.chunks, 64);
+  const int64_t steps = (a.cout + 16 * kWaves - 1) / (16 * kWaves), chunks = std::min<int64_t>(l.chunks, 64);
   if (l.slots * chunks * steps >= int64_t(1) << 31) return hipErrorInvalidConfiguration;
   a.groups = (int)std::min<int64_t>(l.slots * chunks * steps, kGroups);
   const int64_t n = a.groups + (a.in_place ? 0 : (a.cout + kCopy - 1) / kCopy * chunks);
   if (n >= int64_t(1) << 24) return hipErrorInvalidConfiguration;
-  return launch_kernel(k_adapter_out<YF32, WF32, RK, NT>, dim3((unsigned)n, (unsigned)((l.chunks + 63) / 64)), dim3(kThreads), 0, stream, a);
+  return launch_kernel(k_adapter_out<YF32, WF32, RK>, dim3((unsigned)n, (unsigned)((l.chunks + 63) / 64)), dim3(kThreads), 0, stream, a);
 }
 
 template <bool YF32, bool WF32>
 hipError_t go_rank(const Args& a, const Layout& l, hipStream_t stream) {
-  if (a.rank <= 32) return go_out<YF32, WF32, 1, 2>(a, l, stream);
-  if (a.rank <= 64) return go_out<YF32, WF32, 2, 2>(a, l, stream);
-  if (a.rank <= 128) return go_out<YF32, WF32, 4, 1>(a, l, stream);
-  return go_out<YF32, WF32, 8, 1>(a, l, stream);
+  if (a.rank <= 32) return go_out<YF32, WF32, 1>(a, l, stream);
+  if (a.rank <= 64) return go_out<YF32, WF32, 2>(a, l, stream);
+  if (a.rank <= 128) return go_out<YF32, WF32, 4>(a, l, stream);
+  return go_out<YF32, WF32, 8>(a, l, stream);
 }
 
 }  // namespace
