@@ -552,7 +552,8 @@ lh_status lh_rotary(const void* Q, int64_t q_stride, int64_t n_q_heads, const vo
  * (lh_moe skips those).  Where m is +infinity, the logits equal to it count as 1 and all others as 0.
  * logits [tokens, n_experts] of dtype; ids [tokens, topk] int32, weights [tokens, topk] fp32.  Sums are fp32.
  * Errors: UNSUPPORTED for an unknown dtype; INVALID_ARGUMENT for tokens outside [0, 2^31-1], n_experts outside [1, 4096], topk
- * outside [1, 64] or over n_experts, a scale that is not finite, NULL required pointers, non-device or mixed-device pointers.
+ * outside [1, 64] or over n_experts, a scale that is not finite, a launch of 2^32 or more work-items (64 a token), NULL required
+ * pointers, non-device or mixed-device pointers.
  */
 lh_status lh_route(const void* logits, lh_dtype dtype, int64_t tokens, int64_t n_experts, int64_t topk,
                    int32_t renormalize, float scale, int32_t* ids, float* weights, void* stream);
@@ -566,11 +567,13 @@ lh_status lh_route(const void* logits, lh_dtype dtype, int64_t tokens, int64_t n
  * inner/16], down_fp4 [n_experts, hidden, inner/2] (both fp4 8-byte aligned), amax [n_experts] each, scale_norm as in
  * lh_sweep_options.  ids and weights [tokens, topk] int32 and fp32, as lh_route gives them.
  * X [tokens, hidden], x_scale and x_group as in lh_matvec; Y [tokens, hidden] F32 for F32 rows, BF16 otherwise.
- * Weights and rows enter exactly (fp32 elements as in lh_matvec); what comes between the two products is held to 2^-17 of itself
- * (fp32 rows: 2^-24); sums are fp32, in a fixed order, and Y is rounded once.  Infinities and NaN in a row give what the formula
+ * Weights enter exactly, and so do E4M3 rows and their scales.  Of each 128 elements of other rows with the largest magnitude m, BF16
+ * ones enter exactly from 2^-31 m on and to within 2^-39 m below, F32 ones to within 2^-23 of themselves and 2^-39 m.  What comes between the two
+ * products is held to 2^-11 of itself (F32 rows: 2^-23) and 2^-39 of the largest of its 128.  Sums are fp32, in a fixed order; the
+ * routing weights multiply the rows of the second product, and Y is rounded once.  Infinities and NaN in a row give what the formula
  * gives in that row's Y and change no other row.
- * Any number of tokens works; the weights of an expert are read again for every 64 tokens, and among those for every 16 rows of it
- * (32 where tokens > 16 and tokens * topk > 4 * n_experts).
+ * Any number of tokens works; the weights of an expert are read again for every 64 tokens, and among those for every 32 rows of it (16
+ * with up to 16 tokens; up to 64 of rows that are not F32, where tokens > 16, tokens * topk > 4 * n_experts, and hidden and inner >= 128).
  * workspace: device memory of at least lh_moe_workspace bytes (16-byte aligned) that no other call uses until this one has run.
  * Errors: UNSUPPORTED for an unknown dtype; INVALID_ARGUMENT for tokens outside [0, 4194240], hidden or inner < 1, over 2^24
  * or not multiples of 16, hidden * inner over 2^32, n_experts outside [1, 4096], topk outside [1, 64], scale_norm that is not a
@@ -596,9 +599,10 @@ int64_t lh_moe_workspace(lh_dtype x_dtype, int64_t tokens, int64_t hidden, int64
  * NULL: all have `rank`.  scaling [n_adapters] fp32 or NULL (1).  index [rows] int32.
  * X [rows, cin], x_scale and x_group as in lh_matvec; base and Y [rows, cout], F32 for F32 rows, BF16 otherwise; Y may be base.
  * Products of BF16 weights are exact (fp32 elements as in lh_matvec), those of F32 weights fp32 (E4M3 elements are then multiplied by
- * their scale first); A_a x_t is held to 2^-17 of itself with BF16 weights and Y, otherwise to 2^-24; sums are fp32, in a
+ * their scale first); A_a x_t is held to 2^-16 of itself with BF16 weights and Y, otherwise to 2^-24; sums are fp32, in a
  * fixed order, and Y is rounded once.  Infinities and NaN in a row change no other row.
- * The weights of an adapter are read again for every 64 rows, and A for every 16 rows of an adapter among those.
+ * The weights of an adapter are read again for every 64 rows, and among those A for every 16 rows of it, and B for every 32 where rank
+ * is over 64 and every 16 where it is over 128.
  * workspace: device memory of at least lh_adapter_workspace bytes (16-byte aligned) that no other call uses until this one has run.
  * Errors: UNSUPPORTED for an unknown dtype; INVALID_ARGUMENT for rows outside [0, 4194240], cin <= 0, over 2^24 or not a multiple of
  * 16, cout outside [0, 2^24], n_adapters outside [1, 4096], rank outside [8, 256] or not a multiple of 8, x_scale or x_group that do

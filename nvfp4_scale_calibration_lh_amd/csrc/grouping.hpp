@@ -10,7 +10,8 @@ namespace {
 
 constexpr int kTokens = 64;                  // rows of one pass over the weights: one a lane
 
-// What a first kernel leaves of a slot for a second: the matrix, its number of rows (0: none) and the rows (experts: choices, token * topk + j).
+// What a first kernel leaves of a slot for a second: the matrix, its number of rows, (adapters) its rank, one unused, and the rows (experts: choices,
+// token * topk + j).
 constexpr int kPlan = 4 + kTokens;
 
 __device__ inline uint64_t lane_of(uint64_t v, int lane) {

@@ -1,7 +1,10 @@
 // A mixture-of-experts layer for a few tokens, on NVFP4 expert weights as the scale sweep leaves them:
 //   y[t] = sum_j w[t, j] D_e (silu(G_e x[t]) * U_e x[t]),  e = ids[t, j],  silu(g) = g / (1 + exp(-g))
 //
-// Bound by reading the weights of every expert that is hit once (0.5625 bytes each).  Three kernels:
+// Bound by reading the weights of every expert that is hit once (0.5625 bytes each).  Ten experts of 1280x2560 and 2560x640 for one token 22 us
+// (28 MB: three launches, each with its cold instructions, and the tail of the last weights); 32 tokens that hit 125 of 512 such experts 107 us (346 MB at 3.3 TB/s);
+// 61 tokens over eight experts of 24576x4096 and 4096x12288 236 us (680 MB at 2.9 TB/s; 122 rows, whose products and staging
+// share the wave slots with the loads).  Three kernels:
 //   gate and up  the channels of all experts that (up to 64) tokens hit, in tiles, are shared out evenly over as many workgroups as
 //                are resident; each finds the experts of its share and their rows from the ids by itself.  A wave has 8 gate rows
 //                and the 8 up rows that belong to them as one 16-row operand, so that silu(g) * u needs no other wave.
@@ -14,7 +17,8 @@
 // A weight's E2M1 value times its block's E4M3 scale has at most 6 significant bits in [2^-10, 2688], exact in fp16.  Rows are fp16
 // with a factor for each 128 elements: E4M3 values exactly, with the scale they came with; bf16 and fp32 times the power of two that
 // takes the largest of the 128 to [2^14, 2^15), fp32 in two pieces: bf16 exactly from 2^-31 of that largest element on and to within
-// 2^-39 of it below, fp32 to 2^-23 of itself and 2^-39 of the largest.  Products are exact, sums fp32, in a fixed order.
+// 2^-39 of it below, fp32 to 2^-23 of itself and 2^-39 of the largest.  h takes two pieces where y is fp32; where y is bf16, whose rounding is
+// 2^-8, one (2^-11, eight times finer than that and than h in bf16 would be, at half the products).  Products are exact, sums fp32, in a fixed order.
 #include "grouping.hpp"
 #include "lh_internal.hpp"
 #include "nvfp4_weights.hpp"
@@ -503,6 +507,8 @@ Layout layout(const MoeView& v) {
   l.plan = up(l.slots * l.chunks * kPlan * 4);
   l.h = up(v.tokens * v.topk * v.inner * 4);
   l.part = v.tokens * v.topk * v.hidden * 4;
+  // From four rows an expert on: eight experts of 4096x12288 with two for each of 61 tokens 236 us, 280 without; 64 of 2560x1280 with eight for
+  // each of 40 tokens 125 us, 138 without; with eight for each of 20 87 us, 84 without, and two of the eight wide ones for 17 158 and 157.
   l.many = v.tokens > 16 && v.tokens * v.topk > 4 * v.experts && v.hidden >= kChunk && v.inner >= kChunk;
   if (l.many) {
     const int64_t x = v.tokens * ((v.hidden + kChunk - 1) / kChunk), h = v.tokens * v.topk * ((v.inner + kChunk - 1) / kChunk);
@@ -549,6 +555,8 @@ hipError_t go_rows(const MoeView& v, const Args& a, const Layout& l, hipStream_t
     if (e != hipSuccess) return e;
     return go<kXHalf, P, DOWN, P == 1 ? 4 : 2, 4>(v, a, l, stream);
   }
+  // Up to 16 tokens an expert has at most one tile of rows.  24 tokens over 512 experts of 2560x640 86 us, 100 in tiles of one; 16 tokens 69.5 either
+  // way, 5 tokens over eight wide experts 116.8 us, 117.9 in two.
   if ((DOWN ? v.inner : v.hidden) < kChunk) return v.tokens <= 16 ? go<X, P, DOWN, 1, 1>(v, a, l, stream) : go<X, P, DOWN, 2, 1>(v, a, l, stream);
   return v.tokens <= 16 ? go<X, P, DOWN, 1, 4>(v, a, l, stream) : go<X, P, DOWN, 2, 4>(v, a, l, stream);
 }

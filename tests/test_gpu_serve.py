@@ -317,12 +317,14 @@ def layer_rows(rows, cin, x, group, seed):
 def check_moe(xd, scale, xv, x, group, ids, w, gate_up, down, **kw):
     """Products are exact and sums fp32: a sum of n terms is off by at most (n + 8) roundings of its terms' magnitudes (every element of
     fp32 rows is three terms), which the two products pass on; between them exp, the division and three products.  h is one fp16 number
-    with a factor (2^-12 of itself: y's own rounding is 2^-8), for fp32 rows two (2^-24, and 2^-40 of the largest of 128, as are those rows)."""
+    with a factor: 11 bits, half a step is up to 2^-11 of it.  fp32 rows and their h are two: what the first leaves is at most 2^-11 of
+    the power of two under the number, so its own half step is at most 2^-23 of that power, and never under 2^-25, where the largest of
+    128 is at least 2^14: 2^-39 of that one."""
     y = lh.lh_moe(xd, torch.from_numpy(ids).to(DEV), torch.from_numpy(w).to(DEV), on_gpu(gate_up), on_gpu(down), x_scale=scale, x_group=group, **kw)
     want, terms = serve.moe(xv, ids, w.astype(np.float64), gate_up, down, kw.get("norm", 448.0))
     hidden, inner = xv.shape[1], down[0].shape[2] * 16
     pieces = 3 if x == "f32" else 1
-    rel = (pieces * hidden + 8) * U + (3 * inner + 8) * U + 32 * U + (2.0 ** -23 if x == "f32" else 2.0 ** -12) + ids.shape[1] * U
+    rel = (pieces * hidden + 8) * U + (3 * inner + 8) * U + 32 * U + (2 * 2.0 ** -23 if x == "f32" else 2.0 ** -11) + ids.shape[1] * U
     bound = rel * terms + 2.0 ** -38 * terms.max(1, keepdims=True) + 2.0 ** -120
     bound += HALF["f32" if x == "f32" else "bf16"] * (np.abs(want) + bound)
     got, none = y.double().cpu().numpy(), np.isnan(want)        # a NaN in a row (8 bits of what is over 464) is one in its outputs
@@ -390,6 +392,31 @@ def test_moe_infinities_stay_in_their_rows(x):
     assert bool(torch.isnan(y[1]).all()) and not bool(torch.isfinite(y[4]).all())
 
 
+@pytest.mark.parametrize("x", ["bf16", "f32"])
+def test_moe_infinities_where_experts_have_many_rows(x):
+    note(f"moe infinities, many rows, {x}")
+    gate_up, down = matrices(2, 288, 272, 17), matrices(2, 272, 144, 18)
+    xd, _, _ = layer_rows(40, 272, x, 0, 19)
+    ids, w = choices(40, 2, 2, 20)
+    args = [torch.from_numpy(t).to(DEV) for t in (ids, w)]
+    clean = lh.lh_moe(xd, *args, on_gpu(gate_up), on_gpu(down))
+    bad = xd.clone()
+    bad[1, 5], bad[38, 271] = float("nan"), float("-inf")
+    y = lh.lh_moe(bad, *args, on_gpu(gate_up), on_gpu(down))
+    keep = [t for t in range(40) if t not in (1, 38)]
+    assert torch.equal(y[keep], clean[keep])
+    assert bool(torch.isnan(y[1]).all()) and not bool(torch.isfinite(y[38]).all())
+
+
+def test_moe_most_experts():
+    note("moe 64 of 4096 experts")
+    gate_up, down = matrices(4096, 32, 16, 21), matrices(4096, 16, 16, 22)
+    xd, scale, xv = layer_rows(3, 16, "bf16", 0, 23)
+    ids, w = choices(3, 4096, 64, 24)
+    ids[1, 7], ids[2, 63] = 4095, 0
+    check_moe(xd, scale, xv, "bf16", 0, ids, w, gate_up, down)
+
+
 def test_moe_large_activations():
     """silu far from 0: gates where exp overflows or the weight of the up product is next to nothing."""
     note("moe large activations")
@@ -426,12 +453,13 @@ def adapter_case(rows, cin, cout, n, rank, x, group, weights, seed, ragged=True)
 
 def check_adapter(case, x, group, weights, **kw):
     """Sums of n terms are off by at most (n + 8) roundings of their terms' magnitudes (fp32 elements are three terms each, fp32
-    weights round their products, too), u by its pieces and its scaling, and Y once more by its type."""
+    weights round their products, too), u by its pieces and its scaling, and Y once more by its type.  Of two pieces of 8 bits the first, cut off,
+    leaves under 2^-7 of the power of two under u, and the second is off by half a step of that, 2^-8 of 2^-8: 2^-16."""
     xd, scale, xv, base, a, b, index, ranks, scaling = case
     args = dict(scaling=torch.from_numpy(scaling).to(DEV), ranks=None if ranks is None else dev(ranks), x_scale=scale, x_group=group)
     y = lh.lh_adapter(xd, base, a, b, dev(index), **args, **kw)
     want, terms = serve.adapter(xv, base.double().cpu().numpy(), a.double().cpu().numpy(), b.double().cpu().numpy(), index, scaling, ranks)
-    held = 2.0 ** -24 if x == "f32" or weights == "f32" else 2.0 ** -17
+    held = 2.0 ** -24 if x == "f32" or weights == "f32" else 2.0 ** -16
     rel = (3 * a.shape[2] + 8) * U + (3 * a.shape[1] + 8) * U + 8 * U + held
     none = np.isnan(want)
     np.testing.assert_array_equal(np.isnan(y.double().cpu().numpy()), none)
