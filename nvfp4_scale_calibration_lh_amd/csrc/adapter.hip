@@ -9,8 +9,9 @@
 // one, their scale multiplying the sum of each 128; fp32 in three, u in two or, where y is fp32, three); fp32 weights meet fp32
 // rows.  Products of bf16 weights are exact, sums fp32 in a fixed order; u is held to 2^-16 (2^-24) of itself.
 //
-// One row, rank 16, 4096 to 12288 channels: 7.6 us, two launches.  96 rows over 64 adapters of ranks up to 64: 36 us, in 8 and out 28: the
-// 61 MB that are asked for come as 107, because lines of 128 bytes hold the padding of smaller ranks and the two 64 rows read shared adapters twice.
+// One row, rank 16, 4096 to 12288 channels: 7.7 us, two launches.  96 rows over 64 adapters of ranks up to 64: 29.6 us; the 61 MB that are
+// asked for come as 107, because lines of 128 bytes hold the padding of smaller ranks and the two 64 rows read shared adapters twice.  (128
+// rows at a time: 28.3 us here, but 21 instead of 17.9 where 128 rows share four adapters, and 0.25 us more for one row.)
 #include "grouping.hpp"
 #include "lh_internal.hpp"
 #include "nvfp4_weights.hpp"
@@ -22,10 +23,9 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kMaxParts = 8;                 // workgroups that share k (96 rows: 4 39.7 us, 16 36.8 against 36.1; one row: 8.0, 8.0, 7.6)
+constexpr int kMaxParts = 8;                 // workgroups that share k (96 rows: four 3.6 us more, 16 0.7; one row: 0.4 and 0.4)
 constexpr int kRanks = 64;                   // of one workgroup of the first kernel
-constexpr int kGroups = 896;                 // workgroups of the second kernel (768 37.1 us, 1024 36.7, 1280 37.9, 512 41.8 against 36.0)
-constexpr int kCopy = 2048;                  // channels that a workgroup copies of a row without adapter
+constexpr int kCopy = 2048;                  // channels that a wave copies of a row without adapter
 
 struct Args {
   const void* x;
@@ -208,10 +208,16 @@ __global__ __launch_bounds__(kThreads) void k_adapter_in(const Args a) {
   }
 }
 
+// Workgroups of the second kernel on a compute unit, all resident, as the registers for rk steps of 32 ranks allow.  96 rows over 64 adapters of
+// rank 64: 29.6 us with six; 35 with three, 31.1 with four, 29.9 with five, 29.1 with seven and 35.4 with eight, whose weights spill;
+// 128 rows over four: 17.5, 17.6, 17.9, 18.5 and 20.6 against 17.9.
+template <bool WF32>
+constexpr int resident(int rk) { return rk <= (WF32 ? 1 : 2) ? 6 : (rk <= 2 ? 4 : (rk == 4 ? 3 : 2)); }
+
 // RK: steps of 32 ranks; P: bf16 pieces of u.  A workgroup makes its adapter's u once and takes several steps of channels, 16 a wave, the
-// weights and the base of the next on their way (32 channels a wave measured 37.8 us instead of 36 for 96 rows over 64 adapters).
+// weights and the base of the next on their way (32 channels a wave: 1.8 us more for 96 rows over 64 adapters).
 template <bool YF32, bool WF32, int RK>
-__global__ __launch_bounds__(kThreads) void k_adapter_out(const Args a) {
+__global__ __launch_bounds__(kThreads, resident<WF32>(RK)) void k_adapter_out(const Args a) {
   constexpr int P = WF32 ? 1 : (YF32 ? 3 : 2);
   constexpr int kWide = 32 * RK + 8;         // a row of u in LDS, so that 16 rows lie in different banks
   constexpr int kRows = RK <= 2 ? 64 : (RK == 4 ? 32 : 16);          // rows whose u is held
@@ -226,14 +232,24 @@ __global__ __launch_bounds__(kThreads) void k_adapter_out(const Args a) {
   T* y = (T*)a.y;
   // a workgroup serves up to 64 chunks of 64 rows
   const int chunk0 = (int)blockIdx.y * 64, chunks = (int)min((int64_t)64, (a.rows + kTokens - 1) / kTokens - chunk0);
-  if (blockIdx.x >= (unsigned)a.groups) {                            // rows without an adapter
+  if (blockIdx.x >= (unsigned)a.groups) {                            // rows without an adapter, one a wave
     const int place = blockIdx.x - a.groups, parts = (a.cout + kCopy - 1) / kCopy;
-    const int64_t first = ((int64_t)chunk0 + place / parts) * kTokens;
+    const int64_t row = (int64_t)chunk0 * kTokens + (int64_t)(place / parts) * kWaves + wave;
+    if (row >= a.rows) return;
+    const int id = a.index[row];
+    if (id >= 0 && id < a.adapters) return;
+    constexpr int kUnit = 16 / sizeof(T);
     const int c0 = place % parts * kCopy, c1 = min(c0 + kCopy, a.cout);
-    const int id = first + lane < a.rows ? a.index[first + lane] : 0;
-    for (uint64_t left = __ballot(id < 0 || id >= a.adapters); left; left &= left - 1) {
-      const int64_t at = (first + __ffsll((unsigned long long)left) - 1) * a.cout;
-      for (int c = c0 + threadIdx.x; c < c1; c += kThreads) y[at + c] = base[at + c];
+    const T* from = base + row * a.cout;
+    T* to = y + row * a.cout;
+    if (a.cout % kUnit == 0) {
+#pragma unroll
+      for (int k = 0; k < kCopy; k += 64 * kUnit) {
+        const int c = c0 + k + lane * kUnit;
+        if (c < c1) *(v4u*)(to + c) = *(const v4u*)(from + c);
+      }
+    } else {
+      for (int c = c0 + lane; c < c1; c += 64) to[c] = from[c];
     }
     return;
   }
@@ -383,8 +399,8 @@ template <bool YF32, bool WF32, int RK>
 hipError_t go_out(Args a, const Layout& l, hipStream_t stream) {
   const int64_t steps = (a.cout + 16 * kWaves - 1) / (16 * kWaves), chunks = std::min<int64_t>(l.chunks, 64);
   if (l.slots * chunks * steps >= int64_t(1) << 31) return hipErrorInvalidConfiguration;
-  a.groups = (int)std::min<int64_t>(l.slots * chunks * steps, kGroups);
-  const int64_t n = a.groups + (a.in_place ? 0 : (a.cout + kCopy - 1) / kCopy * chunks);
+  a.groups = (int)std::min<int64_t>(l.slots * chunks * steps, 256 * resident<WF32>(RK));
+  const int64_t n = a.groups + (a.in_place ? 0 : (a.cout + kCopy - 1) / kCopy * ((std::min<int64_t>(chunks * kTokens, a.rows) + kWaves - 1) / kWaves));
   if (n >= int64_t(1) << 24) return hipErrorInvalidConfiguration;
   return launch_kernel(k_adapter_out<YF32, WF32, RK>, dim3((unsigned)n, (unsigned)((l.chunks + 63) / 64)), dim3(kThreads), 0, stream, a);
 }
