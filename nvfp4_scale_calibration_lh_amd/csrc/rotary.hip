@@ -3,8 +3,8 @@
 //   by the token's position times frequency j; pairs are elements (j, j + rot / 2), or (2j, 2j + 1) interleaved.
 //
 // Bound by memory: every element is read and written once.  A thread makes the sine and cosine of its pairs of one
-// token once and takes them through several heads.  One token of 40 heads of 128 bf16 3.4 us, a launch; 8191 tokens 36 us (168 MB at
-// 4.7 TB/s, as a copy); 3001 tokens of 10 heads of 256 fp32, 64 turned, 17 us (61 MB).
+// token once and takes them through several heads.  One token of 40 heads of 128 bf16 3.1 us, a launch; 8191 tokens 34.8 us (168 MB at
+// 4.8 TB/s, as a copy); 3001 tokens of 10 heads of 256 fp32, 64 turned, 12.5 us (61 MB, as a copy).
 //
 // The angle: position * frequency is a product of 31 and 24 bits; it is taken in turns, as a sum of two 64-bit
 // numbers, and reduced to an eighth of a turn there, so that positions up to 2^31 lose nothing.  What is left
@@ -16,8 +16,6 @@
 
 namespace lh {
 namespace {
-
-typedef unsigned v4u __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
 
@@ -64,36 +62,31 @@ __device__ inline void turn(int position, float frequency, float& c, float& s) {
 template <class T>
 __device__ inline float widen(T v) { return (float)v; }
 
-// N neighbouring elements; with V = 8 they are 16-byte aligned.
-template <class T, int N, bool WIDE>
+// N neighbouring elements, aligned to all of them.
+template <class T, int N>
 struct Run {
+  typedef T all_t __attribute__((ext_vector_type(N)));
   T v[N];
   __device__ inline void load(const T* p) {
-    if constexpr (WIDE) {
-      static_assert(N * sizeof(T) % 16 == 0, "whole units");
-      v4u u[N * sizeof(T) / 16];
+    const all_t u = *(const all_t*)p;
 #pragma unroll
-      for (unsigned j = 0; j < N * sizeof(T) / 16; ++j) u[j] = ((const v4u*)p)[j];
-      __builtin_memcpy(v, u, sizeof u);
-    } else {
-#pragma unroll
-      for (int j = 0; j < N; ++j) v[j] = p[j];
-    }
+    for (int j = 0; j < N; ++j) v[j] = u[j];
   }
   __device__ inline void store(T* p) const {
-    if constexpr (WIDE) {
-      v4u u[N * sizeof(T) / 16];
-      __builtin_memcpy(u, v, sizeof u);
+    all_t u;
 #pragma unroll
-      for (unsigned j = 0; j < N * sizeof(T) / 16; ++j) ((v4u*)p)[j] = u[j];
-    } else {
-#pragma unroll
-      for (int j = 0; j < N; ++j) p[j] = v[j];
-    }
+    for (int j = 0; j < N; ++j) u[j] = v[j];
+    *(all_t*)p = u;
   }
 };
+template <class T>
+struct Run<T, 1> {
+  T v[1];
+  __device__ inline void load(const T* p) { v[0] = *p; }
+  __device__ inline void store(T* p) const { *p = v[0]; }
+};
 
-// V pairs a thread: 8 where the halves of a head are whole 16-byte units, otherwise 1.
+// V pairs a thread (with 8, lanes lie apart: the fp32 heads 16.9 us instead of 12.5, interleaved bf16 prompts 38 instead of 34.8): 4 where the halves of what is turned are whole units of 4 elements, otherwise 1.
 template <class T, int V, bool PAIRED>
 __global__ __launch_bounds__(kThreads) void k_rotary(const Args a) {
   const unsigned item = blockIdx.x * kThreads + threadIdx.x, each = a.groups * a.pieces;
@@ -118,7 +111,7 @@ __global__ __launch_bounds__(kThreads) void k_rotary(const Args a) {
     const bool is_q = h < a.q_heads;
     const T* from = is_q ? (const T*)a.q + token * a.q_stride + h * a.dim : (const T*)a.k + token * a.k_stride + (h - a.q_heads) * a.dim;
     T* to = is_q ? (T*)a.qo + token * a.qo_stride + h * a.dim : (T*)a.ko + token * a.ko_stride + (h - a.q_heads) * a.dim;
-    Run<T, V, V == 8> x, y;
+    Run<T, V> x, y;
     x.load(from + at);
     y.load(from + at + apart);
     if (turned) {
@@ -152,10 +145,10 @@ template <class T, int V>
 hipError_t go(Args a, bool paired, hipStream_t stream) {
   a.turning = a.rot / (2 * V);
   a.pieces = a.in_place ? a.turning : a.dim / (2 * V);
-  // A run of heads for each of enough threads to fill the chip, at most 4 heads a thread.  40 heads of 128 bf16, 2048 tokens 9.8 us, 11.7
-  // with twice the threads; 8191 tokens 36, 38 with 8 heads a thread, 39 with one.  fp32 asks for twice the threads: 10 heads of 256, 6000
-  // tokens 34 us, 38 with as many as bf16.
-  constexpr uint64_t kFill = 64 * 2048 * sizeof(T);
+  // A run of heads for each of enough threads to fill the chip, at most 4 heads a thread.  40 heads of 128 bf16, 2048 tokens 9.6 us, 10.2
+  // with twice the threads and 13 with four times; 8191 tokens 34.8 (12000 tokens of 10 heads of 256 28.4, 35 with one head a thread).
+  // fp32 asks for more: 10 heads of 256, 6000 tokens 26.5 us, 29 with half the threads.
+  constexpr uint64_t kFill = 2048 * (sizeof(T) == 2 ? 128 : 512);
   a.groups = a.heads;
   while (a.groups > 1 && (uint64_t)a.tokens * ((a.groups + 1) / 2) * a.pieces >= kFill && a.heads <= 2 * a.groups) a.groups = (a.groups + 1) / 2;
   const uint64_t items = (uint64_t)a.tokens * a.groups * a.pieces;
@@ -187,9 +180,9 @@ hipError_t launch_rotary(const RotaryView& v, bool bf16, hipStream_t stream) {
   a.scale = v.scale;
   a.inverse = v.inverse;
   a.in_place = v.q == v.qo && v.k == v.ko;
-  const bool wide = v.rot % 16 == 0;
-  if (bf16) return wide ? go<__bf16, 8>(a, v.interleaved, stream) : go<__bf16, 1>(a, v.interleaved, stream);
-  return wide ? go<float, 8>(a, v.interleaved, stream) : go<float, 1>(a, v.interleaved, stream);
+  const bool wide = v.rot % 8 == 0;
+  if (bf16) return wide ? go<__bf16, 4>(a, v.interleaved, stream) : go<__bf16, 1>(a, v.interleaved, stream);
+  return wide ? go<float, 4>(a, v.interleaved, stream) : go<float, 1>(a, v.interleaved, stream);
 }
 
 }  // namespace lh
