@@ -66,7 +66,7 @@ def check_extend(table, lengths, asked, stack, count, page, max_tokens, in_place
 
 # both sides of one workgroup (up to 1024 requests and 2048 rows), waves that are not full
 @pytest.mark.parametrize("batch,width,page,max_tokens", [(1, 1, 1, 1), (1, 4, 16, 64), (3, 5, 16, 40), (63, 7, 3, 300), (64, 9, 16, 64), (65, 9, 16, 200),
-                                                         (256, 4, 24, 2048), (256, 4, 24, 2049), (1024, 3, 5, 2048), (1025, 3, 5, 2048),
+                                                         (256, 4, 24, 2048), (256, 4, 24, 2049), (512, 3, 5, 2048), (513, 3, 5, 2048), (1024, 3, 5, 2048), (1025, 3, 5, 2048),
                                                          (2500, 6, 7, 9001), (300, 40, 64, 70000)])
 @pytest.mark.parametrize("new", ["mixed", "one", "idle", "back"])
 def test_extend(batch, width, page, max_tokens, new):
@@ -152,7 +152,8 @@ def check_rotary(got, x, positions, f, dtype, half, interleaved, inverse=False, 
 
 
 @pytest.mark.parametrize("tokens,heads,kv,dim,rot", [(1, 32, 8, 128, 128), (1, 1, 0, 16, 2), (3, 7, 1, 64, 64), (65, 5, 5, 96, 48), (17, 8, 2, 256, 64),
-                                                     (2, 3, 3, 80, 80), (40, 4, 2, 64, 20), (5, 2, 1, 112, 6), (3001, 8, 2, 64, 32)])
+                                                     (2, 3, 3, 80, 80), (40, 4, 2, 64, 20), (5, 2, 1, 112, 6), (3001, 8, 2, 64, 32),
+                                                     (7, 3, 2, 64, 40), (9, 2, 1, 48, 8), (33001, 6, 1, 64, 64)])      # the last: several heads a thread
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_rotary(tokens, heads, kv, dim, rot, dtype, interleaved):
