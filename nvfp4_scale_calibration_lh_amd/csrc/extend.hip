@@ -14,7 +14,7 @@
 // a write to the stack.
 //
 // Bound by latencies: of a launch, and of a chain of three loads a row (start, table or stack, store).  One token for each of 64
-// sequences 4.8 us; 900000 rows of 1024 sequences, 14 MB written, 18.7 us: the sums 7.4, the rows 9.3.
+// sequences 4.8 us; 900000 rows of 1024 sequences, 14 MB written, 18.4 us: the sums 7.4, the rows 9.3.
 #include "lh_internal.hpp"
 
 #include <algorithm>
@@ -23,7 +23,7 @@ namespace lh {
 namespace {
 
 constexpr int kMaxThreads = 1024;
-constexpr int kRun = 256;                    // rows of one workgroup of the second kernel, one a thread (four a thread: 23 us instead of 18.7)
+constexpr int kRun = 256;                    // rows of one workgroup of the second kernel, one a thread (four a thread: 4 us more for 900000)
 constexpr int kWindow = 256;                 // sequences whose first rows it holds
 
 struct Args {
@@ -254,9 +254,10 @@ __global__ __launch_bounds__(256) void k_extend_rows(const Args a) {
     a.stack[count + i] = given_back(a, p, (int)i);
 }
 
-// One workgroup: a token for each of 64, 512 and 1024 sequences 4.7, 6.6 and 9.6 us, with two kernels 9.8, 11.4 and 12.7.  Where many pages are
-// given back two are faster: a quarter of 256, 512 or 1024 sequences of some 8000 tokens ending at once 16, 24 and 32 us, two 13, 14 and 17.
-bool together(int64_t batch, int64_t rows) { return batch <= kMaxThreads / 2 && rows <= 2 * kMaxThreads; }
+// One workgroup: a token for each of 256 and 512 sequences 6.0 and 6.6 us, with two kernels 7.9 and 9.4; 500 tokens of one sequence 5.4 and 6.1.
+// More rows than that take it several turns: 1000 tokens of one sequence 7.8 us, 6.1 with two; and so do pages that are given back, where two
+// kernels win at any size: a quarter of 200 or 500 sequences of some 8000 tokens ending at once 20 and 25 us, 9.6 and 12 with two.
+bool together(int64_t batch, int64_t rows) { return batch <= 512 && rows <= 512; }
 
 }  // namespace
 
@@ -282,11 +283,10 @@ hipError_t launch_extend(const ExtendView& v, void* work, hipStream_t stream) {
   a.page = (int)v.page;
   a.capacity = (int)v.capacity;
   a.most = (int)(v.width * v.page);
-  if (together(v.batch, v.rows)) {
-    const int threads = (int)std::min<int64_t>(kMaxThreads, (std::max(v.batch, v.rows) + 63) / 64 * 64);
-    return launch_kernel(k_extend, dim3(1), dim3(std::max(threads, 64)), (size_t)(4 * plan_ints(v.batch)), stream, a);
-  }
-  const hipError_t e = launch_kernel(k_extend_sums, dim3(1), dim3(kMaxThreads), 0, stream, a);
+  auto threads = [](int64_t n) { return dim3((unsigned)std::clamp<int64_t>((n + 63) / 64 * 64, 64, kMaxThreads)); };
+  if (together(v.batch, v.rows))
+    return launch_kernel(k_extend, dim3(1), threads(std::max(v.batch, v.rows)), (size_t)(4 * plan_ints(v.batch)), stream, a);
+  const hipError_t e = launch_kernel(k_extend_sums, dim3(1), threads(v.batch), 0, stream, a);
   if (e != hipSuccess) return e;
   return launch_kernel(k_extend_rows, dim3((unsigned)std::max<int64_t>(64, (v.rows + kRun - 1) / kRun)), dim3(256), 0, stream, a);
 }
