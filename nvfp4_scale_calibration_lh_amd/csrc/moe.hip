@@ -110,30 +110,38 @@ __device__ inline void make_ready(const v4u* got, bool in, h8* out, float& facto
 // Rows of k elements made ready for the products once, where each would otherwise be made ready by many workgroups many times:
 // half [piece][row][chunk][128], factor [row][chunk].  Chunks as in k_experts: the last one, if short, is the last 128 elements
 // with 0 for those that the chunk before it has (k >= 128).
+struct Rows {
+  const void* x;
+  const float* x_scale;
+  _Float16* half;
+  float* factor;
+  int64_t rows;
+  int x_scales, k_all;
+};
 template <int X, int P>
-__global__ __launch_bounds__(256) void k_rows(const void* x, const float* x_scale, int x_scales, _Float16* half, float* factor, int64_t rows, int k_all) {
-  const int chunks = (k_all + kChunk - 1) / kChunk;
+__global__ __launch_bounds__(256) void k_rows(const Rows a) {
+  const int chunks = (a.k_all + kChunk - 1) / kChunk;
   const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 16, row = at / chunks;
-  if (row >= rows) return;                    // 16 lanes together
-  const int c = (int)(at - row * chunks), k = min(c * kChunk, k_all - kChunk) + (threadIdx.x & 15) * 8;
-  const int64_t from = row * k_all + k;
+  if (row >= a.rows) return;                  // 16 lanes together
+  const int c = (int)(at - row * chunks), k = min(c * kChunk, a.k_all - kChunk) + (threadIdx.x & 15) * 8;
+  const int64_t from = row * a.k_all + k;
   v4u got[2];
   float f;
   if constexpr (X == kXF32) {
-    got[0] = *(const v4u*)((const float*)x + from), got[1] = *(const v4u*)((const float*)x + from + 4);
+    got[0] = *(const v4u*)((const float*)a.x + from), got[1] = *(const v4u*)((const float*)a.x + from + 4);
   } else if constexpr (X == kXBf16) {
-    got[0] = *(const v4u*)((const __bf16*)x + from);
+    got[0] = *(const v4u*)((const __bf16*)a.x + from);
   } else {
-    const v2u v = *(const v2u*)((const uint8_t*)x + from);
+    const v2u v = *(const v2u*)((const uint8_t*)a.x + from);
     got[0] = v4u{v[0], v[1], 0, 0};
-    f = x_scale[row * x_scales + (x_scales > 1 ? c : 0)];
+    f = a.x_scale[row * a.x_scales + (a.x_scales > 1 ? c : 0)];
   }
   const bool in = k >= c * kChunk;
   h8 out[P];
   make_ready<X, P>(got, in, out, f);
 #pragma unroll
-  for (int p = 0; p < P; ++p) *(v4u*)(half + (p * rows * chunks + at) * kChunk + (threadIdx.x & 15) * 8) = in ? __builtin_bit_cast(v4u, out[p]) : v4u{0, 0, 0, 0};
-  if ((threadIdx.x & 15) == 0) factor[at] = f;
+  for (int p = 0; p < P; ++p) *(v4u*)(a.half + (p * a.rows * chunks + at) * kChunk + (threadIdx.x & 15) * 8) = in ? __builtin_bit_cast(v4u, out[p]) : v4u{0, 0, 0, 0};
+  if ((threadIdx.x & 15) == 0) a.factor[at] = f;
 }
 
 // n / d for n < 2^21, by the reciprocal of d (a quotient is at least 0.5 / d away from the next whole number).
@@ -550,8 +558,8 @@ hipError_t go_rows(const MoeView& v, const Args& a, const Layout& l, hipStream_t
   if (l.many) {                               // experts have many rows each
     const int64_t rows = DOWN ? v.tokens * v.topk : v.tokens, k = DOWN ? v.inner : v.hidden, blocks = (rows * ((k + kChunk - 1) / kChunk) + 15) / 16;
     if (blocks >= int64_t(1) << 24) return hipErrorInvalidConfiguration;
-    k_rows<X, P><<<dim3((unsigned)blocks), dim3(256), 0, stream>>>(DOWN ? a.h : a.x, a.x_scale, a.x_scales, a.half, a.factor, rows, (int)k);
-    const hipError_t e = hipGetLastError();
+    // (its own status: the thread's last error may be an older call's)
+    const hipError_t e = launch_kernel(k_rows<X, P>, dim3((unsigned)blocks), dim3(256), 0, stream, Rows{DOWN ? a.h : a.x, a.x_scale, a.half, a.factor, rows, a.x_scales, (int)k});
     if (e != hipSuccess) return e;
     return go<kXHalf, P, DOWN, P == 1 ? 4 : 2, 4>(v, a, l, stream);
   }
