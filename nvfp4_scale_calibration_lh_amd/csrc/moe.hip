@@ -147,6 +147,14 @@ __global__ __launch_bounds__(256) void k_rows(const Rows a) {
 // n / d for n < 2^21, by the reciprocal of d (a quotient is at least 0.5 / d away from the next whole number).
 __device__ inline int quotient(int n, float reciprocal) { return (int)(((float)n + 0.5f) * reciprocal); }
 
+// LDS accesses of this wave before and after stay in that order, for lanes that read what others have written.  A wave's LDS accesses are carried out in
+// order, so this holds the compiler and costs no wait.
+__device__ inline void wave_turn() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // 1 / (1 + exp(-g)) * g; the power of two from the exact product's two halves.
 __device__ inline float silu(float g) {
   constexpr float kHigh = -1.4426950216293335f, kLow = -1.9259629911e-8f;       // -log2(e)
@@ -405,11 +413,13 @@ __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
         const bool last = ++step == steps;
         if (last) step = 0;
         const Place p = place_of(group + (last && left > 1), step, left > 1);
+        wave_turn();                          // what was in codes has been read
 #pragma unroll
         for (int s = 0; s < kSets; ++s) {
           *(v2u*)&codes[wave][s][i][8 * quarter] = w.code[s];
           load_code(p, s);
         }
+        wave_turn();
         const int c = (now * a.split + ks) * a.each;
         each<U>([&](auto uu) __attribute__((always_inline)) {
           constexpr int u = decltype(uu)::value;
