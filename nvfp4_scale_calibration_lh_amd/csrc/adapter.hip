@@ -208,16 +208,17 @@ __global__ __launch_bounds__(kThreads) void k_adapter_in(const Args a) {
   }
 }
 
-// Workgroups of the second kernel on a compute unit, all resident, as the registers for rk steps of 32 ranks allow.  96 rows over 64 adapters of
-// rank 64: 29.6 us with six; 35 with three, 31.1 with four, 29.9 with five, 29.1 with seven and 35.4 with eight, whose weights spill;
-// 128 rows over four: 17.5, 17.6, 17.9, 18.5 and 20.6 against 17.9.
-template <bool WF32>
-constexpr int resident(int rk) { return rk <= (WF32 ? 1 : 2) ? 6 : (rk <= 2 ? 4 : (rk == 4 ? 3 : 2)); }
+// Workgroups of the second kernel on a compute unit, all resident, as the registers for rk steps of 32 ranks and u's LDS (28 KB for three pieces of
+// rank 64, so five) allow.  96 rows over 64 adapters of rank 64: 29.6 us with six; 35 with three, 31.1 with four, 29.9 with five, 29.1 with seven and
+// 35.4 with eight, whose weights spill; 128 rows over four: 17.5, 17.6, 17.9, 18.5 and 20.6 against 17.9.  With fp32 rows, whose sixth would
+// wait for another to end, 31.9 us with five and 38.5 with six, and 20.4 and 22.5.
+template <bool YF32, bool WF32>
+constexpr int resident(int rk) { return rk <= (WF32 ? 1 : 2) ? (YF32 && !WF32 && rk == 2 ? 5 : 6) : (rk <= 2 ? 4 : (rk == 4 ? 3 : 2)); }
 
 // RK: steps of 32 ranks; P: bf16 pieces of u.  A workgroup makes its adapter's u once and takes several steps of channels, 16 a wave, the
 // weights and the base of the next on their way (32 channels a wave: 1.8 us more for 96 rows over 64 adapters).
 template <bool YF32, bool WF32, int RK>
-__global__ __launch_bounds__(kThreads, resident<WF32>(RK)) void k_adapter_out(const Args a) {
+__global__ __launch_bounds__(kThreads, (resident<YF32, WF32>(RK))) void k_adapter_out(const Args a) {
   constexpr int P = WF32 ? 1 : (YF32 ? 3 : 2);
   constexpr int kWide = 32 * RK + 8;         // a row of u in LDS, so that 16 rows lie in different banks
   constexpr int kRows = RK <= 2 ? 64 : (RK == 4 ? 32 : 16);          // rows whose u is held
@@ -226,6 +227,7 @@ __global__ __launch_bounds__(kThreads, resident<WF32>(RK)) void k_adapter_out(co
   using four_t = T __attribute__((ext_vector_type(4)));
   __shared__ int rows[kTokens];
   __shared__ __attribute__((aligned(16))) U us[P][kRows][kWide];
+  static_assert(resident<YF32, WF32>(RK) * (sizeof(us) + sizeof(rows)) <= 160 * 1024, "LDS of the workgroups of a compute unit");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, quarter = lane >> 4;
   const T* base = (const T*)a.base;
@@ -399,7 +401,7 @@ template <bool YF32, bool WF32, int RK>
 hipError_t go_out(Args a, const Layout& l, hipStream_t stream) {
   const int64_t steps = (a.cout + 16 * kWaves - 1) / (16 * kWaves), chunks = std::min<int64_t>(l.chunks, 64);
   if (l.slots * chunks * steps >= int64_t(1) << 31) return hipErrorInvalidConfiguration;
-  a.groups = (int)std::min<int64_t>(l.slots * chunks * steps, 256 * resident<WF32>(RK));
+  a.groups = (int)std::min<int64_t>(l.slots * chunks * steps, 256 * resident<YF32, WF32>(RK));
   const int64_t n = a.groups + (a.in_place ? 0 : (a.cout + kCopy - 1) / kCopy * ((std::min<int64_t>(chunks * kTokens, a.rows) + kWaves - 1) / kWaves));
   if (n >= int64_t(1) << 24) return hipErrorInvalidConfiguration;
   return launch_kernel(k_adapter_out<YF32, WF32, RK>, dim3((unsigned)n, (unsigned)((l.chunks + 63) / 64)), dim3(kThreads), 0, stream, a);
