@@ -491,7 +491,7 @@ lh_status lh_cache_extend(int32_t* block_table, int64_t batch, int64_t max_pages
                           int32_t* positions, int32_t* sequence, int32_t* offsets, int32_t* new_lengths,
                           int32_t* new_count, void* workspace, int64_t workspace_bytes, void* stream);
 
-/* Bytes of workspace that lh_cache_extend needs for these sizes (a host computation; 0 for ones that it refuses). */
+/* Bytes of workspace that lh_cache_extend needs for these sizes (a host computation; 0 for ones outside the ranges above). */
 int64_t lh_cache_extend_workspace(int64_t batch, int64_t max_tokens);
 
 /*
@@ -587,7 +587,7 @@ lh_status lh_moe(const void* X, lh_dtype x_dtype, const float* x_scale, int64_t 
                  const float* down_amax, float scale_norm, void* Y, void* workspace, int64_t workspace_bytes,
                  void* stream);
 
-/* Bytes of workspace that lh_moe needs for these sizes (a host computation; 0 for ones that it refuses). */
+/* Bytes of workspace that lh_moe needs for these sizes (a host computation; 0 for types and sizes outside the ranges above). */
 int64_t lh_moe_workspace(lh_dtype x_dtype, int64_t tokens, int64_t hidden, int64_t inner, int64_t n_experts,
                          int64_t topk);
 
@@ -614,7 +614,7 @@ lh_status lh_adapter(const void* X, lh_dtype x_dtype, const float* x_scale, int6
                      lh_dtype w_dtype, const int32_t* index, const float* scaling, const int32_t* ranks,
                      const void* base, void* Y, void* workspace, int64_t workspace_bytes, void* stream);
 
-/* Bytes of workspace that lh_adapter needs for these sizes (a host computation; 0 for ones that it refuses). */
+/* Bytes of workspace that lh_adapter needs for these sizes (a host computation; 0 for ones outside the ranges above). */
 int64_t lh_adapter_workspace(int64_t rows, int64_t cin, int64_t n_adapters, int64_t rank);
 
 /* Message of the last error on the calling thread ("" if none); valid until its next call. */

@@ -814,7 +814,9 @@ def _rows_type(X: torch.Tensor, x_scale: Optional[torch.Tensor], x_group: int) -
 
 def lh_moe_workspace(dtype: torch.dtype, tokens: int, hidden: int, inner: int, n_experts: int, topk: int) -> int:
     """Bytes of workspace that lh_moe needs for rows of dtype and these sizes."""
-    code = {torch.float32: LH_DTYPE_F32, torch.bfloat16: LH_DTYPE_BF16, torch.float8_e4m3fn: LH_DTYPE_E4M3}[dtype]
+    code = {torch.float32: LH_DTYPE_F32, torch.bfloat16: LH_DTYPE_BF16, torch.float8_e4m3fn: LH_DTYPE_E4M3}.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype} (bfloat16, float32 or float8_e4m3fn)")
     return int(lib().lh_moe_workspace(code, tokens, hidden, inner, n_experts, topk))
 
 

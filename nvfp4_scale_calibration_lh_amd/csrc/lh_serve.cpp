@@ -179,6 +179,10 @@ lh_status lh_route(const void* logits, lh_dtype dtype, int64_t tokens, int64_t n
 }
 
 int64_t lh_moe_workspace(lh_dtype x_dtype, int64_t tokens, int64_t hidden, int64_t inner, int64_t n_experts, int64_t topk) {
+  if (x_dtype != LH_DTYPE_E4M3 && !dtype_ok(x_dtype)) {
+    (void)fail(LH_ERR_UNSUPPORTED, "unknown dtype %d", (int)x_dtype);
+    return 0;
+  }
   if (check_moe(tokens, hidden, inner, n_experts, topk) != LH_OK) return 0;
   (void)ok();
   lh::MoeView v{};
