@@ -3,7 +3,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_serve import DEV, check_extend, choices, layer_rows, matrices, note, on_gpu, requests
+from oracle import serve
+from test_gpu_serve import DEV, check_extend, check_moe, choices, layer_rows, matrices, note, on_gpu, requests
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +76,56 @@ def test_extend_numbers_out_of_range_in_either_kernel(batch, max_tokens, one):
         check_extend(table, lengths, asked, stack, np.array([c]), 8, max_tokens)
     note(f"extend {batch} requests, {max_tokens} rows, with a short stack")
     check_extend(table, lengths, asked, stack[:4].copy(), np.array([3]), 8, max_tokens)
+
+
+# ------------------------------------------------------------------------------------------ the expert layer
+def moe64(x, ids, weights, gate_up, down, norm=448.0):
+    """oracle.serve.moe in 64 bits on the device, an expert at a time."""
+    grid = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64, device=DEV)
+    grid = torch.cat((grid, -grid))
+
+    def matrix(m, e):
+        code, fp4 = (torch.from_numpy(t[e]).to(DEV) for t in m[:2])
+        nib = torch.stack((fp4 & 15, fp4 >> 4), -1).flatten(-2).long()
+        return grid[nib] * code.view(torch.float8_e4m3fn).double().repeat_interleave(16, -1) * float(m[2][e] / np.float32(6.0 * norm))
+
+    x = torch.from_numpy(x).to(DEV)
+    y, terms = torch.zeros_like(x), torch.zeros_like(x)
+    for e in np.unique(ids[(ids >= 0) & (ids < len(gate_up[2]))]):
+        t, j = (torch.from_numpy(a).to(DEV) for a in np.nonzero(ids == e))
+        wg, wd, v = matrix(gate_up, e), matrix(down, e), x[t]
+        w = torch.from_numpy(np.asarray(weights, np.float64)).to(DEV)[t, j][:, None]
+        gate, up = (v @ wg.t()).chunk(2, -1)
+        ag, au = (v.abs() @ wg.abs().t()).chunk(2, -1)
+        s = gate / (1 + torch.exp(-gate))
+        h = s * up
+        y.index_add_(0, t, w * (h @ wd.t()))
+        terms.index_add_(0, t, w.abs() * ((h.abs() + 1.1 * ag * up.abs() + s.abs() * au) @ wd.abs().t()))
+    return y.cpu().numpy(), terms.cpu().numpy()
+
+
+def test_moe64_is_the_oracle():
+    note("the expert layer in 64 bits on the device")
+    gate_up, down = matrices(9, 128, 256, 5), matrices(9, 256, 64, 6)
+    x = np.random.default_rng(7).standard_normal((30, 256))
+    ids, w = choices(30, 9, 3, 8)
+    ids[3], ids[4, 1], ids[5] = -1, 9, 4
+    for got, want in zip(moe64(x, ids, w, gate_up, down, 256.0), serve.moe(x, ids, w.astype(np.float64), gate_up, down, 256.0)):
+        assert np.all(np.abs(got - want) <= 1e-12 * np.abs(want).max(1, keepdims=True))
+
+
+# The first expert has every token, so more rows than one pass takes.  Rows as they are, held in several panels of LDS (of the first product,
+# of the second) that several groups of channels go through, each wave with all of k: over half the chip's wave slots have channels of
+# their own.  Few tokens, likewise and with k shared by eight waves.  Rows made ready first, several panels, k not shared and shared.
+@pytest.mark.parametrize("tokens,experts,topk,hidden,inner", [(40, 104, 10, 1040, 640), (40, 104, 10, 640, 1296), (32, 130, 10, 2560, 640), (16, 16, 3, 2576, 784),
+                                                              (16, 5, 2, 4112, 272), (70, 12, 2, 2064, 1040), (70, 12, 2, 1040, 5504)])
+@pytest.mark.parametrize("x,group", [("bf16", 0), ("f32", 0), ("e4m3", 0), ("e4m3", 128)])
+def test_moe_of_many_channels(tokens, experts, topk, hidden, inner, x, group, monkeypatch):
+    note(f"moe {tokens} tokens top {topk} of {experts}, {hidden} x {inner}, {x} group {group}")
+    monkeypatch.setattr(serve, "moe", moe64)
+    gate_up, down = matrices(experts, 2 * inner, hidden, 1), matrices(experts, hidden, inner, 2)
+    xd, scale, xv = layer_rows(tokens, hidden, x, group, 3)
+    ids, w = choices(tokens, experts - 1, topk, 4)
+    ids += 1
+    ids[:, topk // 2] = 0
+    check_moe(xd, scale, xv, x, group, ids, w, gate_up, down)
