@@ -155,12 +155,14 @@ __device__ inline void wave_turn() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
 }
 
-// 1 / (1 + exp(-g)) * g; the power of two from the exact product's two halves.
-__device__ inline float silu(float g) {
+// g / (1 + exp(-g)) * u; the power of two from the exact product's two halves.  Where exp(-g) nears the end of fp32, 96 powers of two of it, beside
+// which the 1 is nothing, are taken off the product instead: g from -76 down to -155.
+__device__ inline float silu_times(float g, float u) {
   constexpr float kHigh = -1.4426950216293335f, kLow = -1.9259629911e-8f;       // -log2(e)
   const float t = g * kHigh, rest = fmaf(g, kHigh, -t) + g * kLow;
-  const float e = __builtin_amdgcn_exp2f(t) * (fabsf(t) < 1e30f ? 1.0f + rest * 0.6931471824645996f : 1.0f);     // exp(-g)
-  return g / (1.0f + e);
+  const bool far = t > 110.0f;
+  const float e = __builtin_amdgcn_exp2f(far ? t - 96.0f : t) * (fabsf(t) < 1e30f ? 1.0f + rest * 0.6931471824645996f : 1.0f);     // exp(-g)
+  return __builtin_ldexpf(g / (far ? e : 1.0f + e) * u, far ? -96 : 0);
 }
 
 // X: type of the rows, in P pieces.  DOWN: the second product, whose rows are h.  MT: 16-row tiles taken at a time at most.  U: chunks of k
@@ -452,7 +454,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_experts(const Args a) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const float up = __shfl_xor(v[r], 32, 64);
-              v[r] = silu(v[r]) * up;
+              v[r] = silu_times(v[r], up);
             }
             if (own && row < live && quarter < 2) *(v4f*)(a.h + (int64_t)rows[r0 + row] * a.inner + 8 * tile + 4 * quarter) = v;
           }

@@ -129,3 +129,43 @@ def test_moe_of_many_channels(tokens, experts, topk, hidden, inner, x, group, mo
     ids += 1
     ids[:, topk // 2] = 0
     check_moe(xd, scale, xv, x, group, ids, w, gate_up, down)
+
+
+@pytest.mark.parametrize("x", ["bf16", "f32", "e4m3"])
+def test_moe_gates_past_the_range_of_exp(x):
+    """Gates of -87 to -140, where exp(-g) ends fp32 at 88.7, beside ups that make their products ordinary numbers.
+    A gate has one term, so three roundings (the factor, the weights' two scales), which exp passes on times the gate; exp and the division
+    take 8 more.  h is held to 2^-11 or 2^-23 of itself, an up has three roundings, the sum of 128 terms one a term (three times for fp32)."""
+    note(f"moe with gates past the range of exp, {x}")
+    hidden, inner = 256, 128
+    r = np.random.default_rng(1)
+    code, fp4, amax = matrices(1, 2 * inner, hidden, 2)
+    fp4[:] = 0
+    fp4[0, :inner, 0], fp4[0, inner:, hidden // 4] = 2, 2                   # 1 at element 0 of the gates, at element 128 of the ups
+    code[0, :inner] = np.array([0x53, 0x54, 0x55], np.uint8)[r.integers(0, 3, inner)][:, None]         # scales of 11, 12 and 13
+    amax[:] = 2688.0                                                        # a global scale of 1
+    down = matrices(1, hidden, inner, 3)
+    v = np.zeros((2, hidden))
+    v[:, 0], v[:, 128] = [-7.92, -10.8], [1e25, -3e37]
+    v[:, 1:128] = r.standard_normal((2, 127))                               # (their weights are 0)
+    if x == "e4m3":
+        s = np.array([[7.92 / 448, 1e25 / 448], [10.8 / 448, 3e37 / 448]], np.float32)
+        q = torch.from_numpy(v / np.repeat(s.astype(np.float64), 128, 1)).float().clamp(-448, 448).to(torch.float8_e4m3fn)
+        xd, scale, xv = q.to(DEV), torch.from_numpy(s).to(DEV), q.double().numpy() * np.repeat(s.astype(np.float64), 128, 1)
+    else:
+        t = torch.from_numpy(v).to(torch.bfloat16 if x == "bf16" else torch.float32)
+        xd, scale, xv = t.to(DEV), None, t.double().numpy()
+    ids, w = np.zeros((2, 1), np.int32), np.ones((2, 1), np.float32)
+    y = lh.lh_moe(xd, torch.from_numpy(ids).to(DEV), torch.from_numpy(w).to(DEV), on_gpu((code, fp4, amax)), on_gpu(down), x_scale=scale,
+                  x_group=128 if x == "e4m3" else 0).double().cpu().numpy()
+    want, _ = serve.moe(xv, ids, w, (code, fp4, amax), down)
+    wg, wd = (serve.decode.weights(m[0][0], m[1][0], m[2][0], 448.0) for m in ((code, fp4, amax), down))
+    gate, up = np.split(xv @ wg.T, 2, 1)
+    assert np.all((gate > -150) & (gate < -80)) and len(np.unique(gate)) >= 6
+    terms = np.abs(serve.silu(gate) * up) @ np.abs(wd).T
+    u = 2.0 ** -24
+    rel = (150 * 3 + 8 + 3 + (3 if x == "f32" else 1) * (inner + 8)) * u + (2.0 ** -23 if x == "f32" else 2.0 ** -11)
+    bound = rel * terms
+    bound += (u if x == "f32" else 2.0 ** -8) * (np.abs(want) + bound)
+    assert np.all(np.abs(y - want) <= bound), float((np.abs(y - want) / bound).max())
+    assert np.abs(want).min() > 0
