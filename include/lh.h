@@ -530,7 +530,7 @@ lh_status lh_rotary_frequencies(double theta, int64_t rot_dim, lh_rotary_scaling
  * Q: element (t, h, i) at t * q_stride + h * head_dim + i, t < tokens; K and the outputs in the same way, so each may be part of
  * wider rows.  Q_out may be Q and K_out K (with equal strides), for a turn in place; otherwise they overlap no input.
  * All of dtype, 16-byte aligned, strides multiples of 16 bytes.  n_k_heads may be 0 (K and K_out NULL).
- * positions [tokens] int32, frequencies [rot_dim / 2] fp32 (see lh_rotary_frequencies), both device.
+ * positions [tokens] int32, frequencies [rot_dim / 2] fp32 (see lh_rotary_frequencies; magnitudes up to 2^16), both device.
  * The angle is the exact product, reduced in 64-bit arithmetic (positions up to 2^31-1 lose nothing); sine and cosine
  * are fp32 to within 2^-23, products and sums fp32, rounded once to dtype.
  * Errors: UNSUPPORTED for an unknown dtype; INVALID_ARGUMENT for tokens outside [0, 2^31-1], head_dim < 1, over 65536 or

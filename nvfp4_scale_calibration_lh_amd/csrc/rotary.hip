@@ -7,7 +7,8 @@
 // 4.8 TB/s, as a copy); 3001 tokens of 10 heads of 256 fp32, 64 turned, 12.5 us (61 MB, as a copy).
 //
 // The angle: position * frequency is a product of 31 and 24 bits; it is taken in turns, as a sum of two 64-bit
-// numbers, and reduced to an eighth of a turn there, so that positions up to 2^31 lose nothing.  What is left
+// numbers, and reduced to an eighth of a turn there, so that positions up to 2^31 lose nothing (at frequencies up to 2^16: the second number
+// stays under 2^-7 turns and their sum right to 2^-60; over 2^20 it could pass that eighth).  What is left
 // goes through the power series of sine and cosine in fp32 (|x| <= pi/4: the terms left out are under
 // 7e-12 and 2e-10).  Results are fp32, rounded once to the output's type.
 #include "lh_internal.hpp"
@@ -51,7 +52,7 @@ __device__ inline void turn(int position, float frequency, float& c, float& s) {
   cs = fmaf(cs, y, 1.0f / 24.0f);
   cs = fmaf(cs, y, -0.5f);
   cs = fmaf(cs, y, 1.0f);
-  // quarter turns: 4 t is under 2^34 in magnitude, its two lowest bits are those of the number mod 4
+  // quarter turns: 4 t is under 2^47 in magnitude, its two lowest bits are those of the number mod 4
   const int turns = (int)(quarter - 4.0 * __builtin_floor(quarter * 0.25));
   const bool swap = turns & 1;
   const float a = swap ? sn : cs, b = swap ? cs : sn;

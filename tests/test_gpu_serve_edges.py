@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from oracle import serve
-from test_gpu_serve import DEV, check_extend, check_moe, choices, layer_rows, matrices, note, on_gpu, requests
+from test_gpu_serve import DEV, check_extend, check_moe, choices, dev, heads_of, layer_rows, matrices, note, on_gpu, requests
 
 pytestmark = pytest.mark.gpu
 
@@ -76,6 +76,34 @@ def test_extend_numbers_out_of_range_in_either_kernel(batch, max_tokens, one):
         check_extend(table, lengths, asked, stack, np.array([c]), 8, max_tokens)
     note(f"extend {batch} requests, {max_tokens} rows, with a short stack")
     check_extend(table, lengths, asked, stack[:4].copy(), np.array([3]), 8, max_tokens)
+
+
+# --------------------------------------------------------------------------------------- rotary positions
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotary_fast_angles(interleaved):
+    """Frequencies up to 2^16, the largest documented, at the largest positions.  The angle is taken in turns with whole numbers; then as for any
+    position: sine and cosine to 2^-23, one rounding with the scale, one of a product, of the sum and of the output."""
+    note(f"rotary fast angles, interleaved {interleaved}")
+    f = np.array([2 ** 16, 65535.99, 40961.37, -31415.926, 1.0 / 3, 7.25, 2 ** 16 - 1, 1e-3], np.float32)
+    positions = np.array([2 ** 31 - 1, 2 ** 31 - 2, 2 ** 30 + 12345, 1999999973, 1, 0, 65537])
+    pi = 31415926535897932384626433832795028841971693993751058209749445923        # times 10^64
+    turns = np.array([[int(p) * int(float(v) * 2 ** 60) for v in f] for p in positions], object)       # angles times 2^60; whole numbers
+    whole = 2 * pi * 2 ** 60
+    left = [[t * 10 ** 64 % whole for t in row] for row in turns]
+    w = np.array([[float((v if 2 * v < whole else v - whole) // 2 ** 60) / 1e64 for v in row] for row in left])
+    x, xv = heads_of(len(positions), 3, 32, "f32", 5)
+    y, _ = lh.lh_rotary(x, None, dev(positions), torch.from_numpy(f).to(DEV), interleaved=interleaved, scale=1.25)
+    at = (np.arange(8) * 2, np.arange(8) * 2 + 1) if interleaved else (np.arange(8), np.arange(8) + 8)
+    a, b = xv[..., at[0]], xv[..., at[1]]
+    c, s = 1.25 * np.cos(w)[:, None], 1.25 * np.sin(w)[:, None]
+    want = xv.copy()
+    want[..., at[0]], want[..., at[1]] = a * c - b * s, a * s + b * c
+    bound = np.zeros_like(want)
+    u = 2.0 ** -24
+    bound[..., at[0]] = bound[..., at[1]] = 1.25 * (np.abs(a) + np.abs(b)) * (2 + 1 + 1 + 1) * u
+    bound += u * (np.abs(want) + bound) * (bound > 0)
+    err = np.abs(y.double().cpu().numpy() - want)
+    assert np.all(err <= bound), float((err - bound).max())
 
 
 # ------------------------------------------------------------------------------------------ the expert layer
