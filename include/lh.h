@@ -569,7 +569,8 @@ lh_status lh_route(const void* logits, lh_dtype dtype, int64_t tokens, int64_t n
  * X [tokens, hidden], x_scale and x_group as in lh_matvec; Y [tokens, hidden] F32 for F32 rows, BF16 otherwise.
  * Weights enter exactly, and so do E4M3 rows and their scales.  Of each 128 elements of other rows with the largest magnitude m, BF16
  * ones enter exactly from 2^-31 m on and to within 2^-39 m below, F32 ones to within 2^-23 of themselves and 2^-39 m.  What comes between the two
- * products is held to 2^-11 of itself (F32 rows: 2^-23) and 2^-39 of the largest of its 128.  Sums are fp32, in a fixed order; the
+ * products is held to 2^-11 of itself (F32 rows: 2^-23) and 2^-39 of the largest of its 128; where exp(-g) is over 2^224 (g under -155) its silu
+ * counts as 0.  Sums are fp32, in a fixed order, of products that the matrix's global scale amax / (6 * scale_norm) multiplies afterwards; the
  * routing weights multiply the rows of the second product, and Y is rounded once.  Infinities and NaN in a row give what the formula
  * gives in that row's Y and change no other row.
  * Any number of tokens works; the weights of an expert are read again for every 64 tokens, and among those for every 32 rows of it (16
@@ -600,7 +601,8 @@ int64_t lh_moe_workspace(lh_dtype x_dtype, int64_t tokens, int64_t hidden, int64
  * X [rows, cin], x_scale and x_group as in lh_matvec; base and Y [rows, cout], F32 for F32 rows, BF16 otherwise; Y may be base.
  * Products of BF16 weights are exact (fp32 elements as in lh_matvec), those of F32 weights fp32 (E4M3 elements are then multiplied by
  * their scale first); A_a x_t is held to 2^-16 of itself with BF16 weights and Y, otherwise to 2^-24; sums are fp32, in a
- * fixed order, and Y is rounded once.  Infinities and NaN in a row change no other row.
+ * fixed order, and Y is rounded once.  Infinities and NaN in a row change no other row.  (Infinite weights may give NaN where the formula gives
+ * an infinity: they meet rows and A_a x_t in pieces, some of them 0.)
  * The weights of an adapter are read again for every 64 rows, and among those A for every 16 rows of it, and B for every 32 where rank
  * is over 64 and every 16 where it is over 128.
  * workspace: device memory of at least lh_adapter_workspace bytes (16-byte aligned) that no other call uses until this one has run.

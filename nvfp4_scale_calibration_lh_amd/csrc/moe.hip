@@ -3,7 +3,7 @@
 //
 // Bound by reading the weights of every expert that is hit once (0.5625 bytes each).  Ten experts of 1280x2560 and 2560x640 for one token 22 us
 // (28 MB: three launches, each with its cold instructions, and the tail of the last weights); 32 tokens that hit 125 of 512 such experts 107 us (346 MB at 3.3 TB/s);
-// 61 tokens over eight experts of 24576x4096 and 4096x12288 236 us (680 MB at 2.9 TB/s; 122 rows, whose products and staging
+// 61 tokens over eight experts of 24576x4096 and 4096x12288 237 us (680 MB at 2.9 TB/s; 122 rows, whose products and staging
 // share the wave slots with the loads).  Three kernels:
 //   gate and up  the channels of all experts that (up to 64) tokens hit, in tiles, are shared out evenly over as many workgroups as
 //                are resident; each finds the experts of its share and their rows from the ids by itself.  A wave has 8 gate rows
@@ -527,7 +527,7 @@ Layout layout(const MoeView& v) {
   l.plan = up(l.slots * l.chunks * kPlan * 4);
   l.h = up(v.tokens * v.topk * v.inner * 4);
   l.part = v.tokens * v.topk * v.hidden * 4;
-  // From four rows an expert on: eight experts of 4096x12288 with two for each of 61 tokens 236 us, 280 without; 64 of 2560x1280 with eight for
+  // From four rows an expert on: eight experts of 4096x12288 with two for each of 61 tokens 237 us, 280 without; 64 of 2560x1280 with eight for
   // each of 40 tokens 125 us, 138 without; with eight for each of 20 87 us, 84 without, and two of the eight wide ones for 17 158 and 157.
   l.many = v.tokens > 16 && v.tokens * v.topk > 4 * v.experts && v.hidden >= kChunk && v.inner >= kChunk;
   if (l.many) {
@@ -546,8 +546,9 @@ hipError_t go(const MoeView& v, Args a, const Layout& l, hipStream_t stream) {
   // rows whose chunks of a step LDS holds
   auto fits = [&](int64_t turn, bool shared) { return (lds - (shared ? kWaves * 1024 : 0)) / (P * (turn * kChunk * 2 + 16) + 4 * turn); };
   // Waves that share k: until some 1500 have work, or all that are resident where each would still take 6000 elements of k.  One token of
-  // ten experts of 1280x2560 and 2560x640 22.1 us, 23.3 with 2048 or 3000 waves, 24.9 with 4096; eight of 4096x12288 with 61 tokens 236 with
-  // all resident, 246 without.
+  // ten experts of 1280x2560 and 2560x640 22.2 us, 23.3 with 2048 or 3000 waves, 24.9 with 4096.  Eight experts, all resident and not: of
+  // 4096x12288 with 61 tokens 237 and 247 us, with 20 161 and 166, with 12 146 and 149, 40 of fp32 261 and 274; of 4096x6144, 2048x24576 and
+  // 12288x2048 with 61 141 and 145, 293 and 303, 148 and 157.
   auto more = [&](int64_t waves) { return waves < 1536 || (waves < kResident * kWaves && chunks / a.split >= 48); };
   a.split = 1;
   while (a.split < kWaves && 2 * a.split <= chunks && more(l.slots * tiles * a.split) && fits(2 * a.split, true) >= most) a.split *= 2;

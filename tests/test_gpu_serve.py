@@ -64,7 +64,7 @@ def check_extend(table, lengths, asked, stack, count, page, max_tokens, in_place
     return got
 
 
-# both sides of one workgroup (up to 1024 requests and 2048 rows), waves that are not full
+# one workgroup and two kernels (up to 512 requests and rows, and over), waves that are not full
 @pytest.mark.parametrize("batch,width,page,max_tokens", [(1, 1, 1, 1), (1, 4, 16, 64), (3, 5, 16, 40), (63, 7, 3, 300), (64, 9, 16, 64), (65, 9, 16, 200),
                                                          (256, 4, 24, 2048), (256, 4, 24, 2049), (512, 3, 5, 2048), (513, 3, 5, 2048), (1024, 3, 5, 2048), (1025, 3, 5, 2048),
                                                          (2500, 6, 7, 9001), (300, 40, 64, 70000)])
@@ -346,7 +346,7 @@ def choices(tokens, experts, topk, seed):
     return ids, w / w.sum(1, keepdims=True)
 
 
-# whole and short chunks of 128, less than a chunk, several panels of LDS, shares of k and none, one tile of rows and more
+# whole and short chunks of 128, less than a chunk, several panels of LDS where rows are made ready first, shares of k, one tile of rows and more
 @pytest.mark.parametrize("tokens,experts,topk,hidden,inner", [(1, 1, 1, 16, 16), (1, 4, 2, 128, 64), (2, 8, 3, 144, 80), (5, 16, 4, 272, 144), (17, 3, 2, 256, 128),
                                                               (64, 2, 1, 384, 48), (65, 5, 2, 640, 272), (33, 40, 10, 512, 32), (130, 6, 3, 112, 208),
                                                               (3, 7, 2, 2560, 640), (40, 2, 2, 2064, 1040), (1, 3, 3, 5136, 96), (20, 300, 6, 64, 16)])
